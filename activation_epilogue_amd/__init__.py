@@ -22,6 +22,12 @@ Entry points (same names as the C ABI, without the ``fl_`` prefix):
   bias_add(X, bias)                       # unfused step 2: X += bias (in place)
   activation(X, Y=None, out=None, act=)   # unfused step 3: out = act(X[, Y])
   tile_grid(M, N, K, dtype, **options), tile_of_program(...), version()
+
+Routed experts (C ABI in ``include/fused_moe.h``, binding in ``moe.py``):
+  moe_route, moe_route_bwd                # k experts of each token and their weights; the logits' gradient
+  moe_plan                                # the choices sorted by expert
+  moe_gather, moe_combine, moe_combine_bwd  # rows into expert order and back
+  grouped_linear, grouped_linear_bwd, grouped_weight_grad  # the fused linear layer of every expert
 """
 from __future__ import annotations
 
@@ -415,3 +421,18 @@ def tile_of_program(program, grid, tiles_m, tiles_n, group_m, xcd_remap):
 
 def version():
     return load_library().fl_version()
+
+
+# the routed-experts operators need torch at import; loaded on first use, so
+# that importing the package stays as light as it was
+_MOE_NAMES = ("Plan", "moe_route", "moe_route_bwd", "moe_plan", "moe_plan_workspace_bytes", "moe_gather", "moe_combine",
+              "moe_combine_bwd", "grouped_linear", "grouped_linear_bwd", "grouped_weight_grad",
+              "grouped_workspace_bytes")
+
+
+def __getattr__(name):
+    if name in _MOE_NAMES:
+        from . import moe
+        globals().update({n: getattr(moe, n) for n in _MOE_NAMES})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,9 +1,11 @@
 """Build libfused_linear.so for gfx950 with hipcc, in-tree.
 
-Ten translation units compiled in parallel: the host/ABI unit (with the
+Fourteen translation units compiled in parallel: the host/ABI unit (with the
 elementwise kernels), one unit of fused GEMM kernels per dtype, one of
 quantized-output kernels per 16-bit dtype, one of FP8-input kernels per
-16-bit output dtype and one of backward-epilogue kernels per 16-bit dtype.
+16-bit output dtype and one of backward-epilogue kernels per 16-bit dtype;
+and, for the routed experts, the host/ABI unit (with the router, plan and
+row-movement kernels) and one unit of the experts' products per dtype.
 Every device compile carries -Xclang -target-feature -Xclang -packed-fp32-ops so
 that no packed fp32 instructions are generated.
 """
@@ -37,6 +39,10 @@ UNITS = [
     ("fl_fp8_inst.hip", ["-DFL_INST_DTYPE=2"]),
     ("fl_bwd_inst.hip", ["-DFL_INST_DTYPE=1"]),
     ("fl_bwd_inst.hip", ["-DFL_INST_DTYPE=2"]),
+    ("fl_moe.hip", []),
+    ("fl_grouped_inst.hip", ["-DFL_INST_DTYPE=0"]),
+    ("fl_grouped_inst.hip", ["-DFL_INST_DTYPE=1"]),
+    ("fl_grouped_inst.hip", ["-DFL_INST_DTYPE=2"]),
 ]
 
 
