@@ -31,6 +31,8 @@ struct GroupedArgs {
     int S, N, K, E;
     int dw_f32;              // gradient: dW in fp32 (else in the dtype)
     int tiles_n;
+    int group;               // row tiles per band of the tile order
+    int max_tiles;           // limit on the tiles found from the offsets
 };
 
 // Expert e's rows, limited to [0, S] whatever the array holds.
@@ -45,6 +47,20 @@ struct RunTile {
     int m;       // tile within the run
     int total;   // row tiles of all experts
 };
+
+// Row tiles of all experts: the runs cut into tiles of bm rows (each run from
+// its own start).
+__device__ __forceinline__ int count_run_tiles(const GroupedArgs &a, int bm) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int e = lane; e < a.E; e += 64) {
+        const int lo = run_bound(a, e), hi = run_bound(a, e + 1);
+        n += hi > lo ? (hi - lo + bm - 1) / bm : 0;
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o);
+    return __builtin_amdgcn_readfirstlane(n);
+}
 
 // Row tile `tile` of the experts' runs cut into tiles of bm rows (each run
 // from its own start): every wave scans the runs 64 at a time.
@@ -76,28 +92,26 @@ __device__ __forceinline__ RunTile find_run_tile(const GroupedArgs &a, int bm, i
     return t;
 }
 
-// ------------------------------------------------------- staged by elements
+// ------------------------------------------------------------- fp32 products
 
-// The kernel for every dtype, size and alignment: 64x64 tiles, 4 waves of one
-// 32x32 block each, K stages of 32 values loaded by elements into LDS.
-template <int DT, int FORM, int ACT>
-struct GroupedPlain {
-    using io = Io<DT>;
-    using raw = typename io::raw;
+// 64x64 tiles, 4 waves of one 32x32 block each (v_mfma_f32_32x32x2_f32), K
+// stages of 32 values loaded by elements into LDS.
+template <int FORM, int ACT>
+struct GroupedF32 {
     static constexpr int BM = 64, BN = 64, BK = 32;
-    static constexpr int ROW = BK + 16 / io::size;  // padded LDS row
+    static constexpr int ROW = BK + 4;  // padded LDS row
     static constexpr int THREADS = 256;
 
-    __device__ static void run(const GroupedArgs &a, raw *As, raw *Bs) {
+    __device__ static void run(const GroupedArgs &a, float *As, float *Bs) {
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
         const int wm = wave >> 1, wn = wave & 1;
-        const raw *A = static_cast<const raw *>(a.A);
-        const raw *B = static_cast<const raw *>(a.B);
+        const float *A = static_cast<const float *>(a.A);
+        const float *B = static_cast<const float *>(a.B);
         int e, lo, hi, m0;  // m0: first row (of the product) of the tile; its rows end at mend
         const int n0 = (int)(blockIdx.x % a.tiles_n) * BN;
         int mend, depth;
         if constexpr (FORM == kFormGrad) {
-            const int per = a.K ? (a.K + BM - 1) / BM : 1;  // (no columns of A: dbias alone)
+            const int per = (a.K + BM - 1) / BM;
             const int q = blockIdx.x / a.tiles_n;
             e = q / per;
             lo = run_bound(a, e);
@@ -118,14 +132,13 @@ struct GroupedPlain {
         f32x16_t acc;
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-        float dsum = 0.0f;
         for (int k0 = 0; k0 < depth; k0 += BK) {
 #pragma unroll
             for (int i = 0; i < BM * BK / THREADS; ++i) {
                 const int q = tid + i * THREADS;
                 // consecutive threads along the operand's contiguous dimension
                 const int r = FORM == kFormGrad ? q % BM : q / BK, k = FORM == kFormGrad ? q / BM : q % BK;
-                raw v = raw(0);
+                float v = 0.0f;
                 if (k0 + k < depth && m0 + r < mend) {
                     if constexpr (FORM == kFormGrad) {
                         v = A[(int64_t)(lo + k0 + k) * a.K + m0 + r];
@@ -140,7 +153,7 @@ struct GroupedPlain {
             for (int i = 0; i < BN * BK / THREADS; ++i) {
                 const int q = tid + i * THREADS;
                 const int n = FORM == kFormBwd ? q / BK : q % BN, k = FORM == kFormBwd ? q % BK : q / BN;
-                raw v = raw(0);
+                float v = 0.0f;
                 if (k0 + k < depth && n0 + n < a.N) {
                     if constexpr (FORM == kFormFwd)
                         v = B[((int64_t)e * a.K + k0 + k) * a.N + n0 + n];
@@ -153,32 +166,12 @@ struct GroupedPlain {
             }
             __syncthreads();
             const int lr = lane & 31, lg = lane >> 5;
-            if constexpr (DT == FL_F32) {
 #pragma unroll
-                for (int k = 0; k < BK; k += 2)
-                    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(Bs[(wn * 32 + lr) * ROW + k + lg],
-                                                               As[(wm * 32 + lr) * ROW + k + lg], acc, 0, 0, 0);
-            } else {
-#pragma unroll
-                for (int k = 0; k < BK; k += 16) {
-                    const u32x4_t bv = *reinterpret_cast<const u32x4_t *>(&Bs[(wn * 32 + lr) * ROW + k + lg * 8]);
-                    const u32x4_t av = *reinterpret_cast<const u32x4_t *>(&As[(wm * 32 + lr) * ROW + k + lg * 8]);
-                    if constexpr (DT == FL_F16)
-                        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, bv),
-                                                                     __builtin_bit_cast(f16x8_t, av), acc, 0, 0, 0);
-                    else
-                        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, bv),
-                                                                      __builtin_bit_cast(bf16x8_t, av), acc, 0, 0, 0);
-                }
-            }
-            if (FORM == kFormGrad && a.dbias && m0 == 0 && tid < BN) {
-#pragma unroll
-                for (int k = 0; k < BK; ++k) dsum += io::to_f32(Bs[tid * ROW + k]);
-            }
+            for (int k = 0; k < BK; k += 2)
+                acc = __builtin_amdgcn_mfma_f32_32x32x2f32(Bs[(wn * 32 + lr) * ROW + k + lg],
+                                                           As[(wm * 32 + lr) * ROW + k + lg], acc, 0, 0, 0);
             __syncthreads();
         }
-        if (FORM == kFormGrad && a.dbias && m0 == 0 && tid < BN && n0 + tid < a.N)
-            a.dbias[(int64_t)e * a.N + n0 + tid] = dsum;
         // lane l: row l%32, columns q*8 + (l/32)*4 + 0..3 of its wave's block
         const int row = m0 + wm * 32 + (lane & 31);
         if (row >= mend) return;
@@ -190,25 +183,18 @@ struct GroupedPlain {
                 if (col >= a.N) continue;
                 const float s = acc[q * 4 + i];
                 if constexpr (FORM == kFormGrad) {
-                    const int64_t o = ((int64_t)e * a.K + row) * a.N + col;
-                    if (a.dw_f32)
-                        static_cast<float *>(a.out)[o] = s;
-                    else
-                        static_cast<raw *>(a.out)[o] = io::from_f32(s);
+                    static_cast<float *>(a.out)[((int64_t)e * a.K + row) * a.N + col] = s;
                 } else {
                     const int64_t o = (int64_t)row * a.N + col;
-                    const float y = ACT == FL_ACT_GLU ? io::to_f32(static_cast<const raw *>(a.Y)[o]) : 0.0f;
+                    const float y = ACT == FL_ACT_GLU ? static_cast<const float *>(a.Y)[o] : 0.0f;
                     if constexpr (FORM == kFormFwd) {
-                        const float b =
-                            a.bias ? io::to_f32(static_cast<const raw *>(a.bias)[(int64_t)e * a.N + col]) : 0.0f;
-                        const float x = s + b;
-                        if (a.out2) static_cast<raw *>(a.out2)[o] = io::from_f32(x);
-                        static_cast<raw *>(a.out)[o] = io::from_f32(activate<ACT>(x, y));
+                        const float x = s + (a.bias ? static_cast<const float *>(a.bias)[(int64_t)e * a.N + col] : 0.0f);
+                        if (a.out2) static_cast<float *>(a.out2)[o] = x;
+                        static_cast<float *>(a.out)[o] = activate<ACT>(x, y);
                     } else {
-                        const float xs = a.X ? io::to_f32(static_cast<const raw *>(a.X)[o]) : 0.0f;
-                        const float dx = s * activate_grad<ACT>(xs, y);
-                        static_cast<raw *>(a.out)[o] = io::from_f32(dx);
-                        if constexpr (ACT == FL_ACT_GLU) static_cast<raw *>(a.out2)[o] = io::from_f32(s * xs);
+                        const float xs = a.X ? static_cast<const float *>(a.X)[o] : 0.0f;
+                        static_cast<float *>(a.out)[o] = s * activate_grad<ACT>(xs, y);
+                        if constexpr (ACT == FL_ACT_GLU) static_cast<float *>(a.out2)[o] = s * xs;
                     }
                 }
             }
@@ -216,18 +202,90 @@ struct GroupedPlain {
     }
 };
 
-template <int DT, int FORM, int ACT>
-__global__ void __launch_bounds__(256) grouped_plain_kernel(GroupedArgs a) {
-    using T = GroupedPlain<DT, FORM, ACT>;
-    __shared__ __attribute__((aligned(16))) typename T::raw As[T::BM * T::ROW], Bs[T::BN * T::ROW];
+template <int FORM, int ACT>
+__global__ void __launch_bounds__(256) grouped_f32_kernel(GroupedArgs a) {
+    using T = GroupedF32<FORM, ACT>;
+    __shared__ __attribute__((aligned(16))) float As[T::BM * T::ROW], Bs[T::BN * T::ROW];
     T::run(a, As, Bs);
+}
+
+// ----------------------------------------------------- the bias gradient
+
+// dbias[e] = the sum of expert e's rows of G: a block sums 128 columns of one
+// expert in 16 groups of rows (group g: rows g, g+16, ..), then adds the groups
+// in order.  A pass over G of its own: 1/K of the operations of dW.
+constexpr int kColumns = 128, kRowGroups = 16;
+typedef uint32_t u32x4_unaligned __attribute__((ext_vector_type(4), aligned(2)));
+
+template <int DT>
+__global__ void __launch_bounds__(256) grouped_column_sum_kernel(GroupedArgs a) {
+    using io = Io<DT>;
+    using raw = typename io::raw;
+    // a thread's 8 columns, in 16-byte loads (which may be unaligned); at the
+    // end of a row it loads the row's last 8 and keeps its own
+    constexpr int PER = 8;
+    __shared__ float part[kRowGroups][kColumns];
+    const int blocks_n = (a.N + kColumns - 1) / kColumns;
+    const int e = blockIdx.x / blocks_n, c0 = (blockIdx.x % blocks_n) * kColumns;
+    const int g = threadIdx.x / (kColumns / PER), c = c0 + (threadIdx.x % (kColumns / PER)) * PER;
+    const int lo = run_bound(a, e), hi = run_bound(a, e + 1);
+    const raw *G = static_cast<const raw *>(a.B);
+    float sum[PER];
+#pragma unroll
+    for (int t = 0; t < PER; ++t) sum[t] = 0.0f;
+    const int at = c + PER <= a.N ? c : a.N - PER;
+    if (at >= 0) {
+        constexpr int W = PER * io::size / 16;
+#pragma unroll 4
+        for (int64_t r = lo + g; r < hi; r += kRowGroups) {
+            const u32x4_unaligned *p = reinterpret_cast<const u32x4_unaligned *>(G + r * a.N + at);
+            raw v[PER];
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const u32x4_t q = p[w];
+                __builtin_memcpy(&v[w * PER / W], &q, 16);
+            }
+#pragma unroll
+            for (int t = 0; t < PER; ++t) sum[t] += io::to_f32(v[t]);
+        }
+    } else {  // fewer than 8 columns in all
+        for (int64_t r = lo + g; r < hi; r += kRowGroups)
+            for (int t = 0; t < PER; ++t)
+                if (at + t >= 0) sum[t] += io::to_f32(G[r * a.N + at + t]);
+    }
+#pragma unroll
+    for (int t = 0; t < PER; ++t)
+        if (at + t >= c) part[g][at + t - c0] = sum[t];
+    __syncthreads();
+    if (threadIdx.x < kColumns && c0 + (int)threadIdx.x < a.N) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kRowGroups; ++i) s += part[i][threadIdx.x];
+        a.dbias[(int64_t)e * a.N + c0 + threadIdx.x] = s;
+    }
 }
 
 typedef void (*grouped_launcher)(const GroupedArgs &, int64_t grid, hipStream_t);
 
-// Launchers of the kernel for (DT, form, act); each dtype's are compiled in
-// their own unit.
+// The tiles of grouped_dma_kernel (fl_grouped_dma.hpp), for 16-bit operands.
+// time: of one workgroup per slot (256 CUs x per_cu), relative to 256x256 tiles
+// at large sizes (8192x2 rows of 8 experts, K 4096, N 14336: 1030, 950, 810, 605
+// and 370 TFLOP/s).
+struct GroupedTileShape {
+    int bm, bn, per_cu;
+    float time;
+};
+enum GroupedVariant { kTile256x256 = 0, kTile256x128, kTile128x128, kTile64x128, kTile32x128, kGroupedVariants };
+constexpr GroupedTileShape kGroupedTiles[kGroupedVariants] = {
+    {256, 256, 1, 1.0f}, {256, 128, 1, 0.54f}, {128, 128, 2, 0.64f}, {64, 128, 2, 0.425f}, {32, 128, 2, 0.35f}};
+typedef void (*grouped_dma_launcher)(const GroupedArgs &, int act, int64_t grid, hipStream_t);
+// Compiled one dtype and form to a unit; the gradient has the first and the third tile only.
+template <int DT, int FORM>
+grouped_dma_launcher pick_grouped_dma_form(int variant);
+
+// Launcher of the fp32 kernel for (form, act).
+grouped_launcher pick_grouped_f32(int form, int act);
 template <int DT>
-grouped_launcher pick_grouped_plain(int form, int act);
+void launch_column_sum(const GroupedArgs &a, hipStream_t s);
 
 }  // namespace fl

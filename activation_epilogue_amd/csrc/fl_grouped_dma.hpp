@@ -1,0 +1,652 @@
+// fl_grouped_dma.hpp -- the experts' products on 16-bit operands: tiles fed by
+// direct-to-LDS loads through a ring of K stages, 16x16x32 MFMA blocks.
+//
+// The three forms of fl_grouped.hpp differ in how an operand lies in memory:
+//   forward   A rows K-contiguous (optionally read through an index), B[e] N-contiguous
+//   backward  G rows K-contiguous, W[e] rows K-contiguous
+//   gradient  A and G both with the summed dimension (the rows of the run) outermost
+// so an operand's tile is either a set of rows of 64 consecutive k (KC) or 64
+// k-rows of consecutive columns (KR), and the tile code is the same for all.
+//
+//   * Copies: one buffer load with the LDS bit moves 64 x 16 bytes into 1 KB of
+//     LDS; the bank swizzle is applied on the global side.  Rows outside the
+//     run, columns past the operand and k past the end get an offset that the
+//     hardware's range check turns into zeros, so a partial tile costs no
+//     traffic for what it lacks.  Pointers need element alignment only.
+//   * MFMA operands: KC tiles are read with 16-byte reads, KR tiles with the
+//     transposing 8-byte read (two for 8 consecutive k of one column).
+//   * A stage is 64 k: two blocks of MFMAs.  The reads of the next block are
+//     slotted between the MFMAs of the current one; the one barrier per stage
+//     stands before the second block, which also issues the copies of the
+//     stage NBUF ahead into the buffer that the barrier has freed.
+//   * Epilogue: 16 rows at a time, a wave's accumulators pass through LDS so
+//     that a lane then holds 8 consecutive columns of one row: Y, X, pre and
+//     out move in 16-byte pieces, whole 128-byte lines per instruction.
+#pragma once
+
+#include "fl_dma16.hpp"
+#include "fl_grouped.hpp"
+
+namespace fl {
+
+constexpr int kStageK = 64;  // k per stage
+
+// A 16-bit load and its wait in one asm block: a load that the compiler tracks,
+// on a branch of the K loop, would make it drain all copies in flight before
+// later LDS reads.
+__device__ __forceinline__ uint32_t load_u16_at(const uint16_t *p) {
+    uint32_t v;
+    asm volatile("global_load_ushort %0, %1, off\n\ts_waitcnt vmcnt(0)" : "=&v"(v) : "v"(p) : "memory");
+    return v & 0xffffu;
+}
+
+// One operand's tile: R rows (KC) or R columns (KR), copied by WAVES waves.
+template <int R, int WAVES, bool KC>
+struct GroupedSide {
+    static constexpr int BYTES = R * kStageK * 2;
+    static constexpr int COPIES = R / (8 * WAVES);  // per wave and stage
+    static constexpr int CB = R / 8;                // KR: 16-byte chunks per k-row
+    static constexpr int PARTS = KC ? 1 : 2;        // LDS reads per MFMA operand
+    static_assert(COPIES >= 1 && COPIES * 8 * WAVES == R, "whole copies");
+    static_assert(KC || R == 128 || R == 256, "KR swizzle");
+
+    i32x4_t rsrc;
+    uint32_t off[COPIES];  // byte offset of the lane's chunk at k = 0, kOob outside the operand
+    int k0[KC ? 2 : 1];    // k within the stage of copies 0 (and 1)
+    int frag;              // LDS address of the wave's first operand read within the side (KC: at chunk 0)
+    int fk;                // KC: chunk xor of the lane's row
+
+    // 16-byte reads of 16 consecutive rows at one chunk per 16 lanes fall on
+    // distinct banks (KC; rows of 128 bytes)
+    __device__ __forceinline__ static int fa(int r) { return ((r >> 1) ^ ((r & 1) << 2)) & 7; }
+    // the 4 k-rows (and those 8 further) of a transposing read fall on
+    // distinct banks (KR; rows of 256 or 512 bytes); always even
+    __device__ __forceinline__ static int fb(int r) { return ((0xAC60 >> (4 * (r & 3))) & 0xF) ^ ((r >> 2) & 2); }
+
+    // Lane's place in copy i: its row (KC) or k-row (KR), and its chunk.
+    __device__ __forceinline__ static void place(int wave, int lane, int i, int &row, int &chunk) {
+        const int q = 64 * (wave * COPIES + i) + lane;
+        if constexpr (KC) {
+            row = q >> 3;
+            chunk = (q & 7) ^ fa(row);
+        } else {
+            row = q / CB;
+            chunk = (q % CB) ^ fb(row);
+        }
+    }
+
+    // Copy i's k within the stage: a KC copy's chunk depends on its row modulo
+    // 16, and copies are 8 rows apart; KR copies are 64 / CB k-rows apart.
+    __device__ __forceinline__ int k(int i) const {
+        if constexpr (KC)
+            return k0[i & 1];
+        else
+            return k0[0] + (64 / CB) * i;
+    }
+
+    // Operand reads for output rows (columns) w0 .. of the tile.
+    __device__ __forceinline__ void set_frag(int w0, int lane) {
+        const int g = lane >> 4, i = lane & 15;
+        if constexpr (KC) {
+            frag = (w0 + i) * 128;
+            fk = g ^ fa(i);  // w0 is a multiple of 16; block kk flips bit 2
+        } else {
+            const int rk = g * 8 + (i >> 2), n = w0 + 4 * (i & 3);
+            frag = rk * (R * 2) + (((n >> 3) ^ fb(rk)) * 16) + ((n >> 2) & 1) * 8;
+            fk = 0;
+        }
+    }
+    // Read P of the operand of 16-row block b at MFMA block kk.
+    template <int P>
+    __device__ __forceinline__ void read(const FL_LDS char *s, int b, int kk, i32x2_t (&v)[2]) const {
+        if constexpr (KC) {
+            const u32x4_t t = *(const FL_LDS u32x4_t *)(s + frag + ((fk ^ (kk * 4)) * 16) + b * (16 * 128));
+            v[0] = i32x2_t{(int)t[0], (int)t[1]};
+            v[1] = i32x2_t{(int)t[2], (int)t[3]};
+        } else {
+            // the wave's first column is a multiple of its columns, a power of two: block b is one xor away
+            v[P] = __builtin_bit_cast(
+                i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                             (FL_LDS s16x4_t *)(s + (frag ^ (b * 32)) + (kk * 32 + P * 4) * (R * 2))));
+        }
+    }
+
+    // Puts right what 16-byte copies get wrong in the last stage (kleft <= 64
+    // k of it exist), on the chunks that this wave copied, after they landed:
+    //  * the range check works on whole dwords, so an odd last element of the
+    //    operand reads as zero: it is loaded again by itself;
+    //  * a KC chunk that crosses the end of k holds values of the next row.
+    // left: elements from the stage's origin to the end of the operand; last:
+    // its last element.
+    __device__ __forceinline__ void fix_tail(FL_LDS char *s, int wave, int lane, int64_t left, int kleft,
+                                             const uint16_t *last) const {
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+            if (off[i] == kOob || k(i) >= kleft) continue;
+            const int64_t rest = left - (int64_t)(off[i] >> 1);  // elements from the chunk's first to the end
+            const int valid = kleft - k(i);
+            const bool odd = rest < 8 && (rest & 1);
+            if (!odd && (!KC || valid >= 8)) continue;
+            FL_LDS char *p = s + (wave * COPIES + i) * 1024 + lane * 16;
+            u32x4_t v = *(FL_LDS u32x4_t *)p;
+            if (odd) {
+                const uint32_t x = load_u16_at(last);
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    if (d == (int)(rest >> 1)) v[d] = x;  // (the element after it is past the end)
+            }
+            if constexpr (KC) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const int n = valid - 2 * d;
+                    v[d] &= n >= 2 ? 0xffffffffu : n == 1 ? 0xffffu : 0u;
+                }
+            }
+            *(FL_LDS u32x4_t *)p = v;
+        }
+    }
+};
+
+// One tile of BM x BN outputs on WM x WN waves.  NBUF stages of LDS.
+template <int DT, int FORM, int BM_, int BN_, int WM, int WN, int NBUF_>
+struct GroupedTile {
+    using io = Io<DT>;
+    using raw = typename io::raw;
+    static constexpr int BM = BM_, BN = BN_, NBUF = NBUF_;
+    static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+    static constexpr int TM = BM / WM, TN = BN / WN, NRB = TM / 16, NI = TN / 16;
+    using SideA = GroupedSide<BM, WAVES, FORM != kFormGrad>;
+    using SideB = GroupedSide<BN, WAVES, FORM == kFormBwd>;
+    static constexpr int BUF_BYTES = SideA::BYTES + SideB::BYTES;
+    static constexpr int COPIES = SideA::COPIES + SideB::COPIES;
+    static constexpr int SLOTS = NRB * NI;
+    static constexpr int RA = SideA::PARTS, RB = SideB::PARTS, READS = NRB * RA + NI * RB;
+    static constexpr int EPI_ROW = TN * 4 + 16;
+    static constexpr int EPI_BYTES = WAVES * 16 * EPI_ROW;
+    static constexpr int SMEM = NBUF * BUF_BYTES;
+    static_assert(NBUF >= 2 && SMEM <= 163840 && EPI_BYTES <= BUF_BYTES, "LDS");
+    static_assert((TN & (TN - 1)) == 0 && (TM & (TM - 1)) == 0, "power-of-two wave tiles");
+
+    struct Ops {
+        SideA A;
+        SideB B;
+        const char *pa, *pb;   // gradient: the stage's origin in A and G
+        int64_t ra, rb;        // elements from the descriptor bases (gradient: the stage's origin) to the end
+        int lda, ldb, depth;
+    };
+    struct Frags {
+        i32x2_t a[NRB][2], b[NI][2];
+    };
+
+    struct Dst {  // LDS addresses of a wave's first copy of either operand
+        uint32_t a, b;
+    };
+    template <int I>
+    __device__ __forceinline__ static void copy_one(const Ops &o, int kt, Dst buf) {
+        const int kleft = o.depth - kt * kStageK;
+        if constexpr (I < SideA::COPIES) {
+            const uint32_t so = FORM == kFormGrad ? 0 : (uint32_t)kt * (kStageK * 2);
+            lds_copy16(o.A.rsrc, o.A.k(I) < kleft ? o.A.off[I] : kOob, so, buf.a + I * 1024);
+        } else {
+            constexpr int i = I - SideA::COPIES;
+            const uint32_t so = FORM == kFormGrad  ? 0
+                                : FORM == kFormBwd ? (uint32_t)kt * (kStageK * 2)
+                                                   : (uint32_t)kt * (uint32_t)(kStageK * 2) * (uint32_t)o.ldb;
+            lds_copy16(o.B.rsrc, o.B.k(i) < kleft ? o.B.off[i] : kOob, so, buf.b + i * 1024);
+        }
+    }
+    template <int C0, int C1>
+    __device__ __forceinline__ static void copy_range(const Ops &o, int kt, Dst buf) {
+        if constexpr (C0 < C1) {
+            copy_one<C0>(o, kt, buf);
+            copy_range<C0 + 1, C1>(o, kt, buf);
+        }
+    }
+    __device__ __forceinline__ static Dst copy_base(uint32_t lds, int b, int wave) {
+        const uint32_t s = lds + b * BUF_BYTES;
+        return {(uint32_t)__builtin_amdgcn_readfirstlane(s + wave * SideA::COPIES * 1024),
+                (uint32_t)__builtin_amdgcn_readfirstlane(s + SideA::BYTES + wave * SideB::COPIES * 1024)};
+    }
+
+    // The gradient's operands may span more than 2 GiB: their descriptors move
+    // with the stages instead of a 32-bit offset.  pa, pb, ra, rb are those of
+    // the stage copied last.
+    __device__ __forceinline__ static void set_descriptors(Ops &o) {
+        o.A.rsrc = sgpr_rsrc(o.pa, o.ra > 0 ? (size_t)o.ra * 2 : 0);
+        o.B.rsrc = sgpr_rsrc(o.pb, o.rb > 0 ? (size_t)o.rb * 2 : 0);
+    }
+    __device__ __forceinline__ static void next_stage(Ops &o) {
+        if constexpr (FORM == kFormGrad) {
+            const int64_t da = (int64_t)kStageK * o.lda, db = (int64_t)kStageK * o.ldb;
+            o.pa += da * 2;
+            o.pb += db * 2;
+            o.ra -= da;
+            o.rb -= db;
+            set_descriptors(o);
+        }
+    }
+
+    template <int P>
+    __device__ __forceinline__ static void read_piece(const Ops &o, const FL_LDS char *s, int kk, Frags &f) {
+        // in the order the MFMAs take them: a0, b0 .. , a1 ..
+        if constexpr (P < RA) {
+            o.A.template read<P>(s, 0, kk, f.a[0]);
+        } else if constexpr (P < RA + NI * RB) {
+            constexpr int q = P - RA;
+            o.B.template read<q % RB>(s + SideA::BYTES, q / RB, kk, f.b[q / RB]);
+        } else {
+            constexpr int q = P - NI * RB;
+            o.A.template read<q % RA>(s, q / RA, kk, f.a[q / RA]);
+        }
+    }
+    template <int P0, int P1>
+    __device__ __forceinline__ static void read_range(const Ops &o, const FL_LDS char *s, int kk, Frags &f) {
+        if constexpr (P0 < P1) {
+            read_piece<P0>(o, s, kk, f);
+            read_range<P0 + 1, P1>(o, s, kk, f);
+        }
+    }
+
+    // MFMA I of a block, rows of blocks in snake order: consecutive MFMAs
+    // share an operand (fewer operand bits toggle, a higher clock).
+    template <int I>
+    __device__ __forceinline__ static void mma(const Frags &f, f32x4_t (&acc)[NRB][NI]) {
+        constexpr int mi = I / NI, ni = (mi & 1) ? NI - 1 - I % NI : I % NI;
+        const auto av = __builtin_shufflevector(f.a[mi][0], f.a[mi][1], 0, 1, 2, 3);
+        const auto bv = __builtin_shufflevector(f.b[ni][0], f.b[ni][1], 0, 1, 2, 3);
+        if constexpr (DT == FL_F16)
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, bv),
+                                                                 __builtin_bit_cast(f16x8_t, av), acc[mi][ni], 0, 0, 0);
+        else
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, bv),
+                                                                  __builtin_bit_cast(bf16x8_t, av), acc[mi][ni], 0, 0, 0);
+    }
+
+    // One block: the MFMAs on `use`, the reads of block kk of `s` into `fill`
+    // and, if COPY, the copies of stage kt into `buf` spread over them.
+    template <int I, bool COPY>
+    __device__ __forceinline__ static void block(const Ops &o, const FL_LDS char *s, int kk, int kt, Dst buf,
+                                                 const Frags &use, Frags &fill, f32x4_t (&acc)[NRB][NI]) {
+        if constexpr (I < SLOTS) {
+            mma<I>(use, acc);
+            if constexpr (COPY)
+                copy_range<(I * COPIES + SLOTS - 1) / SLOTS, ((I + 1) * COPIES + SLOTS - 1) / SLOTS>(o, kt, buf);
+            read_range<I * READS / SLOTS, (I + 1) * READS / SLOTS>(o, s, kk, fill);
+            __builtin_amdgcn_sched_barrier(0);
+            block<I + 1, COPY>(o, s, kk, kt, buf, use, fill, acc);
+        }
+    }
+
+    template <int N>
+    __device__ __forceinline__ static void wait_vm() {
+        __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+        asm volatile("" ::: "memory");
+    }
+
+    __device__ __forceinline__ static bool ragged(const GroupedArgs &a) {
+        return FORM == kFormBwd ? (a.K & 7) : ((a.K | a.N) & 7);
+    }
+    // fix_tail of both sides for stage kt; `ahead` stages after it are copied.
+    __device__ __forceinline__ static void fix_tail(const GroupedArgs &a, const Ops &o, int kt, int ahead, int wave,
+                                                    int lane, FL_LDS char *s) {
+        const int64_t k0 = (int64_t)kt * kStageK;
+        const int kleft = (int)(o.depth - k0);
+        int64_t la = o.ra - k0, lb = o.rb - (FORM == kFormBwd ? k0 : k0 * o.ldb);
+        if constexpr (FORM == kFormGrad) {
+            la = o.ra + (int64_t)ahead * kStageK * o.lda;
+            lb = o.rb + (int64_t)ahead * kStageK * o.ldb;
+        }
+        const int64_t nb = FORM == kFormGrad ? (int64_t)a.S * a.N : (int64_t)a.E * a.K * a.N;
+        o.A.fix_tail(s, wave, lane, la, kleft, static_cast<const uint16_t *>(a.A) + (a.A_rows * a.K - 1));
+        o.B.fix_tail(s + SideA::BYTES, wave, lane, lb, kleft, static_cast<const uint16_t *>(a.B) + (nb - 1));
+    }
+
+    // Stage kt in LDS buffer `buf`; its block 0 operands are in f[0].
+    template <bool TAIL>
+    __device__ __forceinline__ static void stage(const GroupedArgs &a, Ops &o, const FL_LDS char *lds, uint32_t addr,
+                                                 int kt, int nk, int buf, int wave, Frags (&f)[2],
+                                                 f32x4_t (&acc)[NRB][NI]) {
+        block<0, false>(o, lds + buf * BUF_BYTES, 1, 0, Dst{}, f[0], f[1], acc);
+        const FL_LDS char *nxt = lds + (buf + 1 == NBUF ? 0 : buf + 1) * BUF_BYTES;
+        if constexpr (TAIL) {
+            if (ragged(a) && kt + 2 == nk) {
+                wait_vm<(NBUF - 2) * COPIES>();  // the last stage has landed
+                fix_tail(a, o, kt + 1, NBUF - 2, wave, threadIdx.x & 63, (FL_LDS char *)nxt);
+            }
+        }
+        wait_vm<(NBUF - 2) * COPIES>();
+        __syncthreads();
+        next_stage(o);
+        block<0, true>(o, nxt, 0, kt + NBUF, copy_base(addr, buf, wave), f[1], f[0], acc);
+    }
+
+    // Copies of stages B0 .. B1-1 into the buffers of their numbers.
+    template <int B0, int B1>
+    __device__ __forceinline__ static void prefetch(Ops &o, int wave, uint32_t addr) {
+#pragma unroll
+        for (int b = B0; b < B1; ++b) {
+            if (b > 0) next_stage(o);
+            copy_range<0, COPIES>(o, b, copy_base(addr, b, wave));
+        }
+    }
+
+    // The tile's product; stages 0 .. NBUF-1 are on their way.
+    __device__ __forceinline__ static void product(const GroupedArgs &a, Ops &o, int wave, int lane,
+                                                   const FL_LDS char *lds, uint32_t addr, f32x4_t (&acc)[NRB][NI]) {
+#pragma unroll
+        for (int mi = 0; mi < NRB; ++mi)
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        const int nk = o.depth > 0 ? (int)(((int64_t)o.depth + kStageK - 1) / kStageK) : 1;  // (no k: one stage of zeros)
+        // whatever the epilogue before left in flight came after stage 0
+        wait_vm<(NBUF - 1) * COPIES>();
+        if (nk == 1 && ragged(a)) fix_tail(a, o, 0, NBUF - 1, wave, lane, (FL_LDS char *)lds);
+        __syncthreads();
+        Frags f[2];
+        read_range<0, READS>(o, lds, 0, f[0]);
+        int buf = 0, kt = 0;
+#pragma unroll 1
+        for (; kt + 2 < nk; ++kt) {
+            stage<false>(a, o, lds, addr, kt, nk, buf, wave, f, acc);
+            buf = buf + 1 == NBUF ? 0 : buf + 1;
+        }
+#pragma unroll 1
+        for (; kt < nk; ++kt) {
+            stage<true>(a, o, lds, addr, kt, nk, buf, wave, f, acc);
+            buf = buf + 1 == NBUF ? 0 : buf + 1;
+        }
+        // the look-ahead copies past the end land before the LDS is used again
+        wait_vm<0>();
+        __syncthreads();
+    }
+
+    // ---- epilogue
+    __device__ __forceinline__ static u32x4_t load8(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid) {
+        u32x4_t v = {0, 0, 0, 0};
+        if (valid >= 8) {
+            v = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e) {
+                const uint32_t x = load_elem<2>(r, e < valid && off != kOob ? off + e * 2 : kOob);
+                v[e >> 1] |= x << (16 * (e & 1));
+            }
+        }
+        return v;
+    }
+    __device__ __forceinline__ static float get8(const u32x4_t &v, int e) {
+        return io::to_f32((raw)(v[e >> 1] >> (16 * (e & 1))));
+    }
+    __device__ __forceinline__ static void store8(const float (&v)[8], __amdgpu_buffer_rsrc_t r, uint32_t off, int valid) {
+        u32x4_t w;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) w[d] = io::pack2(v[2 * d], v[2 * d + 1]);
+        if (valid >= 8) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, w), r, off, 0, 0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                store_elem<2>((uint16_t)(w[e >> 1] >> (16 * (e & 1))), r,
+                              e < valid && off != kOob ? off + e * 2 : kOob);
+        }
+    }
+    __device__ __forceinline__ static void store8_f32(const float (&v)[8], __amdgpu_buffer_rsrc_t r, uint32_t off,
+                                                      int valid) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (valid >= 4 * h + 4) {
+                const u32x4_t w = {__builtin_bit_cast(uint32_t, v[4 * h]), __builtin_bit_cast(uint32_t, v[4 * h + 1]),
+                                   __builtin_bit_cast(uint32_t, v[4 * h + 2]), __builtin_bit_cast(uint32_t, v[4 * h + 3])};
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, w), r,
+                                                       off != kOob ? off + h * 16 : kOob, 0, 0);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    store_elem<4>(__builtin_bit_cast(uint32_t, v[4 * h + e]), r,
+                                  4 * h + e < valid && off != kOob ? off + h * 16 + e * 4 : kOob);
+            }
+        }
+    }
+
+    struct Tile {
+        int e, tn;     // expert, column tile
+        int depth;     // summed elements
+        int lo;        // first row of the run
+        int m0, rows;  // first output row (within the operands: of all rows, or of the expert's dW), rows that exist
+    };
+
+    template <int ACT>
+    __device__ __forceinline__ static void epilogue(const GroupedArgs &a, const Tile &t, int wave, int lane,
+                                                    const f32x4_t (&acc)[NRB][NI], FL_LDS char *lds) {
+        const int rows = t.rows, n0 = t.tn * BN;
+        const int64_t row0 = FORM == kFormGrad ? (int64_t)t.e * a.K + t.m0 : t.m0;
+        const int wm = wave / WN, wn = wave % WN;
+        constexpr int CPR = TN / 8, RPP = 64 / CPR, PASSES = 16 / RPP;  // lanes per row, rows and passes per row block
+        const int es = FORM == kFormGrad && a.dw_f32 ? 4 : 2;
+        const int64_t org = row0 * a.N + n0;
+        const size_t bytes = ((size_t)rows * a.N - n0) * es;
+        const __amdgpu_buffer_rsrc_t rO = make_rsrc(static_cast<char *>(a.out) + org * es, bytes);
+        const __amdgpu_buffer_rsrc_t rO2 =
+            make_rsrc(a.out2 ? static_cast<char *>(a.out2) + org * 2 : nullptr, a.out2 ? bytes : 0);
+        const __amdgpu_buffer_rsrc_t rY =
+            make_rsrc(a.Y ? static_cast<const char *>(a.Y) + org * 2 : nullptr, a.Y ? bytes : 0);
+        const __amdgpu_buffer_rsrc_t rX =
+            make_rsrc(a.X ? static_cast<const char *>(a.X) + org * 2 : nullptr, a.X ? bytes : 0);
+        const int col = wn * TN + (lane % CPR) * 8, valid = a.N - n0 - col;
+        FL_LDS char *w = lds + wave * 16 * EPI_ROW;
+        auto offset = [&](int mi, int p) -> uint32_t {
+            const int row = wm * TM + mi * 16 + p * RPP + lane / CPR;
+            return row < rows && valid > 0 ? (uint32_t)(row * a.N + col) * es : kOob;
+        };
+        u32x4_t bias = {0, 0, 0, 0};
+        if constexpr (FORM == kFormFwd) {
+            if (a.bias) {
+                const __amdgpu_buffer_rsrc_t rB = make_rsrc(
+                    static_cast<const char *>(a.bias) + ((int64_t)t.e * a.N + n0) * 2, (size_t)(a.N - n0) * 2);
+                bias = load8(rB, valid > 0 ? (uint32_t)col * 2 : kOob, valid);
+            }
+        }
+        constexpr bool NEED_Y = ACT == FL_ACT_GLU, NEED_X = FORM == kFormBwd && ACT != FL_ACT_NONE;
+        u32x4_t yv[2][PASSES], xv[2][PASSES];  // of this row block and the next
+        auto sides = [&](int mi) {
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                if constexpr (NEED_Y) yv[mi & 1][p] = load8(rY, offset(mi, p), valid);
+                if constexpr (NEED_X) xv[mi & 1][p] = load8(rX, offset(mi, p), valid);
+            }
+        };
+        sides(0);
+#pragma unroll
+        for (int mi = 0; mi < NRB; ++mi) {
+            if (mi + 1 < NRB) sides(mi + 1);
+            // lane: row lane % 16 of the block, columns ni*16 + (lane/16)*4 + 0..3
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni)
+                *(FL_LDS f32x4_t *)(w + (lane & 15) * EPI_ROW + (ni * 16 + (lane >> 4) * 4) * 4) = acc[mi][ni];
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const FL_LDS char *s = w + (p * RPP + lane / CPR) * EPI_ROW + (lane % CPR) * 32;
+                const f32x4_t lo = *(const FL_LDS f32x4_t *)s, hi = *(const FL_LDS f32x4_t *)(s + 16);
+                const uint32_t off = offset(mi, p);
+                float v[8], v2[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float d = i < 4 ? lo[i & 3] : hi[i & 3];
+                    const float y = NEED_Y ? get8(yv[mi & 1][p], i) : 0.0f;
+                    if constexpr (FORM == kFormFwd) {
+                        const float x = d + get8(bias, i);
+                        v2[i] = x;
+                        v[i] = activate<ACT>(x, y);
+                    } else if constexpr (FORM == kFormBwd) {
+                        const float xs = NEED_X ? get8(xv[mi & 1][p], i) : 0.0f;
+                        v[i] = d * activate_grad<ACT>(xs, y);
+                        v2[i] = d * xs;
+                        asm("" : "+v"(v[i]), "+v"(v2[i]));  // fp32 before the cast, in every kernel alike
+                    } else {
+                        v[i] = d;
+                    }
+                }
+                if (FORM == kFormGrad && a.dw_f32)
+                    store8_f32(v, rO, off, valid);
+                else
+                    store8(v, rO, off, valid);
+                if (FORM == kFormFwd ? a.out2 != nullptr : FORM == kFormBwd && ACT == FL_ACT_GLU)
+                    store8(v2, rO2, off, valid);
+            }
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // Tile number b of n.  Workgroups of one XCD (b modulo 8) share a run of
+    // consecutive tiles, which belong to few experts, and within an expert to
+    // bands of a.group row tiles swept column by column: the XCD's L2 serves
+    // their shared operands.
+    __device__ __forceinline__ static bool find(const GroupedArgs &a, int b, int n, Tile &t) {
+        if (b >= n) return false;
+        const int pid = xcd_logical(b, n);
+        int m;
+        if constexpr (FORM == kFormGrad) {
+            const int per = (a.K + BM - 1) / BM;
+            t.e = pid / (per * a.tiles_n);
+            t.lo = run_bound(a, t.e);
+            const int hi = run_bound(a, t.e + 1);
+            t.depth = hi > t.lo ? hi - t.lo : 0;
+            grouped_tile(pid - t.e * per * a.tiles_n, per, a.tiles_n, a.group, m, t.tn);
+            t.m0 = m * BM;
+            t.rows = a.K - t.m0 < BM ? a.K - t.m0 : BM;
+        } else {
+            const int q = pid / a.tiles_n;
+            const RunTile r = find_run_tile(a, BM, q);
+            if (r.e < 0) return false;
+            const int cnt = (r.hi - r.lo + BM - 1) / BM;
+            const int local = pid - (q - r.m) * a.tiles_n;
+            if (r.m < 0 || r.m >= cnt || local < 0) return false;  // (offsets that are no plan's)
+            grouped_tile(local, cnt, a.tiles_n, a.group, m, t.tn);
+            if (m < 0 || m >= cnt || t.tn < 0 || t.tn >= a.tiles_n) return false;
+            t.e = r.e;
+            t.lo = r.lo;
+            t.depth = a.K;
+            t.m0 = r.lo + m * BM;
+            t.rows = r.hi - t.m0 < BM ? r.hi - t.m0 : BM;
+        }
+        // scalars, so that descriptors and loop bounds are
+        t.e = __builtin_amdgcn_readfirstlane(t.e);
+        t.tn = __builtin_amdgcn_readfirstlane(t.tn);
+        t.depth = __builtin_amdgcn_readfirstlane(t.depth);
+        t.lo = __builtin_amdgcn_readfirstlane(t.lo);
+        t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
+        t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+        return true;
+    }
+
+    __device__ __forceinline__ static void setup(const GroupedArgs &a, const Tile &t, int wave, int lane, Ops &o) {
+        const int n0 = t.tn * BN;
+        o.depth = t.depth;
+        o.lda = a.K;
+        o.ldb = FORM == kFormBwd ? a.K : a.N;
+        if constexpr (FORM == kFormGrad) {
+            o.pa = static_cast<const char *>(a.A) + ((int64_t)t.lo * a.K + t.m0) * 2;
+            o.pb = static_cast<const char *>(a.B) + ((int64_t)t.lo * a.N + n0) * 2;
+            o.ra = (int64_t)(a.S - t.lo) * a.K - t.m0;
+            o.rb = (int64_t)(a.S - t.lo) * a.N - n0;
+            set_descriptors(o);
+        } else {
+            const int64_t a0 = FORM == kFormFwd && a.index ? 0 : (int64_t)t.m0 * a.K;
+            o.ra = a.A_rows * a.K - a0;
+            o.A.rsrc = sgpr_rsrc(static_cast<const char *>(a.A) + a0 * 2, (size_t)o.ra * 2);
+            const int64_t b0 = (int64_t)t.e * a.K * a.N + (FORM == kFormBwd ? (int64_t)n0 * a.K : n0);
+            o.rb = (int64_t)a.E * a.K * a.N - b0;
+            o.B.rsrc = sgpr_rsrc(static_cast<const char *>(a.B) + b0 * 2, (size_t)o.rb * 2);
+        }
+#pragma unroll
+        for (int i = 0; i < SideA::COPIES; ++i) {
+            int r, c;
+            SideA::place(wave, lane, i, r, c);
+            if constexpr (FORM == kFormGrad) {
+                o.A.off[i] = c * 8 < t.rows ? (uint32_t)(r * o.lda + c * 8) * 2 : kOob;
+                if (i == 0) o.A.k0[0] = r;
+            } else {
+                int64_t row = r;
+                bool ok = r < t.rows;
+                if (FORM == kFormFwd && a.index) {
+                    row = ok ? a.index[t.m0 + r] : 0;
+                    ok = ok && row >= 0 && row < a.A_rows;
+                }
+                o.A.off[i] = ok ? ((uint32_t)row * (uint32_t)o.lda + c * 8) * 2 : kOob;
+                if (i < 2) o.A.k0[i] = c * 8;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < SideB::COPIES; ++i) {
+            int r, c;
+            SideB::place(wave, lane, i, r, c);
+            if constexpr (FORM == kFormBwd) {
+                o.B.off[i] = n0 + r < a.N ? (uint32_t)(r * o.ldb + c * 8) * 2 : kOob;
+                if (i < 2) o.B.k0[i] = c * 8;
+            } else {
+                o.B.off[i] = n0 + c * 8 < a.N ? (uint32_t)(r * o.ldb + c * 8) * 2 : kOob;
+                if (i == 0) o.B.k0[0] = r;
+            }
+        }
+    }
+
+    // Tiles blockIdx.x, + gridDim.x, ..  While a tile's epilogue runs in the
+    // last LDS buffer, the first NBUF-1 stages of the next one are on their
+    // way into the others.
+    __device__ __forceinline__ static void run(const GroupedArgs &a, int act, char *smem) {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        FL_LDS char *lds = (FL_LDS char *)smem;
+        const uint32_t addr = (uint32_t)(uintptr_t)(FL_LDS void *)smem;
+        const int64_t all = FORM == kFormGrad ? (int64_t)a.E * ((a.K + BM - 1) / BM) * a.tiles_n
+                                              : (int64_t)count_run_tiles(a, BM) * a.tiles_n;
+        const int n = __builtin_amdgcn_readfirstlane((int)(all < a.max_tiles ? all : a.max_tiles));
+        int b = blockIdx.x;
+        Tile t;
+        if (!find(a, b, n, t)) return;
+        Ops o;
+        o.A.set_frag((wave / WN) * TM, lane);
+        o.B.set_frag((wave % WN) * TN, lane);
+        setup(a, t, wave, lane, o);
+        prefetch<0, NBUF - 1>(o, wave, addr);
+        for (;;) {
+            prefetch<NBUF - 1, NBUF>(o, wave, addr);
+            b += gridDim.x;
+            Tile next;
+            const bool more = find(a, b, n, next);
+            f32x4_t acc[NRB][NI];
+            product(a, o, wave, lane, lds, addr, acc);
+            // addresses of the next tile and of the epilogue come from a copy
+            // of the lane made here, so that they are not kept across K loops
+            int le = lane;
+            asm volatile("" : "+v"(le));
+            if (more) {
+                setup(a, next, wave, le, o);
+                prefetch<0, NBUF - 1>(o, wave, addr);
+            }
+            FL_LDS char *epi = lds + (NBUF - 1) * BUF_BYTES;
+            if (FORM == kFormGrad || act == FL_ACT_NONE)
+                epilogue<FL_ACT_NONE>(a, t, wave, le, acc, epi);
+            else if (act == FL_ACT_RELU)
+                epilogue<FL_ACT_RELU>(a, t, wave, le, acc, epi);
+            else if (act == FL_ACT_GELU_TANH)
+                epilogue<FL_ACT_GELU_TANH>(a, t, wave, le, acc, epi);
+            else
+                epilogue<FL_ACT_GLU>(a, t, wave, le, acc, epi);
+            if (!more) break;
+            t = next;
+            __syncthreads();  // the last buffer is free for copies again
+        }
+    }
+};
+
+template <int DT, int FORM, int BM, int BN, int WM, int WN, int NBUF, int OCC>
+__global__ void __launch_bounds__(64 * WM * WN, OCC) grouped_dma_kernel(GroupedArgs a, int act) {
+    using T = GroupedTile<DT, FORM, BM, BN, WM, WN, NBUF>;
+    __shared__ __attribute__((aligned(1024))) char smem[T::SMEM];
+    T::run(a, act, smem);
+}
+
+}  // namespace fl

@@ -1,4 +1,5 @@
-// fl_grouped_inst.hip -- instantiates the experts' products for one dtype.
+// fl_grouped_inst.hip -- instantiates the column sum for one dtype, and for
+// fp32 the experts' products (16-bit operands: fl_grouped_dma_inst.hip).
 // Built once per dtype with -DFL_INST_DTYPE=<fl_dtype value>.
 #include "fl_grouped.hpp"
 
@@ -7,31 +8,34 @@
 #endif
 
 namespace fl {
-namespace {
 
-template <int DT, int FORM, int ACT>
-void launch_plain(const GroupedArgs &a, int64_t grid, hipStream_t s) {
-    hipLaunchKernelGGL((grouped_plain_kernel<DT, FORM, ACT>), dim3((unsigned)grid), dim3(256), 0, s, a);
+#if FL_INST_DTYPE == 0
+template <int FORM, int ACT>
+static void launch_f32(const GroupedArgs &a, int64_t grid, hipStream_t s) {
+    hipLaunchKernelGGL((grouped_f32_kernel<FORM, ACT>), dim3((unsigned)grid), dim3(256), 0, s, a);
 }
 
-template <int DT, int FORM>
-grouped_launcher pick_plain_act(int act) {
+template <int FORM>
+static grouped_launcher pick_act(int act) {
     switch (act) {
-    case FL_ACT_NONE: return launch_plain<DT, FORM, FL_ACT_NONE>;
-    case FL_ACT_RELU: return launch_plain<DT, FORM, FL_ACT_RELU>;
-    case FL_ACT_GELU_TANH: return launch_plain<DT, FORM, FL_ACT_GELU_TANH>;
-    default: return launch_plain<DT, FORM, FL_ACT_GLU>;
+    case FL_ACT_NONE: return launch_f32<FORM, FL_ACT_NONE>;
+    case FL_ACT_RELU: return launch_f32<FORM, FL_ACT_RELU>;
+    case FL_ACT_GELU_TANH: return launch_f32<FORM, FL_ACT_GELU_TANH>;
+    default: return launch_f32<FORM, FL_ACT_GLU>;
     }
 }
 
-}  // namespace
+grouped_launcher pick_grouped_f32(int form, int act) {
+    if (form == kFormFwd) return pick_act<kFormFwd>(act);
+    if (form == kFormBwd) return pick_act<kFormBwd>(act);
+    return launch_f32<kFormGrad, FL_ACT_NONE>;
+}
+#endif
 
 template <>
-grouped_launcher pick_grouped_plain<FL_INST_DTYPE>(int form, int act) {
-    constexpr int DT = FL_INST_DTYPE;
-    if (form == kFormFwd) return pick_plain_act<DT, kFormFwd>(act);
-    if (form == kFormBwd) return pick_plain_act<DT, kFormBwd>(act);
-    return launch_plain<DT, kFormGrad, FL_ACT_NONE>;
+void launch_column_sum<FL_INST_DTYPE>(const GroupedArgs &a, hipStream_t s) {
+    const unsigned blocks = (unsigned)a.E * (unsigned)((a.N + kColumns - 1) / kColumns);
+    hipLaunchKernelGGL((grouped_column_sum_kernel<FL_INST_DTYPE>), dim3(blocks), dim3(256), 0, s, a);
 }
 
 }  // namespace fl

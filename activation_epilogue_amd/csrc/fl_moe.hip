@@ -26,6 +26,7 @@ void clear_error() { g_err[0] = '\0'; }
 
 constexpr int64_t kMaxDim = 0x7fffffff;
 constexpr size_t kTwoGiB = 0x80000000ull;
+constexpr int kCus = 256;  // workgroups of a persistent kernel that fill the chip, one per CU
 
 size_t elem_size(int dtype) { return dtype == FL_F32 ? 4 : 2; }
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
@@ -202,22 +203,73 @@ int64_t most_row_tiles(int64_t S, int64_t E, int64_t bm) {
     return (S + runs * (bm - 1)) / bm;
 }
 
-fl::grouped_launcher pick_plain(int dtype, int form, int act) {
-    if (dtype == FL_F32) return fl::pick_grouped_plain<FL_F32>(form, act);
-    if (dtype == FL_F16) return fl::pick_grouped_plain<FL_F16>(form, act);
-    return fl::pick_grouped_plain<FL_BF16>(form, act);
-}
-
 size_t grouped_workspace(int64_t, int64_t, int64_t, int64_t, int) { return 0; }
 
+fl::grouped_dma_launcher pick_dma(int dtype, int form, int variant) {
+    using namespace fl;
+    if (dtype == FL_F16)
+        return form == kFormFwd   ? pick_grouped_dma_form<FL_F16, kFormFwd>(variant)
+               : form == kFormBwd ? pick_grouped_dma_form<FL_F16, kFormBwd>(variant)
+                                  : pick_grouped_dma_form<FL_F16, kFormGrad>(variant);
+    return form == kFormFwd   ? pick_grouped_dma_form<FL_BF16, kFormFwd>(variant)
+           : form == kFormBwd ? pick_grouped_dma_form<FL_BF16, kFormBwd>(variant)
+                              : pick_grouped_dma_form<FL_BF16, kFormGrad>(variant);
+}
+
+// The tile for 16-bit operands: the one of least estimated time, in rounds of
+// a full chip.  Runs end inside a tile, so S rows in R runs make about S/bm +
+// R/2 row tiles (at least R); rounds beyond the first end ragged, half a round
+// on average.
+int pick_variant(int form, int64_t S, int64_t N, int64_t K, int64_t E) {
+    int best = 0;
+    double least = 0.0;
+    for (int v = 0; v < fl::kGroupedVariants; ++v) {
+        if (form == fl::kFormGrad && v != fl::kTile256x256 && v != fl::kTile128x128) continue;
+        const fl::GroupedTileShape &t = fl::kGroupedTiles[v];
+        double m;
+        if (form == fl::kFormGrad) {
+            m = (double)E * ((K + t.bm - 1) / t.bm);
+        } else {
+            const double runs = (double)(E < S ? E : S);
+            m = (double)S / t.bm + 0.5 * runs;
+            m = m > runs ? m : runs;
+        }
+        const double x = m * ((N + t.bn - 1) / t.bn) / (kCus * t.per_cu);
+        const double time = t.time * (x < 0.9 ? 1.0 : x + 0.5);
+        if (v == 0 || time < least) {
+            least = time;
+            best = v;
+        }
+    }
+    return best;
+}
+
 fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void *stream, const char *what) {
-    const int64_t bm = 64, bn = 64, threads = 256;
-    a.tiles_n = (int)((a.N + bn - 1) / bn);
-    const int64_t tiles_m = form == fl::kFormGrad ? a.E * (a.K ? (a.K + bm - 1) / bm : 1) : most_row_tiles(a.S, a.E, bm);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool dma = dtype != FL_F32;  // 16-bit operands
+    const int v = dma ? pick_variant(form, a.S, a.N, a.K, a.E) : 0;
+    const fl::GroupedTileShape t = dma ? fl::kGroupedTiles[v] : fl::GroupedTileShape{64, 64, 1, 1.0f};
+    a.tiles_n = (int)((a.N + t.bn - 1) / t.bn);
+    a.group = 4;
+    const int64_t tiles_m = form == fl::kFormGrad ? a.E * (((int64_t)a.K + t.bm - 1) / t.bm) : most_row_tiles(a.S, a.E, t.bm);
     const int64_t grid = tiles_m * a.tiles_n;
+    if (grid > kMaxDim) return fail(FL_ERR_UNSUPPORTED, "too many output tiles");
+    a.max_tiles = (int)grid;
+    if (form == fl::kFormGrad && a.dbias) {
+        if (dtype == FL_F32)
+            fl::launch_column_sum<FL_F32>(a, st);
+        else if (dtype == FL_F16)
+            fl::launch_column_sum<FL_F16>(a, st);
+        else
+            fl::launch_column_sum<FL_BF16>(a, st);
+        const fl_status s = check_launch(what);
+        if (s != FL_OK) return s;
+    }
     if (grid == 0) return FL_OK;
-    if (grid * threads > 0xffffffffll) return fail(FL_ERR_UNSUPPORTED, "too many output tiles");
-    pick_plain(dtype, form, act)(a, grid, static_cast<hipStream_t>(stream));
+    if (dma)
+        pick_dma(dtype, form, v)(a, act, grid < kCus * t.per_cu ? grid : kCus * t.per_cu, st);
+    else
+        fl::pick_grouped_f32(form, act)(a, grid, st);
     return check_launch(what);
 }
 
@@ -510,6 +562,8 @@ fl_status fl_grouped_weight_grad(const void *A, const void *G, const int32_t *of
     if (s != FL_OK) return s;
     if (dw_dtype != dtype && dw_dtype != FL_F32)
         return fail(FL_ERR_INVALID_ARG, "dW is in the operands' dtype or fp32 (got %d)", (int)dw_dtype);
+    if ((size_t)N * elem_size(dw_dtype) * 256 >= kTwoGiB)
+        return fail(FL_ERR_UNSUPPORTED, "N too large (256 rows of dW must span < 2 GiB)");
     const size_t es = elem_size(dtype), des = elem_size(dw_dtype);
     const Operand ops[] = {{"A", A, (size_t)S * K * es, es, false, N == 0, nullptr},
                            {"G", G, (size_t)S * N * es, es, false, false, nullptr},
