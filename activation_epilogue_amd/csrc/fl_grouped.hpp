@@ -32,6 +32,7 @@ struct GroupedArgs {
     int dw_f32;              // gradient: dW in fp32 (else in the dtype)
     int tiles_n;
     int group;               // row tiles per band of the tile order
+    int spread;              // nonzero: each XCD takes its share of every expert's tiles
     int max_tiles;           // limit on the tiles found from the offsets
 };
 

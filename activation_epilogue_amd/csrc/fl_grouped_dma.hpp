@@ -52,7 +52,6 @@ struct GroupedSide {
 
     i32x4_t rsrc;
     uint32_t off[COPIES];  // byte offset of the lane's chunk at k = 0, kOob outside the operand
-    int k0[KC ? 2 : 1];    // k within the stage of copies 0 (and 1)
     int frag;              // LDS address of the wave's first operand read within the side (KC: at chunk 0)
     int fk;                // KC: chunk xor of the lane's row
 
@@ -75,13 +74,11 @@ struct GroupedSide {
         }
     }
 
-    // Copy i's k within the stage: a KC copy's chunk depends on its row modulo
-    // 16, and copies are 8 rows apart; KR copies are 64 / CB k-rows apart.
-    __device__ __forceinline__ int k(int i) const {
-        if constexpr (KC)
-            return k0[i & 1];
-        else
-            return k0[0] + (64 / CB) * i;
+    // Copy i's k within the stage.
+    __device__ __forceinline__ static int k(int wave, int lane, int i) {
+        int row, chunk;
+        place(wave, lane, i, row, chunk);
+        return KC ? chunk * 8 : row;
     }
 
     // Operand reads for output rows (columns) w0 .. of the tile.
@@ -122,9 +119,10 @@ struct GroupedSide {
                                              const uint16_t *last) const {
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
-            if (off[i] == kOob || k(i) >= kleft) continue;
+            const int kc = k(wave, lane, i);
+            if (off[i] == kOob || kc >= kleft) continue;
             const int64_t rest = left - (int64_t)(off[i] >> 1);  // elements from the chunk's first to the end
-            const int valid = kleft - k(i);
+            const int valid = kleft - kc;
             const bool odd = rest < 8 && (rest & 1);
             if (!odd && (!KC || valid >= 8)) continue;
             FL_LDS char *p = s + (wave * COPIES + i) * 1024 + lane * 16;
@@ -167,6 +165,13 @@ struct GroupedTile {
     static_assert(NBUF >= 2 && SMEM <= 163840 && EPI_BYTES <= BUF_BYTES, "LDS");
     static_assert((TN & (TN - 1)) == 0 && (TM & (TM - 1)) == 0, "power-of-two wave tiles");
 
+    // A wave's place in the tile.  Waves w and w + 4 share a SIMD and differ in
+    // their row and, shifted by half the columns, their column: where half of
+    // the tile's rows or columns do not exist, each SIMD keeps one wave that
+    // works, alone and so at twice the rate.
+    __device__ __forceinline__ static int row_of(int wave) { return wave / WN; }
+    __device__ __forceinline__ static int col_of(int wave) { return (wave + (wave >> 2) * (WN / 2)) % WN; }
+
     struct Ops {
         SideA A;
         SideB B;
@@ -181,25 +186,30 @@ struct GroupedTile {
     struct Dst {  // LDS addresses of a wave's first copy of either operand
         uint32_t a, b;
     };
-    template <int I>
-    __device__ __forceinline__ static void copy_one(const Ops &o, int kt, Dst buf) {
+    // Copy I of stage kt (A's first).  CHECK: the stage may reach past the end
+    // of k, where zeros are copied; all stages issue the same copies, so that
+    // the waits are on constants.
+    template <int I, bool CHECK>
+    __device__ __forceinline__ static void copy_one(const Ops &o, int kt, Dst buf, int wave, int lane) {
         const int kleft = o.depth - kt * kStageK;
         if constexpr (I < SideA::COPIES) {
             const uint32_t so = FORM == kFormGrad ? 0 : (uint32_t)kt * (kStageK * 2);
-            lds_copy16(o.A.rsrc, o.A.k(I) < kleft ? o.A.off[I] : kOob, so, buf.a + I * 1024);
+            const bool ok = !CHECK || SideA::k(wave, lane, I) < kleft;
+            lds_copy16(o.A.rsrc, ok ? o.A.off[I] : kOob, so, buf.a + I * 1024);
         } else {
             constexpr int i = I - SideA::COPIES;
             const uint32_t so = FORM == kFormGrad  ? 0
                                 : FORM == kFormBwd ? (uint32_t)kt * (kStageK * 2)
                                                    : (uint32_t)kt * (uint32_t)(kStageK * 2) * (uint32_t)o.ldb;
-            lds_copy16(o.B.rsrc, o.B.k(i) < kleft ? o.B.off[i] : kOob, so, buf.b + i * 1024);
+            const bool ok = !CHECK || SideB::k(wave, lane, i) < kleft;
+            lds_copy16(o.B.rsrc, ok ? o.B.off[i] : kOob, so, buf.b + i * 1024);
         }
     }
-    template <int C0, int C1>
-    __device__ __forceinline__ static void copy_range(const Ops &o, int kt, Dst buf) {
+    template <int C0, int C1, bool CHECK>
+    __device__ __forceinline__ static void copy_range(const Ops &o, int kt, Dst buf, int wave, int lane) {
         if constexpr (C0 < C1) {
-            copy_one<C0>(o, kt, buf);
-            copy_range<C0 + 1, C1>(o, kt, buf);
+            copy_one<C0, CHECK>(o, kt, buf, wave, lane);
+            copy_range<C0 + 1, C1, CHECK>(o, kt, buf, wave, lane);
         }
     }
     __device__ __forceinline__ static Dst copy_base(uint32_t lds, int b, int wave) {
@@ -263,17 +273,20 @@ struct GroupedTile {
     }
 
     // One block: the MFMAs on `use`, the reads of block kk of `s` into `fill`
-    // and, if COPY, the copies of stage kt into `buf` spread over them.
-    template <int I, bool COPY>
+    // and the copies (0 none, 1 unchecked, 2 checked) of stage kt into `buf`
+    // spread over them.
+    template <int I, int COPY>
     __device__ __forceinline__ static void block(const Ops &o, const FL_LDS char *s, int kk, int kt, Dst buf,
-                                                 const Frags &use, Frags &fill, f32x4_t (&acc)[NRB][NI]) {
+                                                 int wave, int lane, const Frags &use, Frags &fill,
+                                                 f32x4_t (&acc)[NRB][NI]) {
         if constexpr (I < SLOTS) {
             mma<I>(use, acc);
-            if constexpr (COPY)
-                copy_range<(I * COPIES + SLOTS - 1) / SLOTS, ((I + 1) * COPIES + SLOTS - 1) / SLOTS>(o, kt, buf);
+            if constexpr (COPY != 0)
+                copy_range<(I * COPIES + SLOTS - 1) / SLOTS, ((I + 1) * COPIES + SLOTS - 1) / SLOTS, COPY == 2>(
+                    o, kt, buf, wave, lane);
             read_range<I * READS / SLOTS, (I + 1) * READS / SLOTS>(o, s, kk, fill);
             __builtin_amdgcn_sched_barrier(0);
-            block<I + 1, COPY>(o, s, kk, kt, buf, use, fill, acc);
+            block<I + 1, COPY>(o, s, kk, kt, buf, wave, lane, use, fill, acc);
         }
     }
 
@@ -304,34 +317,43 @@ struct GroupedTile {
     // Stage kt in LDS buffer `buf`; its block 0 operands are in f[0].
     template <bool TAIL>
     __device__ __forceinline__ static void stage(const GroupedArgs &a, Ops &o, const FL_LDS char *lds, uint32_t addr,
-                                                 int kt, int nk, int buf, int wave, Frags (&f)[2],
+                                                 int kt, int nk, int buf, int wave, int lane, Frags (&f)[2],
                                                  f32x4_t (&acc)[NRB][NI]) {
-        block<0, false>(o, lds + buf * BUF_BYTES, 1, 0, Dst{}, f[0], f[1], acc);
+        block<0, 0>(o, lds + buf * BUF_BYTES, 1, 0, Dst{}, wave, lane, f[0], f[1], acc);
         const FL_LDS char *nxt = lds + (buf + 1 == NBUF ? 0 : buf + 1) * BUF_BYTES;
+        turn<TAIL>(a, o, nxt, kt, nk, wave, lane);
+        block<0, TAIL ? 2 : 1>(o, nxt, 0, kt + NBUF, copy_base(addr, buf, wave), wave, lane, f[1], f[0], acc);
+    }
+
+    // Between the blocks of stage kt: stage kt+1 has landed (in `nxt`), put
+    // right if it is the last, and every wave is done with stage kt's buffer.
+    template <bool TAIL>
+    __device__ __forceinline__ static void turn(const GroupedArgs &a, Ops &o, const FL_LDS char *nxt, int kt, int nk,
+                                                int wave, int lane) {
         if constexpr (TAIL) {
             if (ragged(a) && kt + 2 == nk) {
                 wait_vm<(NBUF - 2) * COPIES>();  // the last stage has landed
-                fix_tail(a, o, kt + 1, NBUF - 2, wave, threadIdx.x & 63, (FL_LDS char *)nxt);
+                fix_tail(a, o, kt + 1, NBUF - 2, wave, lane, (FL_LDS char *)nxt);
             }
         }
         wait_vm<(NBUF - 2) * COPIES>();
         __syncthreads();
         next_stage(o);
-        block<0, true>(o, nxt, 0, kt + NBUF, copy_base(addr, buf, wave), f[1], f[0], acc);
     }
 
     // Copies of stages B0 .. B1-1 into the buffers of their numbers.
     template <int B0, int B1>
-    __device__ __forceinline__ static void prefetch(Ops &o, int wave, uint32_t addr) {
+    __device__ __forceinline__ static void prefetch(Ops &o, int wave, int lane, uint32_t addr) {
 #pragma unroll
         for (int b = B0; b < B1; ++b) {
             if (b > 0) next_stage(o);
-            copy_range<0, COPIES>(o, b, copy_base(addr, b, wave));
+            copy_range<0, COPIES, true>(o, b, copy_base(addr, b, wave), wave, lane);
         }
     }
 
-    // The tile's product; stages 0 .. NBUF-1 are on their way.
-    __device__ __forceinline__ static void product(const GroupedArgs &a, Ops &o, int wave, int lane,
+    // The tile's product; stages 0 .. NBUF-1 are on their way.  An idle wave
+    // (none of its outputs exist) only does its share of the copies.
+    __device__ __forceinline__ static void product(const GroupedArgs &a, Ops &o, bool idle, int wave, int lane,
                                                    const FL_LDS char *lds, uint32_t addr, f32x4_t (&acc)[NRB][NI]) {
 #pragma unroll
         for (int mi = 0; mi < NRB; ++mi)
@@ -342,18 +364,31 @@ struct GroupedTile {
         wait_vm<(NBUF - 1) * COPIES>();
         if (nk == 1 && ragged(a)) fix_tail(a, o, 0, NBUF - 1, wave, lane, (FL_LDS char *)lds);
         __syncthreads();
-        Frags f[2];
-        read_range<0, READS>(o, lds, 0, f[0]);
         int buf = 0, kt = 0;
+        if (idle) {
 #pragma unroll 1
-        for (; kt + 2 < nk; ++kt) {
-            stage<false>(a, o, lds, addr, kt, nk, buf, wave, f, acc);
-            buf = buf + 1 == NBUF ? 0 : buf + 1;
-        }
+            for (; kt < nk; ++kt) {
+                asm volatile("" : "+v"(lane));
+                const int next = buf + 1 == NBUF ? 0 : buf + 1;
+                turn<true>(a, o, lds + next * BUF_BYTES, kt, nk, wave, lane);
+                copy_range<0, COPIES, true>(o, kt + NBUF, copy_base(addr, buf, wave), wave, lane);
+                buf = next;
+            }
+        } else {
+            Frags f[2];
+            read_range<0, READS>(o, lds, 0, f[0]);
 #pragma unroll 1
-        for (; kt < nk; ++kt) {
-            stage<true>(a, o, lds, addr, kt, nk, buf, wave, f, acc);
-            buf = buf + 1 == NBUF ? 0 : buf + 1;
+            for (; kt < nk - (NBUF + 1); ++kt) {  // stages that copy a whole stage
+                stage<false>(a, o, lds, addr, kt, nk, buf, wave, lane, f, acc);
+                buf = buf + 1 == NBUF ? 0 : buf + 1;
+            }
+            int lt = lane;
+#pragma unroll 1
+            for (; kt < nk; ++kt) {
+                asm volatile("" : "+v"(lt));  // what the checks derive from the lane is computed here, not kept
+                stage<true>(a, o, lds, addr, kt, nk, buf, wave, lt, f, acc);
+                buf = buf + 1 == NBUF ? 0 : buf + 1;
+            }
         }
         // the look-ahead copies past the end land before the LDS is used again
         wait_vm<0>();
@@ -420,7 +455,7 @@ struct GroupedTile {
                                                     const f32x4_t (&acc)[NRB][NI], FL_LDS char *lds) {
         const int rows = t.rows, n0 = t.tn * BN;
         const int64_t row0 = FORM == kFormGrad ? (int64_t)t.e * a.K + t.m0 : t.m0;
-        const int wm = wave / WN, wn = wave % WN;
+        const int wm = row_of(wave), wn = col_of(wave);
         constexpr int CPR = TN / 8, RPP = 64 / CPR, PASSES = 16 / RPP;  // lanes per row, rows and passes per row block
         const int es = FORM == kFormGrad && a.dw_f32 ? 4 : 2;
         const int64_t org = row0 * a.N + n0;
@@ -500,31 +535,33 @@ struct GroupedTile {
         }
     }
 
-    // Tile number b of n.  Workgroups of one XCD (b modulo 8) share a run of
-    // consecutive tiles, which belong to few experts, and within an expert to
-    // bands of a.group row tiles swept column by column: the XCD's L2 serves
-    // their shared operands.
+    // Tile number b of n.  Workgroups of one XCD (b modulo 8) take consecutive
+    // tiles, so that its L2 serves their shared operands: of the list of all
+    // experts' tiles or, with a.spread, of every expert's by itself.  An
+    // expert's tiles are ordered in bands of a.group row tiles swept column by
+    // column.
     __device__ __forceinline__ static bool find(const GroupedArgs &a, int b, int n, Tile &t) {
         if (b >= n) return false;
-        const int pid = xcd_logical(b, n);
         int m;
         if constexpr (FORM == kFormGrad) {
-            const int per = (a.K + BM - 1) / BM;
-            t.e = pid / (per * a.tiles_n);
+            // (an expert's tiles cost as much as it has rows, so always spread)
+            const int tiles_m = (a.K + BM - 1) / BM, per = tiles_m * a.tiles_n;
+            t.e = b / per;
             t.lo = run_bound(a, t.e);
             const int hi = run_bound(a, t.e + 1);
             t.depth = hi > t.lo ? hi - t.lo : 0;
-            grouped_tile(pid - t.e * per * a.tiles_n, per, a.tiles_n, a.group, m, t.tn);
+            grouped_tile(xcd_logical(b - t.e * per, per), tiles_m, a.tiles_n, a.group, m, t.tn);
             t.m0 = m * BM;
             t.rows = a.K - t.m0 < BM ? a.K - t.m0 : BM;
         } else {
+            const int pid = a.spread ? b : xcd_logical(b, n);
             const int q = pid / a.tiles_n;
             const RunTile r = find_run_tile(a, BM, q);
             if (r.e < 0) return false;
             const int cnt = (r.hi - r.lo + BM - 1) / BM;
             const int local = pid - (q - r.m) * a.tiles_n;
             if (r.m < 0 || r.m >= cnt || local < 0) return false;  // (offsets that are no plan's)
-            grouped_tile(local, cnt, a.tiles_n, a.group, m, t.tn);
+            grouped_tile(a.spread ? xcd_logical(local, cnt * a.tiles_n) : local, cnt, a.tiles_n, a.group, m, t.tn);
             if (m < 0 || m >= cnt || t.tn < 0 || t.tn >= a.tiles_n) return false;
             t.e = r.e;
             t.lo = r.lo;
@@ -567,7 +604,6 @@ struct GroupedTile {
             SideA::place(wave, lane, i, r, c);
             if constexpr (FORM == kFormGrad) {
                 o.A.off[i] = c * 8 < t.rows ? (uint32_t)(r * o.lda + c * 8) * 2 : kOob;
-                if (i == 0) o.A.k0[0] = r;
             } else {
                 int64_t row = r;
                 bool ok = r < t.rows;
@@ -576,7 +612,6 @@ struct GroupedTile {
                     ok = ok && row >= 0 && row < a.A_rows;
                 }
                 o.A.off[i] = ok ? ((uint32_t)row * (uint32_t)o.lda + c * 8) * 2 : kOob;
-                if (i < 2) o.A.k0[i] = c * 8;
             }
         }
 #pragma unroll
@@ -585,10 +620,8 @@ struct GroupedTile {
             SideB::place(wave, lane, i, r, c);
             if constexpr (FORM == kFormBwd) {
                 o.B.off[i] = n0 + r < a.N ? (uint32_t)(r * o.ldb + c * 8) * 2 : kOob;
-                if (i < 2) o.B.k0[i] = c * 8;
             } else {
                 o.B.off[i] = n0 + c * 8 < a.N ? (uint32_t)(r * o.ldb + c * 8) * 2 : kOob;
-                if (i == 0) o.B.k0[0] = r;
             }
         }
     }
@@ -607,27 +640,32 @@ struct GroupedTile {
         Tile t;
         if (!find(a, b, n, t)) return;
         Ops o;
-        o.A.set_frag((wave / WN) * TM, lane);
-        o.B.set_frag((wave % WN) * TN, lane);
+        o.A.set_frag(row_of(wave) * TM, lane);
+        o.B.set_frag(col_of(wave) * TN, lane);
         setup(a, t, wave, lane, o);
-        prefetch<0, NBUF - 1>(o, wave, addr);
+        prefetch<0, NBUF - 1>(o, wave, lane, addr);
         for (;;) {
-            prefetch<NBUF - 1, NBUF>(o, wave, addr);
+            // addresses of a tile come from a copy of the lane made for it, so
+            // that none is kept across its K loop
+            int lo = lane;
+            asm volatile("" : "+v"(lo));
+            prefetch<NBUF - 1, NBUF>(o, wave, lo, addr);
             b += gridDim.x;
             Tile next;
             const bool more = find(a, b, n, next);
             f32x4_t acc[NRB][NI];
-            product(a, o, wave, lane, lds, addr, acc);
-            // addresses of the next tile and of the epilogue come from a copy
-            // of the lane made here, so that they are not kept across K loops
-            int le = lane;
+            const bool idle = row_of(wave) * TM >= t.rows || t.tn * BN + col_of(wave) * TN >= a.N;
+            product(a, o, idle, wave, lo, lds, addr, acc);
+            int le = lane;  // (and so for the next tile's and the epilogue's)
             asm volatile("" : "+v"(le));
             if (more) {
                 setup(a, next, wave, le, o);
-                prefetch<0, NBUF - 1>(o, wave, addr);
+                prefetch<0, NBUF - 1>(o, wave, le, addr);
             }
             FL_LDS char *epi = lds + (NBUF - 1) * BUF_BYTES;
-            if (FORM == kFormGrad || act == FL_ACT_NONE)
+            if (idle)
+                ;
+            else if (FORM == kFormGrad || act == FL_ACT_NONE)
                 epilogue<FL_ACT_NONE>(a, t, wave, le, acc, epi);
             else if (act == FL_ACT_RELU)
                 epilogue<FL_ACT_RELU>(a, t, wave, le, acc, epi);
