@@ -5,8 +5,8 @@ elementwise kernels), one unit of fused GEMM kernels per dtype, one of
 quantized-output kernels per 16-bit dtype, one of FP8-input kernels per
 16-bit output dtype and one of backward-epilogue kernels per 16-bit dtype;
 and, for the routed experts, the host/ABI unit (with the router, plan and
-row-movement kernels), one unit of the experts' products per dtype and one
-of their direct-to-LDS tiles per 16-bit dtype and form.
+row-movement kernels) and one unit of the experts' products per dtype and
+form.
 Every device compile carries -Xclang -target-feature -Xclang -packed-fp32-ops so
 that no packed fp32 instructions are generated.
 """
@@ -41,11 +41,8 @@ UNITS = [
     ("fl_bwd_inst.hip", ["-DFL_INST_DTYPE=1"]),
     ("fl_bwd_inst.hip", ["-DFL_INST_DTYPE=2"]),
     ("fl_moe.hip", []),
-    ("fl_grouped_inst.hip", ["-DFL_INST_DTYPE=0"]),
-    ("fl_grouped_inst.hip", ["-DFL_INST_DTYPE=1"]),
-    ("fl_grouped_inst.hip", ["-DFL_INST_DTYPE=2"]),
-    *(("fl_grouped_dma_inst.hip", [f"-DFL_INST_FORM={form}", f"-DFL_INST_DTYPE={dt}"])
-      for form in (0, 1, 2) for dt in (1, 2)),
+    *(("fl_grouped_inst.hip", [f"-DFL_INST_FORM={form}", f"-DFL_INST_DTYPE={dt}"])
+      for form in (0, 1, 2) for dt in (0, 1, 2)),
 ]
 
 

@@ -93,123 +93,6 @@ __device__ __forceinline__ RunTile find_run_tile(const GroupedArgs &a, int bm, i
     return t;
 }
 
-// ------------------------------------------------------------- fp32 products
-
-// 64x64 tiles, 4 waves of one 32x32 block each (v_mfma_f32_32x32x2_f32), K
-// stages of 32 values loaded by elements into LDS.
-template <int FORM, int ACT>
-struct GroupedF32 {
-    static constexpr int BM = 64, BN = 64, BK = 32;
-    static constexpr int ROW = BK + 4;  // padded LDS row
-    static constexpr int THREADS = 256;
-
-    __device__ static void run(const GroupedArgs &a, float *As, float *Bs) {
-        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-        const int wm = wave >> 1, wn = wave & 1;
-        const float *A = static_cast<const float *>(a.A);
-        const float *B = static_cast<const float *>(a.B);
-        int e, lo, hi, m0;  // m0: first row (of the product) of the tile; its rows end at mend
-        const int n0 = (int)(blockIdx.x % a.tiles_n) * BN;
-        int mend, depth;
-        if constexpr (FORM == kFormGrad) {
-            const int per = (a.K + BM - 1) / BM;
-            const int q = blockIdx.x / a.tiles_n;
-            e = q / per;
-            lo = run_bound(a, e);
-            hi = run_bound(a, e + 1);
-            m0 = (q % per) * BM;
-            mend = a.K;
-            depth = hi > lo ? hi - lo : 0;
-        } else {
-            const RunTile t = find_run_tile(a, BM, blockIdx.x / a.tiles_n);
-            if (t.e < 0) return;
-            e = t.e;
-            lo = t.lo;
-            hi = t.hi;
-            m0 = lo + t.m * BM;
-            mend = hi;
-            depth = a.K;
-        }
-        f32x16_t acc;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-        for (int k0 = 0; k0 < depth; k0 += BK) {
-#pragma unroll
-            for (int i = 0; i < BM * BK / THREADS; ++i) {
-                const int q = tid + i * THREADS;
-                // consecutive threads along the operand's contiguous dimension
-                const int r = FORM == kFormGrad ? q % BM : q / BK, k = FORM == kFormGrad ? q / BM : q % BK;
-                float v = 0.0f;
-                if (k0 + k < depth && m0 + r < mend) {
-                    if constexpr (FORM == kFormGrad) {
-                        v = A[(int64_t)(lo + k0 + k) * a.K + m0 + r];
-                    } else {
-                        const int64_t row = FORM == kFormFwd && a.index ? a.index[m0 + r] : m0 + r;
-                        if (row >= 0 && row < a.A_rows) v = A[row * a.K + k0 + k];
-                    }
-                }
-                As[r * ROW + k] = v;
-            }
-#pragma unroll
-            for (int i = 0; i < BN * BK / THREADS; ++i) {
-                const int q = tid + i * THREADS;
-                const int n = FORM == kFormBwd ? q / BK : q % BN, k = FORM == kFormBwd ? q % BK : q / BN;
-                float v = 0.0f;
-                if (k0 + k < depth && n0 + n < a.N) {
-                    if constexpr (FORM == kFormFwd)
-                        v = B[((int64_t)e * a.K + k0 + k) * a.N + n0 + n];
-                    else if constexpr (FORM == kFormBwd)
-                        v = B[((int64_t)e * a.N + n0 + n) * a.K + k0 + k];
-                    else
-                        v = B[(int64_t)(lo + k0 + k) * a.N + n0 + n];
-                }
-                Bs[n * ROW + k] = v;
-            }
-            __syncthreads();
-            const int lr = lane & 31, lg = lane >> 5;
-#pragma unroll
-            for (int k = 0; k < BK; k += 2)
-                acc = __builtin_amdgcn_mfma_f32_32x32x2f32(Bs[(wn * 32 + lr) * ROW + k + lg],
-                                                           As[(wm * 32 + lr) * ROW + k + lg], acc, 0, 0, 0);
-            __syncthreads();
-        }
-        // lane l: row l%32, columns q*8 + (l/32)*4 + 0..3 of its wave's block
-        const int row = m0 + wm * 32 + (lane & 31);
-        if (row >= mend) return;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int col = n0 + wn * 32 + q * 8 + (lane >> 5) * 4 + i;
-                if (col >= a.N) continue;
-                const float s = acc[q * 4 + i];
-                if constexpr (FORM == kFormGrad) {
-                    static_cast<float *>(a.out)[((int64_t)e * a.K + row) * a.N + col] = s;
-                } else {
-                    const int64_t o = (int64_t)row * a.N + col;
-                    const float y = ACT == FL_ACT_GLU ? static_cast<const float *>(a.Y)[o] : 0.0f;
-                    if constexpr (FORM == kFormFwd) {
-                        const float x = s + (a.bias ? static_cast<const float *>(a.bias)[(int64_t)e * a.N + col] : 0.0f);
-                        if (a.out2) static_cast<float *>(a.out2)[o] = x;
-                        static_cast<float *>(a.out)[o] = activate<ACT>(x, y);
-                    } else {
-                        const float xs = a.X ? static_cast<const float *>(a.X)[o] : 0.0f;
-                        static_cast<float *>(a.out)[o] = s * activate_grad<ACT>(xs, y);
-                        if constexpr (ACT == FL_ACT_GLU) static_cast<float *>(a.out2)[o] = s * xs;
-                    }
-                }
-            }
-        }
-    }
-};
-
-template <int FORM, int ACT>
-__global__ void __launch_bounds__(256) grouped_f32_kernel(GroupedArgs a) {
-    using T = GroupedF32<FORM, ACT>;
-    __shared__ __attribute__((aligned(16))) float As[T::BM * T::ROW], Bs[T::BN * T::ROW];
-    T::run(a, As, Bs);
-}
-
 // ----------------------------------------------------- the bias gradient
 
 // dbias[e] = the sum of expert e's rows of G: a block sums 128 columns of one
@@ -266,26 +149,25 @@ __global__ void __launch_bounds__(256) grouped_column_sum_kernel(GroupedArgs a) 
     }
 }
 
-typedef void (*grouped_launcher)(const GroupedArgs &, int64_t grid, hipStream_t);
-
-// The tiles of grouped_dma_kernel (fl_grouped_dma.hpp), for 16-bit operands.
-// time: of one workgroup per slot (256 CUs x per_cu), relative to 256x256 tiles
-// at large sizes (8192x2 rows of 8 experts, K 4096, N 14336: 1030, 950, 810, 605
-// and 370 TFLOP/s).
+// The tiles of grouped_dma_kernel (fl_grouped_dma.hpp).  time: of a round (one
+// workgroup in every slot, 256 CUs x per_cu), in units of the widest tile's at
+// large sizes (8192x2 rows of 8 experts, K 4096, N 14336: 1030, 950, 810, 605
+// and 370 TFLOP/s).  fp32 has one tile: 64x64 reaches 130 TFLOP/s at 4096x2
+// rows, K 2048, N 4096 (128x128: 114 to 134, and half as much where there are
+// few tiles).
 struct GroupedTileShape {
     int bm, bn, per_cu;
     float time;
+    bool grad;  // compiled for the gradient too
 };
-enum GroupedVariant { kTile256x256 = 0, kTile256x128, kTile128x128, kTile64x128, kTile32x128, kGroupedVariants };
+enum GroupedVariant { kTile256x256 = 0, kTile256x128, kTile128x128, kTile64x128, kTile32x128, kTileF32, kGroupedVariants };
 constexpr GroupedTileShape kGroupedTiles[kGroupedVariants] = {
-    {256, 256, 1, 1.0f}, {256, 128, 1, 0.54f}, {128, 128, 2, 0.64f}, {64, 128, 2, 0.425f}, {32, 128, 2, 0.35f}};
-typedef void (*grouped_dma_launcher)(const GroupedArgs &, int act, int64_t grid, hipStream_t);
-// Compiled one dtype and form to a unit; the gradient has the first and the third tile only.
+    {256, 256, 1, 1.0f, true}, {256, 128, 1, 0.54f, false}, {128, 128, 2, 0.64f, true},
+    {64, 128, 2, 0.425f, false}, {32, 128, 2, 0.35f, false}, {64, 64, 3, 1.0f, true}};
+typedef void (*grouped_launcher)(const GroupedArgs &, int act, int64_t grid, hipStream_t);
+// One dtype and form to a compiled unit.
 template <int DT, int FORM>
-grouped_dma_launcher pick_grouped_dma_form(int variant);
-
-// Launcher of the fp32 kernel for (form, act).
-grouped_launcher pick_grouped_f32(int form, int act);
+grouped_launcher pick_grouped(int variant);
 template <int DT>
 void launch_column_sum(const GroupedArgs &a, hipStream_t s);
 

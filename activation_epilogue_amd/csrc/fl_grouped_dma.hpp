@@ -1,12 +1,13 @@
-// fl_grouped_dma.hpp -- the experts' products on 16-bit operands: tiles fed by
-// direct-to-LDS loads through a ring of K stages, 16x16x32 MFMA blocks.
+// fl_grouped_dma.hpp -- the experts' products: tiles fed by direct-to-LDS loads
+// through a ring of K stages, MFMA blocks of 16x16 outputs.
 //
 // The three forms of fl_grouped.hpp differ in how an operand lies in memory:
 //   forward   A rows K-contiguous (optionally read through an index), B[e] N-contiguous
 //   backward  G rows K-contiguous, W[e] rows K-contiguous
 //   gradient  A and G both with the summed dimension (the rows of the run) outermost
-// so an operand's tile is either a set of rows of 64 consecutive k (KC) or 64
-// k-rows of consecutive columns (KR), and the tile code is the same for all.
+// so an operand's tile is either a set of rows of consecutive k (KC) or k-rows
+// of consecutive columns (KR), and the tile code is the same for all.  A stage
+// is 128 bytes of k: 64 k of 16-bit operands, 32 of fp32.
 //
 //   * Copies: one buffer load with the LDS bit moves 64 x 16 bytes into 1 KB of
 //     LDS; the bank swizzle is applied on the global side.  Rows outside the
@@ -14,8 +15,11 @@
 //     hardware's range check turns into zeros, so a partial tile costs no
 //     traffic for what it lacks.  Pointers need element alignment only.
 //   * MFMA operands: KC tiles are read with 16-byte reads, KR tiles with the
-//     transposing 8-byte read (two for 8 consecutive k of one column).
-//   * A stage is 64 k: two blocks of MFMAs.  The reads of the next block are
+//     transposing 8-byte read (two for 8 consecutive k of one column; fp32:
+//     four 4-byte reads of consecutive columns).  A 16-byte read holds 4 fp32
+//     k, which four 16x16x4 MFMAs take one each: MFMA j sums k = 4*g + j over
+//     the lane groups g, in both operands alike.
+//   * A stage is two blocks of MFMAs.  The reads of the next block are
 //     slotted between the MFMAs of the current one; the one barrier per stage
 //     stands before the second block, which also issues the copies of the
 //     stage NBUF ahead into the buffer that the barrier has freed.
@@ -29,26 +33,28 @@
 
 namespace fl {
 
-constexpr int kStageK = 64;  // k per stage
 
 // A 16-bit load and its wait in one asm block: a load that the compiler tracks,
 // on a branch of the K loop, would make it drain all copies in flight before
 // later LDS reads.
-__device__ __forceinline__ uint32_t load_u16_at(const uint16_t *p) {
+__device__ __forceinline__ uint32_t load_u16_at(const void *p) {
     uint32_t v;
     asm volatile("global_load_ushort %0, %1, off\n\ts_waitcnt vmcnt(0)" : "=&v"(v) : "v"(p) : "memory");
     return v & 0xffffu;
 }
 
 // One operand's tile: R rows (KC) or R columns (KR), copied by WAVES waves.
-template <int R, int WAVES, bool KC>
+template <int DT, int R, int WAVES, bool KC>
 struct GroupedSide {
-    static constexpr int BYTES = R * kStageK * 2;
+    static constexpr int ES = Io<DT>::size, EPC = 16 / ES;  // bytes of an element, elements of a chunk
+    static constexpr int KS = 128 / ES;                     // k per stage
+    static constexpr int ROW = R * ES;                      // KR: bytes of a k-row
+    static constexpr int BYTES = R * 128;
     static constexpr int COPIES = R / (8 * WAVES);  // per wave and stage
-    static constexpr int CB = R / 8;                // KR: 16-byte chunks per k-row
-    static constexpr int PARTS = KC ? 1 : 2;        // LDS reads per MFMA operand
+    static constexpr int CB = ROW / 16;             // KR: chunks per k-row
+    static constexpr int PARTS = KC ? 1 : ES;       // LDS reads per MFMA operand
     static_assert(COPIES >= 1 && COPIES * 8 * WAVES == R, "whole copies");
-    static_assert(KC || R == 128 || R == 256, "KR swizzle");
+    static_assert(KC || CB == 16 || CB == 32, "KR swizzle");
 
     i32x4_t rsrc;
     uint32_t off[COPIES];  // byte offset of the lane's chunk at k = 0, kOob outside the operand
@@ -56,11 +62,16 @@ struct GroupedSide {
     int fk;                // KC: chunk xor of the lane's row
 
     // 16-byte reads of 16 consecutive rows at one chunk per 16 lanes fall on
-    // distinct banks (KC; rows of 128 bytes)
+    // distinct banks (KC)
     __device__ __forceinline__ static int fa(int r) { return ((r >> 1) ^ ((r & 1) << 2)) & 7; }
-    // the 4 k-rows (and those 8 further) of a transposing read fall on
-    // distinct banks (KR; rows of 256 or 512 bytes); always even
-    __device__ __forceinline__ static int fb(int r) { return ((0xAC60 >> (4 * (r & 3))) & 0xF) ^ ((r >> 2) & 2); }
+    // KR: the 4 k-rows (and those 8 further) of a transposing read, or the
+    // k-rows 4 apart of a 4-byte read, fall on distinct banks; always even
+    __device__ __forceinline__ static int fb(int r) {
+        if constexpr (ES == 4)
+            return r & 12;
+        else
+            return ((0xAC60 >> (4 * (r & 3))) & 0xF) ^ ((r >> 2) & 2);
+    }
 
     // Lane's place in copy i: its row (KC) or k-row (KR), and its chunk.
     __device__ __forceinline__ static void place(int wave, int lane, int i, int &row, int &chunk) {
@@ -78,53 +89,59 @@ struct GroupedSide {
     __device__ __forceinline__ static int k(int wave, int lane, int i) {
         int row, chunk;
         place(wave, lane, i, row, chunk);
-        return KC ? chunk * 8 : row;
+        return KC ? chunk * EPC : row;
     }
 
     // Operand reads for output rows (columns) w0 .. of the tile.
     __device__ __forceinline__ void set_frag(int w0, int lane) {
         const int g = lane >> 4, i = lane & 15;
+        fk = 0;
         if constexpr (KC) {
             frag = (w0 + i) * 128;
             fk = g ^ fa(i);  // w0 is a multiple of 16; block kk flips bit 2
-        } else {
+        } else if constexpr (ES == 2) {
             const int rk = g * 8 + (i >> 2), n = w0 + 4 * (i & 3);
-            frag = rk * (R * 2) + (((n >> 3) ^ fb(rk)) * 16) + ((n >> 2) & 1) * 8;
-            fk = 0;
+            frag = rk * ROW + (((n >> 3) ^ fb(rk)) * 16) + ((n >> 2) & 1) * 8;
+        } else {
+            const int n = w0 + i;
+            frag = g * 4 * ROW + (((n >> 2) ^ fb(g * 4)) * 16) + (n & 3) * 4;
         }
     }
-    // Read P of the operand of 16-row block b at MFMA block kk.
+    // Read P of the operand of 16-row block b at MFMA block kk.  (KR: the
+    // wave's first column is a multiple of its columns, a power of two, so
+    // that block b is one xor away.)
     template <int P>
     __device__ __forceinline__ void read(const FL_LDS char *s, int b, int kk, i32x2_t (&v)[2]) const {
         if constexpr (KC) {
             const u32x4_t t = *(const FL_LDS u32x4_t *)(s + frag + ((fk ^ (kk * 4)) * 16) + b * (16 * 128));
             v[0] = i32x2_t{(int)t[0], (int)t[1]};
             v[1] = i32x2_t{(int)t[2], (int)t[3]};
+        } else if constexpr (ES == 2) {
+            v[P] = __builtin_bit_cast(i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((
+                                                   FL_LDS s16x4_t *)(s + (frag ^ (b * 32)) + (kk * 32 + P * 4) * ROW)));
         } else {
-            // the wave's first column is a multiple of its columns, a power of two: block b is one xor away
-            v[P] = __builtin_bit_cast(
-                i32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                             (FL_LDS s16x4_t *)(s + (frag ^ (b * 32)) + (kk * 32 + P * 4) * (R * 2))));
+            v[P >> 1][P & 1] = *(const FL_LDS int *)(s + (frag ^ (b * 64)) + (kk * 16 + P) * ROW);
         }
     }
 
-    // Puts right what 16-byte copies get wrong in the last stage (kleft <= 64
-    // k of it exist), on the chunks that this wave copied, after they landed:
-    //  * the range check works on whole dwords, so an odd last element of the
-    //    operand reads as zero: it is loaded again by itself;
+    // Puts right what 16-byte copies get wrong in the last stage (kleft k of it
+    // exist), on the chunks that this wave copied, after they landed:
+    //  * the range check works on whole dwords, so an odd last 16-bit element
+    //    of the operand reads as zero: it is loaded again by itself;
     //  * a KC chunk that crosses the end of k holds values of the next row.
     // left: elements from the stage's origin to the end of the operand; last:
     // its last element.
     __device__ __forceinline__ void fix_tail(FL_LDS char *s, int wave, int lane, int64_t left, int kleft,
-                                             const uint16_t *last) const {
+                                             const void *last) const {
+        if (ES == 4 && !KC) return;
 #pragma unroll
         for (int i = 0; i < COPIES; ++i) {
             const int kc = k(wave, lane, i);
             if (off[i] == kOob || kc >= kleft) continue;
-            const int64_t rest = left - (int64_t)(off[i] >> 1);  // elements from the chunk's first to the end
+            const int64_t rest = left - (int64_t)(off[i] / ES);  // elements from the chunk's first to the end
             const int valid = kleft - kc;
-            const bool odd = rest < 8 && (rest & 1);
-            if (!odd && (!KC || valid >= 8)) continue;
+            const bool odd = ES == 2 && rest < 8 && (rest & 1);
+            if (!odd && (!KC || valid >= EPC)) continue;
             FL_LDS char *p = s + (wave * COPIES + i) * 1024 + lane * 16;
             u32x4_t v = *(FL_LDS u32x4_t *)p;
             if (odd) {
@@ -136,8 +153,8 @@ struct GroupedSide {
             if constexpr (KC) {
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                    const int n = valid - 2 * d;
-                    v[d] &= n >= 2 ? 0xffffffffu : n == 1 ? 0xffffu : 0u;
+                    const int n = valid * ES - 4 * d;  // bytes of dword d that exist
+                    v[d] &= n >= 4 ? 0xffffffffu : n == 2 ? 0xffffu : 0u;
                 }
             }
             *(FL_LDS u32x4_t *)p = v;
@@ -153,11 +170,13 @@ struct GroupedTile {
     static constexpr int BM = BM_, BN = BN_, NBUF = NBUF_;
     static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
     static constexpr int TM = BM / WM, TN = BN / WN, NRB = TM / 16, NI = TN / 16;
-    using SideA = GroupedSide<BM, WAVES, FORM != kFormGrad>;
-    using SideB = GroupedSide<BN, WAVES, FORM == kFormBwd>;
+    using SideA = GroupedSide<DT, BM, WAVES, FORM != kFormGrad>;
+    using SideB = GroupedSide<DT, BN, WAVES, FORM == kFormBwd>;
+    static constexpr int ES = SideA::ES, EPC = SideA::EPC, KS = SideA::KS;
+    static constexpr int MPB = ES == 4 ? 4 : 1;  // MFMAs per pair of operand reads
     static constexpr int BUF_BYTES = SideA::BYTES + SideB::BYTES;
     static constexpr int COPIES = SideA::COPIES + SideB::COPIES;
-    static constexpr int SLOTS = NRB * NI;
+    static constexpr int SLOTS = NRB * NI * MPB;
     static constexpr int RA = SideA::PARTS, RB = SideB::PARTS, READS = NRB * RA + NI * RB;
     static constexpr int EPI_ROW = TN * 4 + 16;
     static constexpr int EPI_BYTES = WAVES * 16 * EPI_ROW;
@@ -191,16 +210,16 @@ struct GroupedTile {
     // the waits are on constants.
     template <int I, bool CHECK>
     __device__ __forceinline__ static void copy_one(const Ops &o, int kt, Dst buf, int wave, int lane) {
-        const int kleft = o.depth - kt * kStageK;
+        const int kleft = o.depth - kt * KS;
         if constexpr (I < SideA::COPIES) {
-            const uint32_t so = FORM == kFormGrad ? 0 : (uint32_t)kt * (kStageK * 2);
+            const uint32_t so = FORM == kFormGrad ? 0 : (uint32_t)kt * 128;
             const bool ok = !CHECK || SideA::k(wave, lane, I) < kleft;
             lds_copy16(o.A.rsrc, ok ? o.A.off[I] : kOob, so, buf.a + I * 1024);
         } else {
             constexpr int i = I - SideA::COPIES;
             const uint32_t so = FORM == kFormGrad  ? 0
-                                : FORM == kFormBwd ? (uint32_t)kt * (kStageK * 2)
-                                                   : (uint32_t)kt * (uint32_t)(kStageK * 2) * (uint32_t)o.ldb;
+                                : FORM == kFormBwd ? (uint32_t)kt * 128
+                                                   : (uint32_t)kt * 128 * (uint32_t)o.ldb;
             const bool ok = !CHECK || SideB::k(wave, lane, i) < kleft;
             lds_copy16(o.B.rsrc, ok ? o.B.off[i] : kOob, so, buf.b + i * 1024);
         }
@@ -222,14 +241,14 @@ struct GroupedTile {
     // with the stages instead of a 32-bit offset.  pa, pb, ra, rb are those of
     // the stage copied last.
     __device__ __forceinline__ static void set_descriptors(Ops &o) {
-        o.A.rsrc = sgpr_rsrc(o.pa, o.ra > 0 ? (size_t)o.ra * 2 : 0);
-        o.B.rsrc = sgpr_rsrc(o.pb, o.rb > 0 ? (size_t)o.rb * 2 : 0);
+        o.A.rsrc = sgpr_rsrc(o.pa, o.ra > 0 ? (size_t)o.ra * ES : 0);
+        o.B.rsrc = sgpr_rsrc(o.pb, o.rb > 0 ? (size_t)o.rb * ES : 0);
     }
     __device__ __forceinline__ static void next_stage(Ops &o) {
         if constexpr (FORM == kFormGrad) {
-            const int64_t da = (int64_t)kStageK * o.lda, db = (int64_t)kStageK * o.ldb;
-            o.pa += da * 2;
-            o.pb += db * 2;
+            const int64_t da = (int64_t)KS * o.lda, db = (int64_t)KS * o.ldb;
+            o.pa += da * ES;
+            o.pb += db * ES;
             o.ra -= da;
             o.rb -= db;
             set_descriptors(o);
@@ -261,7 +280,14 @@ struct GroupedTile {
     // share an operand (fewer operand bits toggle, a higher clock).
     template <int I>
     __device__ __forceinline__ static void mma(const Frags &f, f32x4_t (&acc)[NRB][NI]) {
-        constexpr int mi = I / NI, ni = (mi & 1) ? NI - 1 - I % NI : I % NI;
+        constexpr int q = I / MPB, mi = q / NI, ni = (mi & 1) ? NI - 1 - q % NI : q % NI;
+        if constexpr (DT == FL_F32) {
+            constexpr int j = I % MPB;
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                __builtin_bit_cast(f32x2_t, f.b[ni][j >> 1])[j & 1], __builtin_bit_cast(f32x2_t, f.a[mi][j >> 1])[j & 1],
+                acc[mi][ni], 0, 0, 0);
+            return;
+        }
         const auto av = __builtin_shufflevector(f.a[mi][0], f.a[mi][1], 0, 1, 2, 3);
         const auto bv = __builtin_shufflevector(f.b[ni][0], f.b[ni][1], 0, 1, 2, 3);
         if constexpr (DT == FL_F16)
@@ -297,21 +323,22 @@ struct GroupedTile {
     }
 
     __device__ __forceinline__ static bool ragged(const GroupedArgs &a) {
-        return FORM == kFormBwd ? (a.K & 7) : ((a.K | a.N) & 7);
+        if (FORM == kFormBwd || ES == 4) return a.K % EPC;
+        return (a.K | a.N) % EPC;
     }
     // fix_tail of both sides for stage kt; `ahead` stages after it are copied.
     __device__ __forceinline__ static void fix_tail(const GroupedArgs &a, const Ops &o, int kt, int ahead, int wave,
                                                     int lane, FL_LDS char *s) {
-        const int64_t k0 = (int64_t)kt * kStageK;
+        const int64_t k0 = (int64_t)kt * KS;
         const int kleft = (int)(o.depth - k0);
         int64_t la = o.ra - k0, lb = o.rb - (FORM == kFormBwd ? k0 : k0 * o.ldb);
         if constexpr (FORM == kFormGrad) {
-            la = o.ra + (int64_t)ahead * kStageK * o.lda;
-            lb = o.rb + (int64_t)ahead * kStageK * o.ldb;
+            la = o.ra + (int64_t)ahead * KS * o.lda;
+            lb = o.rb + (int64_t)ahead * KS * o.ldb;
         }
         const int64_t nb = FORM == kFormGrad ? (int64_t)a.S * a.N : (int64_t)a.E * a.K * a.N;
-        o.A.fix_tail(s, wave, lane, la, kleft, static_cast<const uint16_t *>(a.A) + (a.A_rows * a.K - 1));
-        o.B.fix_tail(s + SideA::BYTES, wave, lane, lb, kleft, static_cast<const uint16_t *>(a.B) + (nb - 1));
+        o.A.fix_tail(s, wave, lane, la, kleft, static_cast<const raw *>(a.A) + (a.A_rows * a.K - 1));
+        o.B.fix_tail(s + SideA::BYTES, wave, lane, lb, kleft, static_cast<const raw *>(a.B) + (nb - 1));
     }
 
     // Stage kt in LDS buffer `buf`; its block 0 operands are in f[0].
@@ -359,7 +386,7 @@ struct GroupedTile {
         for (int mi = 0; mi < NRB; ++mi)
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        const int nk = o.depth > 0 ? (int)(((int64_t)o.depth + kStageK - 1) / kStageK) : 1;  // (no k: one stage of zeros)
+        const int nk = o.depth > 0 ? (int)(((int64_t)o.depth + KS - 1) / KS) : 1;  // (no k: one stage of zeros)
         // whatever the epilogue before left in flight came after stage 0
         wait_vm<(NBUF - 1) * COPIES>();
         if (nk == 1 && ragged(a)) fix_tail(a, o, 0, NBUF - 1, wave, lane, (FL_LDS char *)lds);
@@ -395,50 +422,64 @@ struct GroupedTile {
         __syncthreads();
     }
 
-    // ---- epilogue
-    __device__ __forceinline__ static u32x4_t load8(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid) {
-        u32x4_t v = {0, 0, 0, 0};
-        if (valid >= 8) {
-            v = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-        } else {
+    // ---- epilogue: 8 consecutive columns of a row
+    struct Octet {
+        u32x4_t w[ES / 2];
+        __device__ __forceinline__ float get(int e) const {
+            if constexpr (ES == 4)
+                return __builtin_bit_cast(float, (uint32_t)w[e >> 2][e & 3]);
+            else
+                return io::to_f32((raw)(w[0][e >> 1] >> (16 * (e & 1))));
+        }
+    };
+    __device__ __forceinline__ static uint32_t at(uint32_t off, int bytes, bool ok) {
+        return ok && off != kOob ? off + bytes : kOob;
+    }
+    __device__ __forceinline__ static Octet load8(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid) {
+        Octet v;
 #pragma unroll
-            for (int e = 0; e < 7; ++e) {
-                const uint32_t x = load_elem<2>(r, e < valid && off != kOob ? off + e * 2 : kOob);
-                v[e >> 1] |= x << (16 * (e & 1));
+        for (int h = 0; h < ES / 2; ++h) {
+            if (valid >= EPC * (h + 1)) {
+                v.w[h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at(off, h * 16, true), 0, 0));
+            } else {
+                v.w[h] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < EPC - 1; ++e) {
+                    const uint32_t x = load_elem<ES>(r, at(off, h * 16 + e * ES, h * EPC + e < valid));
+                    v.w[h][e * ES / 4] |= x << (8 * (e * ES & 3));
+                }
             }
         }
         return v;
-    }
-    __device__ __forceinline__ static float get8(const u32x4_t &v, int e) {
-        return io::to_f32((raw)(v[e >> 1] >> (16 * (e & 1))));
-    }
-    __device__ __forceinline__ static void store8(const float (&v)[8], __amdgpu_buffer_rsrc_t r, uint32_t off, int valid) {
-        u32x4_t w;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) w[d] = io::pack2(v[2 * d], v[2 * d + 1]);
-        if (valid >= 8) {
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, w), r, off, 0, 0);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 7; ++e)
-                store_elem<2>((uint16_t)(w[e >> 1] >> (16 * (e & 1))), r,
-                              e < valid && off != kOob ? off + e * 2 : kOob);
-        }
     }
     __device__ __forceinline__ static void store8_f32(const float (&v)[8], __amdgpu_buffer_rsrc_t r, uint32_t off,
                                                       int valid) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            const f32x4_t w = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
             if (valid >= 4 * h + 4) {
-                const u32x4_t w = {__builtin_bit_cast(uint32_t, v[4 * h]), __builtin_bit_cast(uint32_t, v[4 * h + 1]),
-                                   __builtin_bit_cast(uint32_t, v[4 * h + 2]), __builtin_bit_cast(uint32_t, v[4 * h + 3])};
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, w), r,
-                                                       off != kOob ? off + h * 16 : kOob, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, w), r, at(off, h * 16, true), 0, 0);
             } else {
 #pragma unroll
                 for (int e = 0; e < 3; ++e)
                     store_elem<4>(__builtin_bit_cast(uint32_t, v[4 * h + e]), r,
-                                  4 * h + e < valid && off != kOob ? off + h * 16 + e * 4 : kOob);
+                                  at(off, h * 16 + e * 4, 4 * h + e < valid));
+            }
+        }
+    }
+    __device__ __forceinline__ static void store8(const float (&v)[8], __amdgpu_buffer_rsrc_t r, uint32_t off, int valid) {
+        if constexpr (ES == 4) {
+            store8_f32(v, r, off, valid);
+        } else {
+            u32x4_t w;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) w[d] = io::pack2(v[2 * d], v[2 * d + 1]);
+            if (valid >= 8) {
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, w), r, off, 0, 0);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    store_elem<2>((uint16_t)(w[e >> 1] >> (16 * (e & 1))), r, at(off, e * 2, e < valid));
             }
         }
     }
@@ -457,32 +498,32 @@ struct GroupedTile {
         const int64_t row0 = FORM == kFormGrad ? (int64_t)t.e * a.K + t.m0 : t.m0;
         const int wm = row_of(wave), wn = col_of(wave);
         constexpr int CPR = TN / 8, RPP = 64 / CPR, PASSES = 16 / RPP;  // lanes per row, rows and passes per row block
-        const int es = FORM == kFormGrad && a.dw_f32 ? 4 : 2;
+        const int es = FORM == kFormGrad && a.dw_f32 ? 4 : ES;
         const int64_t org = row0 * a.N + n0;
         const size_t bytes = ((size_t)rows * a.N - n0) * es;
         const __amdgpu_buffer_rsrc_t rO = make_rsrc(static_cast<char *>(a.out) + org * es, bytes);
         const __amdgpu_buffer_rsrc_t rO2 =
-            make_rsrc(a.out2 ? static_cast<char *>(a.out2) + org * 2 : nullptr, a.out2 ? bytes : 0);
+            make_rsrc(a.out2 ? static_cast<char *>(a.out2) + org * ES : nullptr, a.out2 ? bytes : 0);
         const __amdgpu_buffer_rsrc_t rY =
-            make_rsrc(a.Y ? static_cast<const char *>(a.Y) + org * 2 : nullptr, a.Y ? bytes : 0);
+            make_rsrc(a.Y ? static_cast<const char *>(a.Y) + org * ES : nullptr, a.Y ? bytes : 0);
         const __amdgpu_buffer_rsrc_t rX =
-            make_rsrc(a.X ? static_cast<const char *>(a.X) + org * 2 : nullptr, a.X ? bytes : 0);
+            make_rsrc(a.X ? static_cast<const char *>(a.X) + org * ES : nullptr, a.X ? bytes : 0);
         const int col = wn * TN + (lane % CPR) * 8, valid = a.N - n0 - col;
         FL_LDS char *w = lds + wave * 16 * EPI_ROW;
         auto offset = [&](int mi, int p) -> uint32_t {
             const int row = wm * TM + mi * 16 + p * RPP + lane / CPR;
             return row < rows && valid > 0 ? (uint32_t)(row * a.N + col) * es : kOob;
         };
-        u32x4_t bias = {0, 0, 0, 0};
+        Octet bias{};
         if constexpr (FORM == kFormFwd) {
             if (a.bias) {
                 const __amdgpu_buffer_rsrc_t rB = make_rsrc(
-                    static_cast<const char *>(a.bias) + ((int64_t)t.e * a.N + n0) * 2, (size_t)(a.N - n0) * 2);
-                bias = load8(rB, valid > 0 ? (uint32_t)col * 2 : kOob, valid);
+                    static_cast<const char *>(a.bias) + ((int64_t)t.e * a.N + n0) * ES, (size_t)(a.N - n0) * ES);
+                bias = load8(rB, valid > 0 ? (uint32_t)col * ES : kOob, valid);
             }
         }
         constexpr bool NEED_Y = ACT == FL_ACT_GLU, NEED_X = FORM == kFormBwd && ACT != FL_ACT_NONE;
-        u32x4_t yv[2][PASSES], xv[2][PASSES];  // of this row block and the next
+        Octet yv[2][PASSES], xv[2][PASSES];  // of this row block and the next
         auto sides = [&](int mi) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
@@ -509,13 +550,13 @@ struct GroupedTile {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float d = i < 4 ? lo[i & 3] : hi[i & 3];
-                    const float y = NEED_Y ? get8(yv[mi & 1][p], i) : 0.0f;
+                    const float y = NEED_Y ? yv[mi & 1][p].get(i) : 0.0f;
                     if constexpr (FORM == kFormFwd) {
-                        const float x = d + get8(bias, i);
+                        const float x = d + bias.get(i);
                         v2[i] = x;
                         v[i] = activate<ACT>(x, y);
                     } else if constexpr (FORM == kFormBwd) {
-                        const float xs = NEED_X ? get8(xv[mi & 1][p], i) : 0.0f;
+                        const float xs = NEED_X ? xv[mi & 1][p].get(i) : 0.0f;
                         v[i] = d * activate_grad<ACT>(xs, y);
                         v2[i] = d * xs;
                         asm("" : "+v"(v[i]), "+v"(v2[i]));  // fp32 before the cast, in every kernel alike
@@ -585,25 +626,25 @@ struct GroupedTile {
         o.lda = a.K;
         o.ldb = FORM == kFormBwd ? a.K : a.N;
         if constexpr (FORM == kFormGrad) {
-            o.pa = static_cast<const char *>(a.A) + ((int64_t)t.lo * a.K + t.m0) * 2;
-            o.pb = static_cast<const char *>(a.B) + ((int64_t)t.lo * a.N + n0) * 2;
+            o.pa = static_cast<const char *>(a.A) + ((int64_t)t.lo * a.K + t.m0) * ES;
+            o.pb = static_cast<const char *>(a.B) + ((int64_t)t.lo * a.N + n0) * ES;
             o.ra = (int64_t)(a.S - t.lo) * a.K - t.m0;
             o.rb = (int64_t)(a.S - t.lo) * a.N - n0;
             set_descriptors(o);
         } else {
             const int64_t a0 = FORM == kFormFwd && a.index ? 0 : (int64_t)t.m0 * a.K;
             o.ra = a.A_rows * a.K - a0;
-            o.A.rsrc = sgpr_rsrc(static_cast<const char *>(a.A) + a0 * 2, (size_t)o.ra * 2);
+            o.A.rsrc = sgpr_rsrc(static_cast<const char *>(a.A) + a0 * ES, (size_t)o.ra * ES);
             const int64_t b0 = (int64_t)t.e * a.K * a.N + (FORM == kFormBwd ? (int64_t)n0 * a.K : n0);
             o.rb = (int64_t)a.E * a.K * a.N - b0;
-            o.B.rsrc = sgpr_rsrc(static_cast<const char *>(a.B) + b0 * 2, (size_t)o.rb * 2);
+            o.B.rsrc = sgpr_rsrc(static_cast<const char *>(a.B) + b0 * ES, (size_t)o.rb * ES);
         }
 #pragma unroll
         for (int i = 0; i < SideA::COPIES; ++i) {
             int r, c;
             SideA::place(wave, lane, i, r, c);
             if constexpr (FORM == kFormGrad) {
-                o.A.off[i] = c * 8 < t.rows ? (uint32_t)(r * o.lda + c * 8) * 2 : kOob;
+                o.A.off[i] = c * EPC < t.rows ? (uint32_t)(r * o.lda + c * EPC) * ES : kOob;
             } else {
                 int64_t row = r;
                 bool ok = r < t.rows;
@@ -611,7 +652,7 @@ struct GroupedTile {
                     row = ok ? a.index[t.m0 + r] : 0;
                     ok = ok && row >= 0 && row < a.A_rows;
                 }
-                o.A.off[i] = ok ? ((uint32_t)row * (uint32_t)o.lda + c * 8) * 2 : kOob;
+                o.A.off[i] = ok ? ((uint32_t)row * (uint32_t)o.lda + c * EPC) * ES : kOob;
             }
         }
 #pragma unroll
@@ -619,9 +660,9 @@ struct GroupedTile {
             int r, c;
             SideB::place(wave, lane, i, r, c);
             if constexpr (FORM == kFormBwd) {
-                o.B.off[i] = n0 + r < a.N ? (uint32_t)(r * o.ldb + c * 8) * 2 : kOob;
+                o.B.off[i] = n0 + r < a.N ? (uint32_t)(r * o.ldb + c * EPC) * ES : kOob;
             } else {
-                o.B.off[i] = n0 + c * 8 < a.N ? (uint32_t)(r * o.ldb + c * 8) * 2 : kOob;
+                o.B.off[i] = n0 + c * EPC < a.N ? (uint32_t)(r * o.ldb + c * EPC) * ES : kOob;
             }
         }
     }

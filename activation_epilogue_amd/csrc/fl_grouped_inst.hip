@@ -1,41 +1,41 @@
-// fl_grouped_inst.hip -- instantiates the column sum for one dtype, and for
-// fp32 the experts' products (16-bit operands: fl_grouped_dma_inst.hip).
-// Built once per dtype with -DFL_INST_DTYPE=<fl_dtype value>.
-#include "fl_grouped.hpp"
+// fl_grouped_inst.hip -- instantiates the experts' products for one dtype and
+// one form (and the column sum with the gradient).  Built once per dtype and
+// form with -DFL_INST_DTYPE=<fl_dtype value> -DFL_INST_FORM=<form>.
+#include "fl_grouped_dma.hpp"
 
-#ifndef FL_INST_DTYPE
-#error "define FL_INST_DTYPE"
+#if !defined(FL_INST_DTYPE) || !defined(FL_INST_FORM)
+#error "define FL_INST_DTYPE and FL_INST_FORM"
 #endif
 
 namespace fl {
 
+template <int BM, int BN, int WM, int WN, int NBUF, int OCC>
+static void launch(const GroupedArgs &a, int act, int64_t grid, hipStream_t s) {
+    hipLaunchKernelGGL((grouped_dma_kernel<FL_INST_DTYPE, FL_INST_FORM, BM, BN, WM, WN, NBUF, OCC>),
+                       dim3((unsigned)grid), dim3(64 * WM * WN), 0, s, a, act);
+}
+
+template <>
+grouped_launcher pick_grouped<FL_INST_DTYPE, FL_INST_FORM>(int variant) {
 #if FL_INST_DTYPE == 0
-template <int FORM, int ACT>
-static void launch_f32(const GroupedArgs &a, int64_t grid, hipStream_t s) {
-    hipLaunchKernelGGL((grouped_f32_kernel<FORM, ACT>), dim3((unsigned)grid), dim3(256), 0, s, a);
-}
-
-template <int FORM>
-static grouped_launcher pick_act(int act) {
-    switch (act) {
-    case FL_ACT_NONE: return launch_f32<FORM, FL_ACT_NONE>;
-    case FL_ACT_RELU: return launch_f32<FORM, FL_ACT_RELU>;
-    case FL_ACT_GELU_TANH: return launch_f32<FORM, FL_ACT_GELU_TANH>;
-    default: return launch_f32<FORM, FL_ACT_GLU>;
-    }
-}
-
-grouped_launcher pick_grouped_f32(int form, int act) {
-    if (form == kFormFwd) return pick_act<kFormFwd>(act);
-    if (form == kFormBwd) return pick_act<kFormBwd>(act);
-    return launch_f32<kFormGrad, FL_ACT_NONE>;
-}
+    return variant == kTileF32 ? launch<64, 64, 2, 2, 3, 3> : nullptr;
+#else
+    if (variant == kTile256x256) return launch<256, 256, 2, 4, 2, 1>;
+#if FL_INST_FORM != 2
+    if (variant == kTile256x128) return launch<256, 128, 4, 2, 3, 1>;
+    if (variant == kTile64x128) return launch<64, 128, 1, 4, 3, 2>;
+    if (variant == kTile32x128) return launch<32, 128, 1, 4, 4, 2>;
 #endif
+    return launch<128, 128, 2, 2, 2, 2>;
+#endif
+}
 
+#if FL_INST_FORM == 2
 template <>
 void launch_column_sum<FL_INST_DTYPE>(const GroupedArgs &a, hipStream_t s) {
     const unsigned blocks = (unsigned)a.E * (unsigned)((a.N + kColumns - 1) / kColumns);
     hipLaunchKernelGGL((grouped_column_sum_kernel<FL_INST_DTYPE>), dim3(blocks), dim3(256), 0, s, a);
 }
+#endif
 
 }  // namespace fl

@@ -205,27 +205,30 @@ int64_t most_row_tiles(int64_t S, int64_t E, int64_t bm) {
 
 size_t grouped_workspace(int64_t, int64_t, int64_t, int64_t, int) { return 0; }
 
-fl::grouped_dma_launcher pick_dma(int dtype, int form, int variant) {
-    using namespace fl;
-    if (dtype == FL_F16)
-        return form == kFormFwd   ? pick_grouped_dma_form<FL_F16, kFormFwd>(variant)
-               : form == kFormBwd ? pick_grouped_dma_form<FL_F16, kFormBwd>(variant)
-                                  : pick_grouped_dma_form<FL_F16, kFormGrad>(variant);
-    return form == kFormFwd   ? pick_grouped_dma_form<FL_BF16, kFormFwd>(variant)
-           : form == kFormBwd ? pick_grouped_dma_form<FL_BF16, kFormBwd>(variant)
-                              : pick_grouped_dma_form<FL_BF16, kFormGrad>(variant);
+template <int DT>
+fl::grouped_launcher pick_grouped_dt(int form, int variant) {
+    return form == fl::kFormFwd   ? fl::pick_grouped<DT, fl::kFormFwd>(variant)
+           : form == fl::kFormBwd ? fl::pick_grouped<DT, fl::kFormBwd>(variant)
+                                  : fl::pick_grouped<DT, fl::kFormGrad>(variant);
 }
 
-// The tile for 16-bit operands: the one of least estimated time, in rounds of
+fl::grouped_launcher pick_grouped(int dtype, int form, int variant) {
+    return dtype == FL_F32   ? pick_grouped_dt<FL_F32>(form, variant)
+           : dtype == FL_F16 ? pick_grouped_dt<FL_F16>(form, variant)
+                             : pick_grouped_dt<FL_BF16>(form, variant);
+}
+
+// The tile: the one of least estimated time, in rounds of
 // a full chip.  Runs end inside a tile, so S rows in R runs make about S/bm +
 // R/2 row tiles (at least R); rounds beyond the first end ragged, half a round
 // on average.
-int pick_variant(int form, int64_t S, int64_t N, int64_t K, int64_t E) {
-    int best = 0;
+int pick_variant(int dtype, int form, int64_t S, int64_t N, int64_t K, int64_t E) {
+    if (dtype == FL_F32) return fl::kTileF32;
+    int best = -1;
     double least = 0.0;
-    for (int v = 0; v < fl::kGroupedVariants; ++v) {
-        if (form == fl::kFormGrad && v != fl::kTile256x256 && v != fl::kTile128x128) continue;
+    for (int v = 0; v < fl::kTileF32; ++v) {
         const fl::GroupedTileShape &t = fl::kGroupedTiles[v];
+        if (form == fl::kFormGrad && !t.grad) continue;
         double m;
         if (form == fl::kFormGrad) {
             m = (double)E * ((K + t.bm - 1) / t.bm);
@@ -236,7 +239,7 @@ int pick_variant(int form, int64_t S, int64_t N, int64_t K, int64_t E) {
         }
         const double x = m * ((N + t.bn - 1) / t.bn) / (kCus * t.per_cu);
         const double time = t.time * (x < 0.9 ? 1.0 : x + 0.5);
-        if (v == 0 || time < least) {
+        if (best < 0 || time < least) {
             least = time;
             best = v;
         }
@@ -246,9 +249,8 @@ int pick_variant(int form, int64_t S, int64_t N, int64_t K, int64_t E) {
 
 fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void *stream, const char *what) {
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const bool dma = dtype != FL_F32;  // 16-bit operands
-    const int v = dma ? pick_variant(form, a.S, a.N, a.K, a.E) : 0;
-    const fl::GroupedTileShape t = dma ? fl::kGroupedTiles[v] : fl::GroupedTileShape{64, 64, 1, 1.0f};
+    const int v = pick_variant(dtype, form, a.S, a.N, a.K, a.E);
+    const fl::GroupedTileShape &t = fl::kGroupedTiles[v];
     a.tiles_n = (int)((a.N + t.bn - 1) / t.bn);
     // bands of 8 row tiles: prompts through 64 experts 210 us, 218 with 4 or
     // 16; weight gradient (operands of equal height) 1614 us with 4, 1627 with 8
@@ -272,10 +274,8 @@ fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void 
         if (s != FL_OK) return s;
     }
     if (grid == 0) return FL_OK;
-    if (dma)
-        pick_dma(dtype, form, v)(a, act, grid < kCus * t.per_cu ? grid : kCus * t.per_cu, st);
-    else
-        fl::pick_grouped_f32(form, act)(a, grid, st);
+    const int64_t slots = kCus * t.per_cu;
+    pick_grouped(dtype, form, v)(a, act, grid < slots ? grid : slots, st);
     return check_launch(what);
 }
 
