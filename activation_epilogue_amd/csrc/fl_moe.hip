@@ -370,10 +370,19 @@ fl_status fl_moe_plan(const int32_t *experts, int32_t *offsets, int32_t *token_o
     a.k = k ? (int)k : 1;
     a.E = (int)E;
     const int64_t blocks = (a.S + fl::kPlanChunk - 1) / fl::kPlanChunk;
-    const dim3 grid((unsigned)(blocks ? blocks : 1)), block(fl::kPlanThreads);
+    const dim3 grid((unsigned)(blocks ? blocks : 1));
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (need) hipLaunchKernelGGL(fl::plan_count_kernel, grid, block, 0, st, a);
-    hipLaunchKernelGGL(fl::plan_kernel, grid, block, 0, st, a);
+    if (need) hipLaunchKernelGGL(fl::plan_count_kernel, grid, dim3(1024), 0, st, a);
+    if (a.S <= fl::kPlanSmall) {
+        if (E <= 256)
+            hipLaunchKernelGGL((fl::plan_kernel<4, 256>), grid, dim3(256), 0, st, a);
+        else
+            hipLaunchKernelGGL((fl::plan_kernel<4, 1024>), grid, dim3(256), 0, st, a);
+    } else if (E <= 256) {
+        hipLaunchKernelGGL((fl::plan_kernel<16, 256>), grid, dim3(1024), 0, st, a);
+    } else {
+        hipLaunchKernelGGL((fl::plan_kernel<16, 1024>), grid, dim3(1024), 0, st, a);
+    }
     return check_launch("moe_plan");
 }
 

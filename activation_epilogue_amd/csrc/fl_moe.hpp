@@ -18,21 +18,53 @@ __device__ __forceinline__ void store_f32(void *p, int64_t i, float v) {
     static_cast<typename Io<DT>::raw *>(p)[i] = Io<DT>::from_f32(v);
 }
 
-// Sums and maxima over the 64 lanes, the same bits in every lane.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+// Sums and maxima over the 64 lanes, the same in every lane: moves between
+// neighbouring lanes, then rows of 16, on the vector unit (an LDS permute costs
+// ten times the latency, and a router is a chain of such steps).
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float lane_move(float old, float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old),
+                                                                 __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
 }
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ double lane_move(double old, double v) {
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    const i32x2 o = __builtin_bit_cast(i32x2, old), w = __builtin_bit_cast(i32x2, v);
+    return __builtin_bit_cast(double, i32x2{__builtin_amdgcn_update_dpp(o[0], w[0], CTRL, ROWS, 0xf, false),
+                                            __builtin_amdgcn_update_dpp(o[1], w[1], CTRL, ROWS, 0xf, false)});
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o));
-    return v;
+__device__ __forceinline__ float read_lane(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ double read_lane(double v, int lane) {
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    const i32x2 w = __builtin_bit_cast(i32x2, v);
+    return __builtin_bit_cast(
+        double, i32x2{__builtin_amdgcn_readlane(w[0], lane), __builtin_amdgcn_readlane(w[1], lane)});
+}
+// row_shr 1, 2, 4, 8: lane 15 of every row of 16 holds the row's; row_bcast 15
+// and 31: lane 63 holds all.  Lanes without a source keep `old`.
+template <class F>
+__device__ __forceinline__ F wave_sum(F v) {
+    v += lane_move<0x111>(F(0), v);
+    v += lane_move<0x112>(F(0), v);
+    v += lane_move<0x114>(F(0), v);
+    v += lane_move<0x118>(F(0), v);
+    v += lane_move<0x142, 0xa>(F(0), v);
+    v += lane_move<0x143, 0xc>(F(0), v);
+    return read_lane(v, 63);
+}
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
+template <class F>
+__device__ __forceinline__ F wave_max(F v) {
+    v = larger(v, lane_move<0x111>(v, v));
+    v = larger(v, lane_move<0x112>(v, v));
+    v = larger(v, lane_move<0x114>(v, v));
+    v = larger(v, lane_move<0x118>(v, v));
+    v = larger(v, lane_move<0x142>(v, v));
+    v = larger(v, lane_move<0x143>(v, v));
+    return read_lane(v, 63);
 }
 
 // ------------------------------------------------------------------ router
@@ -63,47 +95,65 @@ __device__ __forceinline__ F below(F x, F m) {
     return x == m ? F(0) : x - m;
 }
 
-// The largest key of the wave, ties to the lowest expert; e < 0 where no
-// lane has one left.
-__device__ __forceinline__ void wave_best(double &key, int &e) {
+// The k largest keys (-inf: not to be chosen), ties to the lowest expert;
+// choice j and its logit end up in lane j, -1 where no key is left.
+template <int EPL, class F>
+__device__ __forceinline__ void choose(F (&key)[EPL], const float (&x)[EPL], int k, int lane, int &sel, float &xs) {
+    for (int j = 0; j < k; ++j) {
+        F b = key[0];
 #pragma unroll
-    for (int o = 32; o; o >>= 1) {
-        const double k2 = __shfl_xor(key, o);
-        const int e2 = __shfl_xor(e, o);
-        const bool take = e2 >= 0 && (e < 0 || k2 > key || (k2 == key && e2 < e));
-        key = take ? k2 : key;
-        e = take ? e2 : e;
+        for (int i = 1; i < EPL; ++i) b = larger(b, key[i]);
+        b = wave_max(b);
+        if (!(b > F(kNegInf))) break;
+        int e = -1;
+        float xe = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const uint64_t at = __ballot(key[i] == b);
+            if (e < 0 && at) {
+                const int l = __builtin_ctzll(at);
+                e = l + 64 * i;
+                xe = read_lane(x[i], l);
+            }
+        }
+        if (lane == j) {
+            sel = e;
+            xs = xe;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (e == lane + 64 * i) key[i] = F(kNegInf);
     }
 }
 
 // One wave per token; expert e = lane + 64*i sits in register i of its lane.
-// Keys and scores that decide a choice are 64-bit; the weights are 32-bit.
+// Keys and scores that decide a choice are 64-bit (logits are as they are: with
+// neither a bias nor sums over a run, their order decides); the weights are
+// 32-bit.
 template <int DT, int EPL>
 __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
-    __shared__ double gkeys[4][EPL > 1 ? EPL * 64 : 64];
+    __shared__ double gkeys[4][EPL * 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double *gk = gkeys[wave];
-    for (int64_t t0 = (int64_t)blockIdx.x * 4; t0 < a.T; t0 += (int64_t)gridDim.x * 4) {
-        const int64_t t = t0 + wave;
-        const bool on = t < a.T;
+    const bool sums = a.groups > 1 && a.group_top == 2;
+    const int per = a.E / a.groups;
+    for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.T; t += (int64_t)gridDim.x * 4) {
         float x[EPL];
         float m = kNegInf;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = lane + 64 * i;
-            x[i] = on && e < a.E ? load_f32<DT>(a.logits, t * a.E + e) : kNegInf;
+            x[i] = e < a.E ? load_f32<DT>(a.logits, t * a.E + e) : kNegInf;
             if (!(x[i] > kNegInf)) x[i] = kNegInf;  // NaN counts as masked
             m = __builtin_fmaxf(m, x[i]);
         }
         m = wave_max(m);
-        const bool sums = a.groups > 1 && a.group_top == 2;
         double key[EPL], score[EPL];
         if (a.bias || sums) {
             double z = 0.0;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const double xd = x[i];
-                score[i] = a.sigmoid ? 1.0 / (1.0 + exp(-xd)) : x[i] > kNegInf ? exp(below(xd, (double)m)) : 0.0;
+                score[i] = x[i] > kNegInf ? (a.sigmoid ? 1.0 / (1.0 + exp(-xd)) : exp(below(xd, (double)m))) : 0.0;
                 z += score[i];
             }
             if (!a.sigmoid) {
@@ -111,74 +161,68 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) score[i] /= z;
             }
-        }
-        bool live[EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = lane + 64 * i;
-            key[i] = a.bias ? score[i] + (double)(e < a.E ? a.bias[e] : 0.0f) : (double)x[i];
-            live[i] = x[i] > kNegInf && key[i] > (double)kNegInf;  // (a NaN key fails)
+            for (int i = 0; i < EPL; ++i) {
+                const int e = lane + 64 * i;
+                key[i] = kNegInf;
+                if (x[i] > kNegInf) {
+                    const double v = a.bias ? score[i] + (double)a.bias[e] : (double)x[i];
+                    if (v > (double)kNegInf) key[i] = v;  // (a NaN key is no key)
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) key[i] = x[i];
         }
         if (a.groups > 1) {
-            // lane g scores run g from the keys of its experts
-            const int per = a.E / a.groups;
+            // 64 / 2^ceil(log2 groups) lanes find the largest two keys of a run together
+            double *gk = gkeys[wave];
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (lane + 64 * i < a.E)
-                    gk[lane + 64 * i] = live[i] ? (sums && !a.bias ? score[i] : key[i]) : (double)kNegInf;
-            __syncthreads();
-            double gs = 0.0;
-            int g = -1;
-            if (lane < a.groups) {
-                double b1 = kNegInf, b2 = kNegInf;
-                for (int j = 0; j < per; ++j) {
-                    const double v = gk[lane * per + j];
-                    if (v > b1) {
-                        b2 = b1;
-                        b1 = v;
-                    } else if (v > b2) {
-                        b2 = v;
-                    }
+                gk[lane + 64 * i] = key[i] > (double)kNegInf && sums && !a.bias ? score[i] : key[i];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            int team = 64;
+            while (64 / team < a.groups) team >>= 1;
+            const int g = lane / team;
+            double b1 = kNegInf, b2 = kNegInf;
+            if (g < a.groups)
+                for (int j = lane % team; j < per; j += team) {
+                    const double v = gk[g * per + j];
+                    b2 = larger(b2, v < b1 ? v : b1);
+                    b1 = larger(b1, v);
                 }
-                gs = a.group_top == 2 && b2 > (double)kNegInf ? b1 + b2 : b1;
-                g = b1 > (double)kNegInf ? lane : -1;
+            for (int o = 1; o < team; o <<= 1) {
+                const double o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
+                b2 = larger(larger(b2, o2), b1 < o1 ? b1 : o1);
+                b1 = larger(b1, o1);
             }
+            double gs = a.group_top == 2 && b2 > (double)kNegInf ? b1 + b2 : b1;
             uint64_t kept = 0;
             for (int j = 0; j < a.top_groups; ++j) {
-                double bk = gs;
-                int bg = (kept >> lane) & 1 ? -1 : g;
-                wave_best(bk, bg);
-                if (bg < 0) break;
-                kept |= 1ull << bg;
+                const double b = wave_max(gs);
+                if (!(b > (double)kNegInf)) break;
+                const int best = __builtin_ctzll(__ballot(gs == b)) / team;
+                kept |= 1ull << best;
+                if (g == best) gs = kNegInf;
             }
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                live[i] = live[i] && ((kept >> ((lane + 64 * i) / per)) & 1);
-            __syncthreads();
+            for (int i = 0; i < EPL; ++i) {
+                const int e = lane + 64 * i;
+                if (e < a.E && !((kept >> (e / per)) & 1)) key[i] = kNegInf;
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
         }
-        // choice j ends up in lane j
         int sel = -1;
-        for (int j = 0; j < a.k; ++j) {
-            double bk = 0.0;
-            int be = -1;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (live[i] && (be < 0 || key[i] > bk)) {
-                    bk = key[i];
-                    be = lane + 64 * i;
-                }
-            wave_best(bk, be);
-            if (be < 0) break;
-            if (lane == j) sel = be;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (be == lane + 64 * i) live[i] = false;
-        }
         float xs = kNegInf;  // the chosen expert's logit
+        if (a.bias) {
+            choose(key, x, a.k, lane, sel, xs);
+        } else {
+            float key32[EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const float v = __shfl(x[i], sel & 63);
-            if (sel >= 0 && (sel >> 6) == i) xs = v;
+            for (int i = 0; i < EPL; ++i) key32[i] = (float)key[i];  // (the logit itself, or -inf)
+            choose(key32, x, a.k, lane, sel, xs);
         }
         float w;
         if (!a.raw) {
@@ -197,7 +241,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
             z = wave_sum(z);
             w = expf(below(xs, m)) / z;
         }
-        if (on && lane < a.k) {
+        if (lane < a.k) {
             a.experts[t * a.k + lane] = sel;
             a.weights[t * a.k + lane] = sel < 0 ? 0.0f : w * a.scale;
         }
@@ -251,8 +295,8 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
         }
         if (sel < 0) ds = 0.0f;
         for (int j = 0; j < a.k; ++j) {
-            const int e = __shfl(sel, j);
-            const float v = __shfl(ds, j);
+            const int e = __builtin_amdgcn_readlane(sel, j);
+            const float v = read_lane(ds, j);
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
                 if (e == lane + 64 * i) d[i] += v;
@@ -285,12 +329,13 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
 
 // -------------------------------------------------------------------- plan
 
-// A stable counting sort of the slots by expert.  Block b owns the kPlanChunk
-// slots from b*kPlanChunk, wave w of it a run of kPlanRun of them.
-constexpr int kPlanThreads = 512;
-constexpr int kPlanWaves = kPlanThreads / 64;
-constexpr int kPlanChunk = 4096;
-constexpr int kPlanRun = kPlanChunk / kPlanWaves;
+// A stable counting sort of the slots by expert.  A block owns CHUNK slots, a
+// wave of it a run of kPlanRun of them, kept in registers between counting and
+// placing.  Up to kPlanSmall slots one block of 4 waves does it all (the fewest
+// steps from launch to end); above, blocks of 16 waves, and where there are
+// several, a launch before them counts every block's slots.
+constexpr int kPlanRun = 256;
+constexpr int kPlanSmall = 4 * kPlanRun, kPlanChunk = 16 * kPlanRun;
 
 struct PlanArgs {
     const int32_t *experts;
@@ -305,43 +350,67 @@ __device__ __forceinline__ int slot_expert(const PlanArgs &a, int64_t s) {
     return e >= 0 && e < a.E ? e : -1;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(PlanArgs a) {
+__global__ void __launch_bounds__(1024) plan_count_kernel(PlanArgs a) {
     __shared__ int cnt[kMaxExperts];
-    for (int e = threadIdx.x; e < a.E; e += kPlanThreads) cnt[e] = 0;
+    for (int e = threadIdx.x; e < a.E; e += 1024) cnt[e] = 0;
     __syncthreads();
     const int64_t s0 = (int64_t)blockIdx.x * kPlanChunk;
-    for (int i = threadIdx.x; i < kPlanChunk; i += kPlanThreads) {
-        const int e = slot_expert(a, s0 + i);
+#pragma unroll
+    for (int i = 0; i < kPlanChunk / 1024; ++i) {
+        const int e = slot_expert(a, s0 + threadIdx.x + i * 1024);
         if (e >= 0) atomicAdd(&cnt[e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kPlanThreads) a.counts[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+    for (int e = threadIdx.x; e < a.E; e += 1024) a.counts[(int64_t)blockIdx.x * a.E + e] = cnt[e];
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
-    __shared__ int run[kPlanWaves][kMaxExperts];  // counts of a wave's run, then its next row of every expert
-    __shared__ int first[kMaxExperts + 1];        // first row of every expert
-    __shared__ int before[kMaxExperts];           // this block's first row within the expert
+// EC: an upper limit of E, a power of two.
+template <int WAVES, int EC>
+__global__ void __launch_bounds__(64 * WAVES) plan_kernel(PlanArgs a) {
+    constexpr int THREADS = 64 * WAVES, CHUNK = WAVES * kPlanRun, STEPS = kPlanRun / 64;
+    constexpr int PARTS = THREADS > EC ? THREADS / EC : 1;
+    __shared__ int run[WAVES][EC];           // counts of a wave's run, then its next row of every expert
+    __shared__ int first[EC + 1];            // first row of every expert
+    __shared__ int before[EC];               // this block's first row within the expert
+    __shared__ int sums[PARTS][EC], prevs[PARTS][EC];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t s0 = (int64_t)blockIdx.x * kPlanChunk + wave * kPlanRun;
+    const int64_t s0 = (int64_t)blockIdx.x * CHUNK + wave * kPlanRun;
+    int ex[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) ex[i] = slot_expert(a, s0 + i * 64 + lane);
     for (int e = lane; e < a.E; e += 64) run[wave][e] = 0;
     __syncthreads();
-    for (int i = lane; i < kPlanRun; i += 64) {
-        const int e = slot_expert(a, s0 + i);
-        if (e >= 0) atomicAdd(&run[wave][e], 1);
-    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+        if (ex[i] >= 0) atomicAdd(&run[wave][ex[i]], 1);
     __syncthreads();
     // every expert's rows in earlier blocks, and in all of them
-    for (int e = tid; e < a.E; e += kPlanThreads) {
-        int all = 0, prev = 0;
-        if (a.counts) {
-            for (int b = 0; b < (int)gridDim.x; ++b) {
+    if (a.counts) {
+        const int part = tid / EC;
+        for (int e = tid % EC; e < a.E; e += PARTS == 1 ? THREADS : EC) {
+            int all = 0, prev = 0;
+#pragma unroll 8
+            for (int b = part; b < (int)gridDim.x; b += PARTS) {
                 const int c = a.counts[(int64_t)b * a.E + e];
-                if (b < (int)blockIdx.x) prev += c;
+                prev += b < (int)blockIdx.x ? c : 0;
                 all += c;
             }
+            sums[part][e] = all;
+            prevs[part][e] = prev;
+        }
+        __syncthreads();
+    }
+    for (int e = tid; e < a.E; e += THREADS) {
+        int all = 0, prev = 0;
+        if (a.counts) {
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+                all += sums[p][e];
+                prev += prevs[p][e];
+            }
         } else {
-            for (int w = 0; w < kPlanWaves; ++w) all += run[w][e];
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) all += run[w][e];
         }
         before[e] = prev;
         first[e] = all;
@@ -366,10 +435,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     __syncthreads();
     const int total = first[a.E];
     if (blockIdx.x == 0)
-        for (int e = tid; e <= a.E; e += kPlanThreads) a.offsets[e] = first[e];
-    for (int e = tid; e < a.E; e += kPlanThreads) {
+        for (int e = tid; e <= a.E; e += THREADS) a.offsets[e] = first[e];
+    for (int e = tid; e < a.E; e += THREADS) {
         int at = first[e] + before[e];
-        for (int w = 0; w < kPlanWaves; ++w) {
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
             const int c = run[w][e];
             run[w][e] = at;
             at += c;
@@ -377,28 +447,33 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     }
     __syncthreads();
     volatile int *next = run[wave];
-    for (int i = 0; i < kPlanRun; i += 64) {
-        const int64_t s = s0 + i + lane;
-        if (s0 + i >= a.S) break;
-        const int e = slot_expert(a, s);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int64_t s = s0 + i * 64 + lane;
+        const int e = ex[i];
         // the lanes of this step with the same expert
         uint64_t same = __ballot(e >= 0);
-        for (int b = 0; (1 << b) < a.E; ++b) {
-            const uint64_t m = __ballot((e >> b) & 1);
-            same &= ((e >> b) & 1) ? m : ~m;
+        if (same) {
+            for (int b = 0; (1 << b) < a.E; ++b) {
+                const uint64_t m = __ballot((e >> b) & 1);
+                same &= ((e >> b) & 1) ? m : ~m;
+            }
+            int row = -1;
+            const uint64_t lower = same & ((1ull << lane) - 1);
+            if (e >= 0) row = next[e] + __popcll(lower);
+            __builtin_amdgcn_wave_barrier();
+            if (e >= 0 && lower == 0) next[e] = row + __popcll(same);
+            __builtin_amdgcn_wave_barrier();
+            if (row >= 0) {
+                a.row_of_slot[s] = row;
+                a.token_of_row[row] = (int32_t)(s / a.k);
+            }
         }
-        int row = -1;
-        const uint64_t lower = same & ((1ull << lane) - 1);
-        if (e >= 0) row = next[e] + __popcll(lower);
-        __builtin_amdgcn_wave_barrier();
-        if (e >= 0 && lower == 0) next[e] = row + __popcll(same);
-        __builtin_amdgcn_wave_barrier();
-        if (s < a.S) a.row_of_slot[s] = row;
-        if (row >= 0) a.token_of_row[row] = (int32_t)(s / a.k);
+        if (e < 0 && s < a.S) a.row_of_slot[s] = -1;
     }
     // rows past the last expert's
-    for (int i = tid; i < kPlanChunk; i += kPlanThreads) {
-        const int64_t r = (int64_t)blockIdx.x * kPlanChunk + i;
+    for (int i = tid; i < CHUNK; i += THREADS) {
+        const int64_t r = (int64_t)blockIdx.x * CHUNK + i;
         if (r >= total && r < a.S) a.token_of_row[r] = -1;
     }
 }
