@@ -427,7 +427,7 @@ def version():
 # that importing the package stays as light as it was
 _MOE_NAMES = ("Plan", "moe_route", "moe_route_bwd", "moe_plan", "moe_plan_workspace_bytes", "moe_gather", "moe_combine",
               "moe_combine_bwd", "grouped_linear", "grouped_linear_bwd", "grouped_weight_grad",
-              "grouped_workspace_bytes")
+              "grouped_workspace_bytes", "grouped_grad_workspace_bytes")
 
 
 def __getattr__(name):

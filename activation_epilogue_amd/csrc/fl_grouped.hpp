@@ -33,6 +33,8 @@ struct GroupedArgs {
     int tiles_n;
     int group;               // row tiles per band of the tile order
     int spread;              // nonzero: each XCD takes its share of every expert's tiles
+    int parts;               // K is summed in 4, 8 or 16 parts by different workgroups (1: whole)
+    float *part;             // parts > 1: fp32 sums, (parts, S, N) or, gradient, (parts, E*K, N)
     int max_tiles;           // limit on the tiles found from the offsets
 };
 
@@ -96,13 +98,14 @@ __device__ __forceinline__ RunTile find_run_tile(const GroupedArgs &a, int bm, i
 // ----------------------------------------------------- the bias gradient
 
 // dbias[e] = the sum of expert e's rows of G: a block sums 128 columns of one
-// expert in 16 groups of rows (group g: rows g, g+16, ..), then adds the groups
-// in order.  A pass over G of its own: 1/K of the operations of dW.
-constexpr int kColumns = 128, kRowGroups = 16;
+// expert in 64 groups of rows (group g: rows g, g+64, ..), then adds the groups
+// in order.  A pass over G of its own: 1/K of the operations of dW.  Many rows
+// in flight per block, because few columns make few blocks.
+constexpr int kColumns = 128, kRowGroups = 64;
 typedef uint32_t u32x4_unaligned __attribute__((ext_vector_type(4), aligned(2)));
 
 template <int DT>
-__global__ void __launch_bounds__(256) grouped_column_sum_kernel(GroupedArgs a) {
+__global__ void __launch_bounds__(1024) grouped_column_sum_kernel(GroupedArgs a) {
     using io = Io<DT>;
     using raw = typename io::raw;
     // a thread's 8 columns, in 16-byte loads (which may be unaligned); at the
@@ -141,11 +144,72 @@ __global__ void __launch_bounds__(256) grouped_column_sum_kernel(GroupedArgs a) 
     for (int t = 0; t < PER; ++t)
         if (at + t >= c) part[g][at + t - c0] = sum[t];
     __syncthreads();
-    if (threadIdx.x < kColumns && c0 + (int)threadIdx.x < a.N) {
-        float s = 0.0f;
+    constexpr int SEGS = 1024 / kColumns;
+    const int col = threadIdx.x % kColumns, seg = threadIdx.x / kColumns;
+    float s = 0.0f;
+    if (c0 + col < a.N) {
 #pragma unroll
-        for (int i = 0; i < kRowGroups; ++i) s += part[i][threadIdx.x];
-        a.dbias[(int64_t)e * a.N + c0 + threadIdx.x] = s;
+        for (int i = 0; i < kRowGroups / SEGS; ++i) s += part[seg * (kRowGroups / SEGS) + i][col];
+        part[seg * (kRowGroups / SEGS)][col] = s;
+    }
+    __syncthreads();
+    if (seg == 0 && c0 + col < a.N) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < SEGS; ++i) s += part[i * (kRowGroups / SEGS)][col];
+        a.dbias[(int64_t)e * a.N + c0 + col] = s;
+    }
+}
+
+// ------------------------------------------------------ joining parts of K
+
+// Adds the parts' sums in order and ends as the tiles' epilogue does.  Forward:
+// a block takes 1024 columns of one row; gradient: of one row of dW.
+template <int DT, int FORM>
+__global__ void __launch_bounds__(256) grouped_join_kernel(GroupedArgs a, int act) {
+    using io = Io<DT>;
+    using raw = typename io::raw;
+    const int64_t r = blockIdx.x, rows = gridDim.x;
+    int e = -1;
+    if constexpr (FORM == kFormFwd) {  // the row's expert, the first whose run has it
+        for (int e0 = 0; e0 < a.E && e < 0; e0 += 64) {
+            const int x = e0 + (threadIdx.x & 63);
+            const uint64_t has = __ballot(x < a.E && r >= run_bound(a, x) && r < run_bound(a, x + 1));
+            if (has) e = e0 + __builtin_ctzll(has);
+        }
+        if (e < 0) return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = blockIdx.y * 1024 + i * 256 + threadIdx.x;
+        if (c >= a.N) break;
+        const int64_t o = r * a.N + c;
+        float d = 0.0f;
+        for (int p = 0; p < a.parts; p += 4) {  // (4, 8 or 16 parts)
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = a.part[(p + i) * rows * a.N + o];
+            d += v[0];
+            d += v[1];
+            d += v[2];
+            d += v[3];
+        }
+        if constexpr (FORM == kFormGrad) {
+            if (a.dw_f32)
+                static_cast<float *>(a.out)[o] = d;
+            else
+                static_cast<raw *>(a.out)[o] = io::from_f32(d);
+        } else {
+            const float x =
+                d + (a.bias ? io::to_f32(static_cast<const raw *>(a.bias)[(int64_t)e * a.N + c]) : 0.0f);
+            const float y = act == FL_ACT_GLU ? io::to_f32(static_cast<const raw *>(a.Y)[o]) : 0.0f;
+            const float v = act == FL_ACT_RELU        ? activate<FL_ACT_RELU>(x, y)
+                            : act == FL_ACT_GELU_TANH ? activate<FL_ACT_GELU_TANH>(x, y)
+                            : act == FL_ACT_GLU       ? activate<FL_ACT_GLU>(x, y)
+                                                      : activate<FL_ACT_NONE>(x, y);
+            if (a.out2) static_cast<raw *>(a.out2)[o] = io::from_f32(x);
+            static_cast<raw *>(a.out)[o] = io::from_f32(v);
+        }
     }
 }
 
@@ -158,17 +222,20 @@ __global__ void __launch_bounds__(256) grouped_column_sum_kernel(GroupedArgs a) 
 struct GroupedTileShape {
     int bm, bn, per_cu;
     float time;
-    bool grad;  // compiled for the gradient too
+    float stage;  // us of one stage where a CU has one workgroup
+    bool grad;    // compiled for the gradient too
 };
 enum GroupedVariant { kTile256x256 = 0, kTile256x128, kTile128x128, kTile64x128, kTile32x128, kTileF32, kGroupedVariants };
 constexpr GroupedTileShape kGroupedTiles[kGroupedVariants] = {
-    {256, 256, 1, 1.0f, true}, {256, 128, 1, 0.54f, false}, {128, 128, 2, 0.64f, true},
-    {64, 128, 2, 0.425f, false}, {32, 128, 2, 0.35f, false}, {64, 64, 3, 1.0f, true}};
+    {256, 256, 1, 1.0f, 1.9f, true}, {256, 128, 1, 0.54f, 0.95f, false}, {128, 128, 2, 0.64f, 0.5f, true},
+    {64, 128, 2, 0.425f, 0.25f, false}, {32, 128, 2, 0.35f, 0.23f, false}, {64, 64, 3, 1.0f, 0.58f, true}};
 typedef void (*grouped_launcher)(const GroupedArgs &, int act, int64_t grid, hipStream_t);
 // One dtype and form to a compiled unit.
 template <int DT, int FORM>
 grouped_launcher pick_grouped(int variant);
 template <int DT>
 void launch_column_sum(const GroupedArgs &a, hipStream_t s);
+template <int DT, int FORM>
+void launch_join(const GroupedArgs &a, int act, hipStream_t s);
 
 }  // namespace fl

@@ -486,22 +486,26 @@ struct GroupedTile {
 
     struct Tile {
         int e, tn;     // expert, column tile
+        int part;      // part of the sum
         int depth;     // summed elements
         int lo;        // first row of the run
         int m0, rows;  // first output row (within the operands: of all rows, or of the expert's dW), rows that exist
     };
 
-    template <int ACT>
+    // PART: the fp32 sums go to the tile's part of a.part, and no further.
+    template <int ACT, bool PART = false>
     __device__ __forceinline__ static void epilogue(const GroupedArgs &a, const Tile &t, int wave, int lane,
                                                     const f32x4_t (&acc)[NRB][NI], FL_LDS char *lds) {
         const int rows = t.rows, n0 = t.tn * BN;
         const int64_t row0 = FORM == kFormGrad ? (int64_t)t.e * a.K + t.m0 : t.m0;
         const int wm = row_of(wave), wn = col_of(wave);
         constexpr int CPR = TN / 8, RPP = 64 / CPR, PASSES = 16 / RPP;  // lanes per row, rows and passes per row block
-        const int es = FORM == kFormGrad && a.dw_f32 ? 4 : ES;
+        const int es = PART || (FORM == kFormGrad && a.dw_f32) ? 4 : ES;
         const int64_t org = row0 * a.N + n0;
         const size_t bytes = ((size_t)rows * a.N - n0) * es;
-        const __amdgpu_buffer_rsrc_t rO = make_rsrc(static_cast<char *>(a.out) + org * es, bytes);
+        const int64_t all_rows = FORM == kFormGrad ? (int64_t)a.E * a.K : a.S;
+        void *to = PART ? static_cast<void *>(a.part + t.part * all_rows * a.N) : a.out;
+        const __amdgpu_buffer_rsrc_t rO = make_rsrc(static_cast<char *>(to) + org * es, bytes);
         const __amdgpu_buffer_rsrc_t rO2 =
             make_rsrc(a.out2 ? static_cast<char *>(a.out2) + org * ES : nullptr, a.out2 ? bytes : 0);
         const __amdgpu_buffer_rsrc_t rY =
@@ -515,7 +519,7 @@ struct GroupedTile {
             return row < rows && valid > 0 ? (uint32_t)(row * a.N + col) * es : kOob;
         };
         Octet bias{};
-        if constexpr (FORM == kFormFwd) {
+        if constexpr (FORM == kFormFwd && !PART) {
             if (a.bias) {
                 const __amdgpu_buffer_rsrc_t rB = make_rsrc(
                     static_cast<const char *>(a.bias) + ((int64_t)t.e * a.N + n0) * ES, (size_t)(a.N - n0) * ES);
@@ -551,7 +555,9 @@ struct GroupedTile {
                 for (int i = 0; i < 8; ++i) {
                     const float d = i < 4 ? lo[i & 3] : hi[i & 3];
                     const float y = NEED_Y ? yv[mi & 1][p].get(i) : 0.0f;
-                    if constexpr (FORM == kFormFwd) {
+                    if constexpr (PART) {
+                        v[i] = d;
+                    } else if constexpr (FORM == kFormFwd) {
                         const float x = d + bias.get(i);
                         v2[i] = x;
                         v[i] = activate<ACT>(x, y);
@@ -564,11 +570,11 @@ struct GroupedTile {
                         v[i] = d;
                     }
                 }
-                if (FORM == kFormGrad && a.dw_f32)
+                if (PART || (FORM == kFormGrad && a.dw_f32))
                     store8_f32(v, rO, off, valid);
                 else
                     store8(v, rO, off, valid);
-                if (FORM == kFormFwd ? a.out2 != nullptr : FORM == kFormBwd && ACT == FL_ACT_GLU)
+                if (!PART && (FORM == kFormFwd ? a.out2 != nullptr : FORM == kFormBwd && ACT == FL_ACT_GLU))
                     store8(v2, rO2, off, valid);
             }
             asm volatile("" ::: "memory");
@@ -582,7 +588,14 @@ struct GroupedTile {
     // expert's tiles are ordered in bands of a.group row tiles swept column by
     // column.
     __device__ __forceinline__ static bool find(const GroupedArgs &a, int b, int n, Tile &t) {
-        if (b >= n) return false;
+        t.part = 0;
+        if (a.parts > 1) {
+            t.part = b / n;
+            if (t.part >= a.parts) return false;
+            b -= t.part * n;
+        } else if (b >= n) {
+            return false;
+        }
         int m;
         if constexpr (FORM == kFormGrad) {
             // (an expert's tiles cost as much as it has rows, so always spread)
@@ -617,25 +630,34 @@ struct GroupedTile {
         t.lo = __builtin_amdgcn_readfirstlane(t.lo);
         t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
         t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+        t.part = __builtin_amdgcn_readfirstlane(t.part);
         return true;
     }
 
     __device__ __forceinline__ static void setup(const GroupedArgs &a, const Tile &t, int wave, int lane, Ops &o) {
         const int n0 = t.tn * BN;
+        int k0 = 0;  // the part's first k
         o.depth = t.depth;
+        if (FORM != kFormBwd && a.parts > 1) {
+            const int stages = (int)(((int64_t)t.depth + KS - 1) / KS);
+            const int64_t len = (int64_t)((stages + a.parts - 1) / a.parts) * KS, k = t.part * len;
+            k0 = k < t.depth ? (int)k : t.depth;
+            o.depth = t.depth - k0 < len ? t.depth - k0 : (int)len;
+        }
         o.lda = a.K;
         o.ldb = FORM == kFormBwd ? a.K : a.N;
         if constexpr (FORM == kFormGrad) {
-            o.pa = static_cast<const char *>(a.A) + ((int64_t)t.lo * a.K + t.m0) * ES;
-            o.pb = static_cast<const char *>(a.B) + ((int64_t)t.lo * a.N + n0) * ES;
-            o.ra = (int64_t)(a.S - t.lo) * a.K - t.m0;
-            o.rb = (int64_t)(a.S - t.lo) * a.N - n0;
+            const int64_t r0 = (int64_t)t.lo + k0;
+            o.pa = static_cast<const char *>(a.A) + (r0 * a.K + t.m0) * ES;
+            o.pb = static_cast<const char *>(a.B) + (r0 * a.N + n0) * ES;
+            o.ra = (a.S - r0) * a.K - t.m0;
+            o.rb = (a.S - r0) * a.N - n0;
             set_descriptors(o);
         } else {
-            const int64_t a0 = FORM == kFormFwd && a.index ? 0 : (int64_t)t.m0 * a.K;
+            const int64_t a0 = (FORM == kFormFwd && a.index ? 0 : (int64_t)t.m0 * a.K) + k0;
             o.ra = a.A_rows * a.K - a0;
-            o.A.rsrc = sgpr_rsrc(static_cast<const char *>(a.A) + a0 * ES, (size_t)o.ra * ES);
-            const int64_t b0 = (int64_t)t.e * a.K * a.N + (FORM == kFormBwd ? (int64_t)n0 * a.K : n0);
+            o.A.rsrc = sgpr_rsrc(static_cast<const char *>(a.A) + a0 * ES, o.ra > 0 ? (size_t)o.ra * ES : 0);
+            const int64_t b0 = (int64_t)t.e * a.K * a.N + (FORM == kFormBwd ? (int64_t)n0 * a.K : (int64_t)k0 * a.N + n0);
             o.rb = (int64_t)a.E * a.K * a.N - b0;
             o.B.rsrc = sgpr_rsrc(static_cast<const char *>(a.B) + b0 * ES, (size_t)o.rb * ES);
         }
@@ -706,6 +728,8 @@ struct GroupedTile {
             FL_LDS char *epi = lds + (NBUF - 1) * BUF_BYTES;
             if (idle)
                 ;
+            else if (FORM != kFormBwd && a.parts > 1)
+                epilogue<FL_ACT_NONE, true>(a, t, wave, le, acc, epi);
             else if (FORM == kFormGrad || act == FL_ACT_NONE)
                 epilogue<FL_ACT_NONE>(a, t, wave, le, acc, epi);
             else if (act == FL_ACT_RELU)

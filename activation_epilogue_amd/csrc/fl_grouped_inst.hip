@@ -1,5 +1,5 @@
 // fl_grouped_inst.hip -- instantiates the experts' products for one dtype and
-// one form (and the column sum with the gradient).  Built once per dtype and
+// one form (and the join of parts, and with the gradient the column sum).  Built once per dtype and
 // form with -DFL_INST_DTYPE=<fl_dtype value> -DFL_INST_FORM=<form>.
 #include "fl_grouped_dma.hpp"
 
@@ -34,7 +34,16 @@ grouped_launcher pick_grouped<FL_INST_DTYPE, FL_INST_FORM>(int variant) {
 template <>
 void launch_column_sum<FL_INST_DTYPE>(const GroupedArgs &a, hipStream_t s) {
     const unsigned blocks = (unsigned)a.E * (unsigned)((a.N + kColumns - 1) / kColumns);
-    hipLaunchKernelGGL((grouped_column_sum_kernel<FL_INST_DTYPE>), dim3(blocks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((grouped_column_sum_kernel<FL_INST_DTYPE>), dim3(blocks), dim3(1024), 0, s, a);
+}
+#endif
+
+#if FL_INST_FORM != 1
+template <>
+void launch_join<FL_INST_DTYPE, FL_INST_FORM>(const GroupedArgs &a, int act, hipStream_t s) {
+    const unsigned rows = FL_INST_FORM == 2 ? (unsigned)((int64_t)a.E * a.K) : (unsigned)a.S;
+    hipLaunchKernelGGL((grouped_join_kernel<FL_INST_DTYPE, FL_INST_FORM>), dim3(rows, (a.N + 1023) / 1024), dim3(256), 0,
+                       s, a, act);
 }
 #endif
 

@@ -203,8 +203,6 @@ int64_t most_row_tiles(int64_t S, int64_t E, int64_t bm) {
     return (S + runs * (bm - 1)) / bm;
 }
 
-size_t grouped_workspace(int64_t, int64_t, int64_t, int64_t, int) { return 0; }
-
 template <int DT>
 fl::grouped_launcher pick_grouped_dt(int form, int variant) {
     return form == fl::kFormFwd   ? fl::pick_grouped<DT, fl::kFormFwd>(variant)
@@ -218,17 +216,45 @@ fl::grouped_launcher pick_grouped(int dtype, int form, int variant) {
                              : pick_grouped_dt<FL_BF16>(form, variant);
 }
 
+template <int FORM>
+void join_form(int dtype, const fl::GroupedArgs &a, int act, hipStream_t st) {
+    if (dtype == FL_F32)
+        fl::launch_join<FL_F32, FORM>(a, act, st);
+    else if (dtype == FL_F16)
+        fl::launch_join<FL_F16, FORM>(a, act, st);
+    else
+        fl::launch_join<FL_BF16, FORM>(a, act, st);
+}
+
+void join(int dtype, int form, const fl::GroupedArgs &a, int act, hipStream_t st) {
+    if (form == fl::kFormGrad)
+        join_form<fl::kFormGrad>(dtype, a, act, st);
+    else
+        join_form<fl::kFormFwd>(dtype, a, act, st);
+}
+
 // The tile: the one of least estimated time, in rounds of
 // a full chip.  Runs end inside a tile, so S rows in R runs make about S/bm +
 // R/2 row tiles (at least R); rounds beyond the first end ragged, half a round
 // on average.
-int pick_variant(int dtype, int form, int64_t S, int64_t N, int64_t K, int64_t E) {
-    if (dtype == FL_F32) return fl::kTileF32;
-    int best = -1;
-    double least = 0.0;
-    for (int v = 0; v < fl::kTileF32; ++v) {
+//
+// Where the chosen tiles leave most of the chip idle and the sum is long, it is
+// cut into 4, 8 or 16 parts for more workgroups, whose fp32 sums another launch
+// joins (4 us and a little per part), if that takes clearly less time than the
+// stages of one workgroup, as far as the memory (6 TB/s) can follow.  Measured without and
+// with: bf16, one token through 2 of 8 experts, K 4096, N 1024: 19.4 -> 14.1 us;
+// fp32: 75.8 -> 20.8 us; weight gradient of 16384 rows, 2 experts, 256x256: 67.7
+// -> 15.9 us.
+struct GroupedPlan {
+    int variant, parts;
+};
+
+GroupedPlan plan_grouped(int dtype, int form, int64_t S, int64_t N, int64_t K, int64_t E) {
+    GroupedPlan best{-1, 1};
+    double least = 0.0, tiles = 0.0;
+    for (int v = 0; v < fl::kGroupedVariants; ++v) {
         const fl::GroupedTileShape &t = fl::kGroupedTiles[v];
-        if (form == fl::kFormGrad && !t.grad) continue;
+        if ((v == fl::kTileF32) != (dtype == FL_F32) || (form == fl::kFormGrad && !t.grad)) continue;
         double m;
         if (form == fl::kFormGrad) {
             m = (double)E * ((K + t.bm - 1) / t.bm);
@@ -237,20 +263,42 @@ int pick_variant(int dtype, int form, int64_t S, int64_t N, int64_t K, int64_t E
             m = (double)S / t.bm + 0.5 * runs;
             m = m > runs ? m : runs;
         }
-        const double x = m * ((N + t.bn - 1) / t.bn) / (kCus * t.per_cu);
+        m *= (N + t.bn - 1) / t.bn;
+        const double x = m / (kCus * t.per_cu);
         const double time = t.time * (x < 0.9 ? 1.0 : x + 0.5);
-        if (best < 0 || time < least) {
+        if (best.variant < 0 || time < least) {
             least = time;
-            best = v;
+            tiles = m;
+            best.variant = v;
+        }
+    }
+    const int64_t ks = dtype == FL_F32 ? 32 : 64, depth = form == fl::kFormGrad ? S / E : K;
+    const fl::GroupedTileShape &t = fl::kGroupedTiles[best.variant];
+    const double stages = (double)((depth + ks - 1) / ks);
+    const double memory = tiles * stages * (t.bm + t.bn) * 128 / 6e6;
+    double limit = 0.85 * (4.0 + (stages * t.stage > memory ? stages * t.stage : memory));  // a clear gain, or none
+    for (int p = 4; form != fl::kFormBwd && p <= 16 && p * 4 <= stages && p * tiles <= kCus * t.per_cu; p *= 2) {
+        const double each = stages / p * t.stage;
+        const double time = 8.0 + 0.1 * p + (each > memory ? each : memory);
+        if (time < limit) {
+            limit = time;
+            best.parts = p;
         }
     }
     return best;
 }
 
-fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void *stream, const char *what) {
+size_t grouped_workspace(int form, int64_t S, int64_t N, int64_t K, int64_t E, int dtype) {
+    if (S == 0 || N == 0 || K == 0) return 0;
+    const GroupedPlan p = plan_grouped(dtype, form, S, N, K, E);
+    return p.parts > 1 ? (size_t)p.parts * (form == fl::kFormGrad ? E * K : S) * N * 4 : 0;
+}
+
+fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void *workspace, void *stream,
+                         const char *what) {
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const int v = pick_variant(dtype, form, a.S, a.N, a.K, a.E);
-    const fl::GroupedTileShape &t = fl::kGroupedTiles[v];
+    const GroupedPlan p = plan_grouped(dtype, form, a.S, a.N, a.K, a.E);
+    const fl::GroupedTileShape &t = fl::kGroupedTiles[p.variant];
     a.tiles_n = (int)((a.N + t.bn - 1) / t.bn);
     // bands of 8 row tiles: prompts through 64 experts 210 us, 218 with 4 or
     // 16; weight gradient (operands of equal height) 1614 us with 4, 1627 with 8
@@ -259,10 +307,12 @@ fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void 
     // but the work is even whatever the runs' lengths: 1780 against 1820 us
     // where an expert has 470 tiles, 233 against 210 us where it has 22.
     a.spread = (int64_t)a.S / a.E / t.bm * a.tiles_n >= 128;
+    a.parts = workspace ? p.parts : 1;
+    a.part = static_cast<float *>(workspace);
     const int64_t tiles_m = form == fl::kFormGrad ? a.E * (((int64_t)a.K + t.bm - 1) / t.bm) : most_row_tiles(a.S, a.E, t.bm);
-    const int64_t grid = tiles_m * a.tiles_n;
+    const int64_t tiles = tiles_m * a.tiles_n, grid = tiles * a.parts, slots = kCus * t.per_cu;
     if (grid > kMaxDim) return fail(FL_ERR_UNSUPPORTED, "too many output tiles");
-    a.max_tiles = (int)grid;
+    a.max_tiles = (int)tiles;
     if (form == fl::kFormGrad && a.dbias) {
         if (dtype == FL_F32)
             fl::launch_column_sum<FL_F32>(a, st);
@@ -274,8 +324,12 @@ fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void 
         if (s != FL_OK) return s;
     }
     if (grid == 0) return FL_OK;
-    const int64_t slots = kCus * t.per_cu;
-    pick_grouped(dtype, form, v)(a, act, grid < slots ? grid : slots, st);
+    pick_grouped(dtype, form, p.variant)(a, act, grid < slots ? grid : slots, st);
+    if (a.parts > 1) {
+        const fl_status s = check_launch(what);
+        if (s != FL_OK) return s;
+        join(dtype, form, a, act, st);
+    }
     return check_launch(what);
 }
 
@@ -482,7 +536,16 @@ fl_status fl_grouped_workspace_bytes(int64_t S, int64_t N, int64_t K, int64_t E,
     if (!bytes) return fail(FL_ERR_INVALID_ARG, "bytes is NULL");
     const fl_status s = check_grouped(S, N, K, E, FL_ACT_NONE, dtype);
     if (s != FL_OK) return s;
-    *bytes = grouped_workspace(S, N, K, E, dtype);
+    *bytes = grouped_workspace(fl::kFormFwd, S, N, K, E, dtype);
+    return FL_OK;
+}
+
+fl_status fl_grouped_grad_workspace_bytes(int64_t S, int64_t N, int64_t K, int64_t E, fl_dtype dtype, size_t *bytes) {
+    clear_error();
+    if (!bytes) return fail(FL_ERR_INVALID_ARG, "bytes is NULL");
+    const fl_status s = check_grouped(S, N, K, E, FL_ACT_NONE, dtype);
+    if (s != FL_OK) return s;
+    *bytes = grouped_workspace(fl::kFormGrad, S, N, K, E, dtype);
     return FL_OK;
 }
 
@@ -494,7 +557,7 @@ fl_status fl_grouped_linear(const void *A, const int32_t *index, const int32_t *
     fl_status s = check_grouped(S, N, K, E, act, dtype);
     if (s != FL_OK) return s;
     if ((s = check_sizes({A_rows})) != FL_OK) return s;
-    const size_t need = grouped_workspace(S, N, K, E, dtype);
+    const size_t need = grouped_workspace(fl::kFormFwd, S, N, K, E, dtype);
     const size_t es = elem_size(dtype), o_bytes = (size_t)S * N * es;
     if (!index && A_rows < S)
         return fail(FL_ERR_INVALID_ARG, "A has %lld rows, %lld needed without an index", (long long)A_rows,
@@ -530,7 +593,7 @@ fl_status fl_grouped_linear(const void *A, const int32_t *index, const int32_t *
     a.N = (int)N;
     a.K = (int)K;
     a.E = (int)E;
-    return launch_grouped(a, fl::kFormFwd, act, dtype, stream, "grouped_linear");
+    return launch_grouped(a, fl::kFormFwd, act, dtype, need ? workspace : nullptr, stream, "grouped_linear");
 }
 
 fl_status fl_grouped_linear_bwd(const void *G, const int32_t *offsets, const void *W, const void *X, const void *Y,
@@ -566,12 +629,18 @@ fl_status fl_grouped_linear_bwd(const void *G, const int32_t *offsets, const voi
     a.N = (int)N;
     a.K = (int)K;
     a.E = (int)E;
-    return launch_grouped(a, fl::kFormBwd, act, dtype, stream, "grouped_linear_bwd");
+    return launch_grouped(a, fl::kFormBwd, act, dtype, nullptr, stream, "grouped_linear_bwd");
 }
 
 fl_status fl_grouped_weight_grad(const void *A, const void *G, const int32_t *offsets, void *dW, float *dbias,
                                  int64_t S, int64_t N, int64_t K, int64_t E, fl_dtype dtype, fl_dtype dw_dtype,
                                  void *stream) {
+    return fl_grouped_weight_grad_ws(A, G, offsets, dW, dbias, S, N, K, E, dtype, dw_dtype, nullptr, 0, stream);
+}
+
+fl_status fl_grouped_weight_grad_ws(const void *A, const void *G, const int32_t *offsets, void *dW, float *dbias,
+                                    int64_t S, int64_t N, int64_t K, int64_t E, fl_dtype dtype, fl_dtype dw_dtype,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
     clear_error();
     fl_status s = check_grouped(S, N, K, E, FL_ACT_NONE, dtype);
     if (s != FL_OK) return s;
@@ -579,12 +648,16 @@ fl_status fl_grouped_weight_grad(const void *A, const void *G, const int32_t *of
         return fail(FL_ERR_INVALID_ARG, "dW is in the operands' dtype or fp32 (got %d)", (int)dw_dtype);
     if ((size_t)N * elem_size(dw_dtype) * 256 >= kTwoGiB)
         return fail(FL_ERR_UNSUPPORTED, "N too large (256 rows of dW must span < 2 GiB)");
+    const size_t need = grouped_workspace(fl::kFormGrad, S, N, K, E, dtype);
+    if (workspace && workspace_bytes < need)
+        return fail(FL_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     const size_t es = elem_size(dtype), des = elem_size(dw_dtype);
     const Operand ops[] = {{"A", A, (size_t)S * K * es, es, false, N == 0, nullptr},
                            {"G", G, (size_t)S * N * es, es, false, false, nullptr},
                            {"offsets", offsets, (size_t)(E + 1) * 4, 4, false, false, nullptr},
                            {"dW", dW, (size_t)E * K * N * des, des, true, false, nullptr},
-                           {"dbias", dbias, (size_t)E * N * 4, 4, true, true, nullptr}};
+                           {"dbias", dbias, (size_t)E * N * 4, 4, true, true, nullptr},
+                           {"workspace", workspace, workspace ? need : 0, 16, true, true, nullptr}};
     if ((s = check_operands(ops)) != FL_OK) return s;
     if (N == 0 || (K == 0 && !dbias)) return FL_OK;
     fl::GroupedArgs a{};
@@ -599,7 +672,7 @@ fl_status fl_grouped_weight_grad(const void *A, const void *G, const int32_t *of
     a.N = (int)N;
     a.K = (int)K;
     a.E = (int)E;
-    return launch_grouped(a, fl::kFormGrad, FL_ACT_NONE, dtype, stream, "grouped_weight_grad");
+    return launch_grouped(a, fl::kFormGrad, FL_ACT_NONE, dtype, need ? workspace : nullptr, stream, "grouped_weight_grad");
 }
 
 const char *fl_moe_last_error(void) { return g_err; }

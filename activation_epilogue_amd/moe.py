@@ -19,6 +19,7 @@ The plan's arrays stay on the device: no call waits for the GPU.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -28,7 +29,8 @@ from . import ACTS, FusedLinearError, _dev_ptr, _dtype_code, load_library
 SCORES = {"softmax": 0, "sigmoid": 1}
 MOE_EXPORTS = ("fl_moe_route", "fl_moe_route_bwd", "fl_moe_plan", "fl_moe_plan_workspace_bytes", "fl_moe_gather",
                "fl_moe_combine", "fl_moe_combine_bwd", "fl_grouped_linear", "fl_grouped_workspace_bytes",
-               "fl_grouped_linear_bwd", "fl_grouped_weight_grad", "fl_moe_last_error")
+               "fl_grouped_linear_bwd", "fl_grouped_weight_grad", "fl_grouped_weight_grad_ws",
+               "fl_grouped_grad_workspace_bytes", "fl_moe_last_error")
 
 
 class RouteOptions(ctypes.Structure):
@@ -65,6 +67,8 @@ def _lib():
         lib.fl_grouped_workspace_bytes.argtypes = [i64, i64, i64, i64, c_int, psz]
         lib.fl_grouped_linear_bwd.argtypes = [vp] * 7 + [i64] * 4 + [c_int, c_int, vp]
         lib.fl_grouped_weight_grad.argtypes = [vp] * 5 + [i64] * 4 + [c_int, c_int, vp]
+        lib.fl_grouped_weight_grad_ws.argtypes = [vp] * 5 + [i64] * 4 + [c_int, c_int, vp, sz, vp]
+        lib.fl_grouped_grad_workspace_bytes.argtypes = [i64, i64, i64, i64, c_int, psz]
         for name in MOE_EXPORTS[:-1]:
             getattr(lib, name).restype = c_int
         lib.fl_moe_last_error.restype = ctypes.c_char_p
@@ -81,21 +85,22 @@ class _On:
     """The stream a call runs on: the given one, or the current one of t's
     device; that device and stream are current while the call allocates and
     launches, so its temporary and result tensors belong to that stream."""
+    __slots__ = ("ctx", "index")
 
     def __init__(self, t, stream):
         if not t.is_cuda:
             raise ValueError("operands must be device tensors")
         self.ctx = None
+        self.index = t.device.index
         if stream is not None:
             self.ctx = torch.cuda.stream(stream)
-        elif t.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(t.device)
-        self.device = t.device
+        elif self.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.index)
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -105,7 +110,7 @@ class _On:
 def _out(t, name, shape, dtype, like):
     """`t` checked, or a new tensor where it is None."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     _ptr(t, name, dtype, shape, like)
     return t
 
@@ -117,12 +122,18 @@ def _ptr(t, name, dtype=None, shape=None, like=None):
     return p
 
 
+@functools.lru_cache(maxsize=64)
 def _route_options(score, groups, top_groups, group_top, renorm, scale):
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
     if scale == 0.0:
         raise ValueError("scale must not be 0")
-    return RouteOptions(SCORES[score], int(groups), int(top_groups), int(group_top), 0 if renorm else 1, float(scale))
+    return ctypes.byref(RouteOptions(SCORES[score], int(groups), int(top_groups), int(group_top), 0 if renorm else 1,
+                                     float(scale)))
+
+
+def _bytes(t):
+    return t.numel() * t.element_size() if t is not None else 0
 
 
 def _matrix(t, name):
@@ -145,7 +156,7 @@ def moe_route(logits, k, bias=None, score="softmax", groups=1, top_groups=1, gro
         experts = _out(experts, "experts", (T, k), torch.int32, logits)
         _ok(_lib().fl_moe_route(_ptr(logits, "logits"), _ptr(bias, "bias", torch.float32, (E,), logits),
                                 experts.data_ptr() or None, weights.data_ptr() or None, T, E, k, code,
-                                ctypes.byref(opt), st))
+                                opt, st))
     return weights, experts
 
 
@@ -159,10 +170,11 @@ def moe_route_bwd(logits, experts, dweights, score="softmax", renorm=True, scale
         dlogits = _out(dlogits, "dlogits", (T, E), logits.dtype, logits)
         _ok(_lib().fl_moe_route_bwd(_ptr(logits, "logits"), _ptr(experts, "experts", torch.int32, (T, k), logits),
                                     _ptr(dweights, "dweights", torch.float32, (T, k), logits),
-                                    dlogits.data_ptr() or None, T, E, k, code, ctypes.byref(opt), st))
+                                    dlogits.data_ptr() or None, T, E, k, code, opt, st))
     return dlogits
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_plan_workspace_bytes(T, k, E):
     """Bytes of workspace fl_moe_plan needs."""
     n = ctypes.c_size_t()
@@ -183,11 +195,11 @@ def moe_plan(experts, E, out=None, *, stream=None, workspace=None):
                     _out(o[1], "token_of_row", (T * k,), torch.int32, experts),
                     _out(o[2], "row_of_slot", (T, k), torch.int32, experts))
         if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=experts.device)
+            workspace = experts.new_empty(need, dtype=torch.uint8)
         _ok(_lib().fl_moe_plan(_ptr(experts, "experts", torch.int32), plan.offsets.data_ptr(),
                                plan.token_of_row.data_ptr() or None, plan.row_of_slot.data_ptr() or None, T, k, E,
                                _ptr(workspace, "workspace", None, None, experts),
-                               workspace.numel() * workspace.element_size() if workspace is not None else 0, st))
+                               _bytes(workspace), st))
     return plan
 
 
@@ -233,11 +245,21 @@ def moe_combine_bwd(dout, rows, row_of_slot, weights=None, drows=None, dweights=
     return drows, dweights
 
 
+@functools.lru_cache(maxsize=1024)
 def grouped_workspace_bytes(S, N, K, E, dtype):
     """Bytes of workspace fl_grouped_linear needs."""
     n = ctypes.c_size_t()
     _ok(_lib().fl_grouped_workspace_bytes(S, N, K, E, _dtype_code(dtype) if not isinstance(dtype, int) else dtype,
                                           ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def grouped_grad_workspace_bytes(S, N, K, E, dtype):
+    """Bytes of workspace fl_grouped_weight_grad_ws takes."""
+    n = ctypes.c_size_t()
+    _ok(_lib().fl_grouped_grad_workspace_bytes(S, N, K, E, _dtype_code(dtype) if not isinstance(dtype, int) else dtype,
+                                               ctypes.byref(n)))
     return n.value
 
 
@@ -260,18 +282,18 @@ def grouped_linear(A, B, offsets, bias=None, Y=None, act="relu", out=None, *, in
     with _On(A, stream) as st:
         out = _out(out, "out", (S, N), dt, A)
         if pre is True:
-            pre = torch.empty((S, N), dtype=dt, device=A.device)
+            pre = A.new_empty((S, N))
         elif pre is False:
             pre = None
         if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=A.device)
+            workspace = A.new_empty(need, dtype=torch.uint8)
         _ok(_lib().fl_grouped_linear(
             _ptr(A, "A"), _ptr(index, "index", torch.int32, (S,), A),
             _ptr(offsets, "offsets", torch.int32, (E + 1,), A), _ptr(B, "B", dt, None, A),
             _ptr(bias, "bias", dt, (E, N), A), _ptr(Y, "Y", dt, (S, N), A), out.data_ptr() or None,
             _ptr(pre, "pre", dt, (S, N), A), A_rows, S, N, K, E, ACTS[act], code,
             _ptr(workspace, "workspace", None, None, A),
-            workspace.numel() * workspace.element_size() if workspace is not None else 0, st))
+            _bytes(workspace), st))
     return out if pre is None else (out, pre)
 
 
@@ -296,25 +318,29 @@ def grouped_linear_bwd(G, W, X, offsets, Y=None, act="relu", dX=None, dY=None, *
     return dX, dY
 
 
-def grouped_weight_grad(A, G, offsets, dbias=True, dW=None, dw_dtype=None, *, stream=None):
+def grouped_weight_grad(A, G, offsets, dbias=True, dW=None, dw_dtype=None, *, stream=None, workspace=None):
     """dW[e] = A[e]^T G[e] over every expert's rows and dbias[e] = the sum of
-    its rows of G (fl_grouped_weight_grad): A (S,K), G (S,N).  dW is (E,K,N) in
-    dw_dtype (the operands' dtype by default, or float32).  dbias=True
+    its rows of G (fl_grouped_weight_grad_ws): A (S,K), G (S,N).  dW is (E,K,N)
+    in dw_dtype (the operands' dtype by default, or float32).  dbias=True
     allocates the (E,N) fp32 result, a tensor is overwritten, None/False skips
     it.  Returns (dW, dbias or None)."""
     S, K = _matrix(A, "A")
     N = _matrix(G, "G")[1]
     E = offsets.numel() - 1
     dt = A.dtype
+    code = _dtype_code(dt)
     dw_dtype = dw_dtype or (dW.dtype if dW is not None else dt)
+    need = grouped_grad_workspace_bytes(S, N, K, E, code)
     with _On(A, stream) as st:
         dW = _out(dW, "dW", (E, K, N), dw_dtype, A)
         if dbias is True:
-            dbias = torch.empty((E, N), dtype=torch.float32, device=A.device)
+            dbias = A.new_empty((E, N), dtype=torch.float32)
         elif dbias is False:
             dbias = None
-        _ok(_lib().fl_grouped_weight_grad(
+        if need and workspace is None:
+            workspace = A.new_empty(need, dtype=torch.uint8)
+        _ok(_lib().fl_grouped_weight_grad_ws(
             _ptr(A, "A"), _ptr(G, "G", dt, (S, N), A), _ptr(offsets, "offsets", torch.int32, (E + 1,), A),
-            dW.data_ptr() or None, _ptr(dbias, "dbias", torch.float32, (E, N), A), S, N, K, E, _dtype_code(dt),
-            _dtype_code(dw_dtype), st))
+            dW.data_ptr() or None, _ptr(dbias, "dbias", torch.float32, (E, N), A), S, N, K, E, code,
+            _dtype_code(dw_dtype), _ptr(workspace, "workspace", None, None, A), _bytes(workspace), st))
     return dW, dbias

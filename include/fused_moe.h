@@ -168,6 +168,14 @@ fl_status fl_grouped_linear_bwd(const void *G, const int32_t *offsets, const voi
 fl_status fl_grouped_weight_grad(const void *A, const void *G, const int32_t *offsets, void *dW, float *dbias,
                                  int64_t S, int64_t N, int64_t K, int64_t E, fl_dtype dtype, fl_dtype dw_dtype,
                                  void *stream);
+/* The same with a workspace of fl_grouped_grad_workspace_bytes(S, N, K, E,
+ * dtype) bytes, 16-byte aligned: long runs of a small dW are summed in parts
+ * that meet there in a fixed order (the rounding of fp32 sums may then differ
+ * from the call without).  NULL: no parts. */
+fl_status fl_grouped_weight_grad_ws(const void *A, const void *G, const int32_t *offsets, void *dW, float *dbias,
+                                    int64_t S, int64_t N, int64_t K, int64_t E, fl_dtype dtype, fl_dtype dw_dtype,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+fl_status fl_grouped_grad_workspace_bytes(int64_t S, int64_t N, int64_t K, int64_t E, fl_dtype dtype, size_t *bytes);
 
 const char *fl_moe_last_error(void); /* thread-local; "" when none */
 
