@@ -123,29 +123,40 @@ fl_status check_route(int64_t T, int64_t E, int64_t k, int dtype) {
     return check_slots(T, k);
 }
 
-// Registers per lane for E experts: 1, 2, 4, 8 or 16.
-template <int DT, bool BWD, int EPL>
-void launch_route_epl(const fl::RouteArgs &a, int grid, hipStream_t st) {
+// Teams of 16 lanes wherever a team holds the experts (8 to a lane, 16 where
+// there are tokens enough to hide the longer steps), the choices and the runs;
+// else whole waves.
+template <int DT, bool BWD, int EPL, int TEAM>
+void launch_route_team(const fl::RouteArgs &a, hipStream_t st) {
+    constexpr int TOKENS = 256 / TEAM;
+    const int64_t blocks = ((int64_t)a.T + TOKENS - 1) / TOKENS;
+    const dim3 grid((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20));
     if (BWD)
-        hipLaunchKernelGGL((fl::route_bwd_kernel<DT, EPL>), dim3(grid), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fl::route_bwd_kernel<DT, EPL, TEAM>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((fl::route_kernel<DT, EPL>), dim3(grid), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fl::route_kernel<DT, EPL, TEAM>), grid, dim3(256), 0, st, a);
+}
+
+template <int DT, bool BWD, int TEAM>
+void launch_route_dt(const fl::RouteArgs &a, hipStream_t st) {
+    if (a.E <= TEAM)
+        launch_route_team<DT, BWD, 1, TEAM>(a, st);
+    else if (a.E <= 2 * TEAM)
+        launch_route_team<DT, BWD, 2, TEAM>(a, st);
+    else if (a.E <= 4 * TEAM)
+        launch_route_team<DT, BWD, 4, TEAM>(a, st);
+    else if (a.E <= 8 * TEAM)
+        launch_route_team<DT, BWD, 8, TEAM>(a, st);
+    else
+        launch_route_team<DT, BWD, 16, TEAM>(a, st);
 }
 
 template <int DT, bool BWD>
 void launch_route_dt(const fl::RouteArgs &a, hipStream_t st) {
-    const int64_t blocks = ((int64_t)a.T + 3) / 4;
-    const int grid = (int)(blocks < 1 << 20 ? blocks : 1 << 20);
-    if (a.E <= 64)
-        launch_route_epl<DT, BWD, 1>(a, grid, st);
-    else if (a.E <= 128)
-        launch_route_epl<DT, BWD, 2>(a, grid, st);
-    else if (a.E <= 256)
-        launch_route_epl<DT, BWD, 4>(a, grid, st);
-    else if (a.E <= 512)
-        launch_route_epl<DT, BWD, 8>(a, grid, st);
+    if (a.E <= (a.T < 4096 ? 128 : 256) && a.k <= 16 && a.groups <= 16)
+        launch_route_dt<DT, BWD, 16>(a, st);
     else
-        launch_route_epl<DT, BWD, 16>(a, grid, st);
+        launch_route_dt<DT, BWD, 64>(a, st);
 }
 
 template <bool BWD>

@@ -18,54 +18,73 @@ __device__ __forceinline__ void store_f32(void *p, int64_t i, float v) {
     static_cast<typename Io<DT>::raw *>(p)[i] = Io<DT>::from_f32(v);
 }
 
-// Sums and maxima over the 64 lanes, the same in every lane: moves between
-// neighbouring lanes, then rows of 16, on the vector unit (an LDS permute costs
+// Sums and extremes over a team of 16 or 64 lanes, the same in every lane of
+// it: moves between neighbouring lanes on the vector unit (an LDS permute costs
 // ten times the latency, and a router is a chain of such steps).
-template <int CTRL, int ROWS = 0xf>
-__device__ __forceinline__ float lane_move(float old, float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old),
-                                                                 __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+template <int CTRL, int ROWS = 0xf, class V>
+__device__ __forceinline__ V lane_move(V old, V v) {
+    typedef int words __attribute__((ext_vector_type(sizeof(V) / 4)));
+    words o, w, r;
+    __builtin_memcpy(&o, &old, sizeof(V));
+    __builtin_memcpy(&w, &v, sizeof(V));
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(V) / 4); ++i)
+        r[i] = __builtin_amdgcn_update_dpp(o[i], w[i], CTRL, ROWS, 0xf, false);
+    V out;
+    __builtin_memcpy(&out, &r, sizeof(V));
+    return out;
 }
-template <int CTRL, int ROWS = 0xf>
-__device__ __forceinline__ double lane_move(double old, double v) {
-    typedef int i32x2 __attribute__((ext_vector_type(2)));
-    const i32x2 o = __builtin_bit_cast(i32x2, old), w = __builtin_bit_cast(i32x2, v);
-    return __builtin_bit_cast(double, i32x2{__builtin_amdgcn_update_dpp(o[0], w[0], CTRL, ROWS, 0xf, false),
-                                            __builtin_amdgcn_update_dpp(o[1], w[1], CTRL, ROWS, 0xf, false)});
+template <class V>
+__device__ __forceinline__ V read_lane(V v, int lane) {
+    typedef int words __attribute__((ext_vector_type(sizeof(V) / 4)));
+    words w;
+    __builtin_memcpy(&w, &v, sizeof(V));
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(V) / 4); ++i) w[i] = __builtin_amdgcn_readlane(w[i], lane);
+    V out;
+    __builtin_memcpy(&out, &w, sizeof(V));
+    return out;
 }
-__device__ __forceinline__ float read_lane(float v, int lane) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+struct Add {
+    template <class V> __device__ static V zero(V) { return V(0); }
+    __device__ static float of(float a, float b) { return a + b; }
+    __device__ static double of(double a, double b) { return a + b; }
+};
+struct Larger {  // `zero`: what a lane without a source takes, itself
+    template <class V> __device__ static V zero(V v) { return v; }
+    __device__ static float of(float a, float b) { return __builtin_fmaxf(a, b); }
+    __device__ static double of(double a, double b) { return __builtin_fmax(a, b); }
+};
+struct Lower {
+    template <class V> __device__ static V zero(V v) { return v; }
+    __device__ static int of(int a, int b) { return a < b ? a : b; }
+};
+template <class OP, int TEAM, class V>
+__device__ __forceinline__ V team_reduce(V v) {
+    static_assert(TEAM == 16 || TEAM == 64, "a row of lanes or a wave");
+    if constexpr (TEAM == 16) {
+        // lanes 1 and 2 apart, then mirrored halves and rows: every lane adds
+        // the same pairs (a rotation would not, and its lanes' sums differ)
+        v = OP::of(v, lane_move<0xb1>(v, v));
+        v = OP::of(v, lane_move<0x4e>(v, v));
+        v = OP::of(v, lane_move<0x141>(v, v));
+        return OP::of(v, lane_move<0x140>(v, v));
+    } else {  // shifts of the row by 1, 2, 4, 8: its lane 15 holds the row's; then broadcasts of lanes 15 and 31
+        v = OP::of(v, lane_move<0x111>(OP::zero(v), v));
+        v = OP::of(v, lane_move<0x112>(OP::zero(v), v));
+        v = OP::of(v, lane_move<0x114>(OP::zero(v), v));
+        v = OP::of(v, lane_move<0x118>(OP::zero(v), v));
+        v = OP::of(v, lane_move<0x142, 0xa>(OP::zero(v), v));
+        v = OP::of(v, lane_move<0x143, 0xc>(OP::zero(v), v));
+        return read_lane(v, 63);
+    }
 }
-__device__ __forceinline__ double read_lane(double v, int lane) {
-    typedef int i32x2 __attribute__((ext_vector_type(2)));
-    const i32x2 w = __builtin_bit_cast(i32x2, v);
-    return __builtin_bit_cast(
-        double, i32x2{__builtin_amdgcn_readlane(w[0], lane), __builtin_amdgcn_readlane(w[1], lane)});
-}
-// row_shr 1, 2, 4, 8: lane 15 of every row of 16 holds the row's; row_bcast 15
-// and 31: lane 63 holds all.  Lanes without a source keep `old`.
-template <class F>
-__device__ __forceinline__ F wave_sum(F v) {
-    v += lane_move<0x111>(F(0), v);
-    v += lane_move<0x112>(F(0), v);
-    v += lane_move<0x114>(F(0), v);
-    v += lane_move<0x118>(F(0), v);
-    v += lane_move<0x142, 0xa>(F(0), v);
-    v += lane_move<0x143, 0xc>(F(0), v);
-    return read_lane(v, 63);
-}
+template <int TEAM, class V>
+__device__ __forceinline__ V team_sum(V v) { return team_reduce<Add, TEAM>(v); }
+template <int TEAM, class V>
+__device__ __forceinline__ V team_max(V v) { return team_reduce<Larger, TEAM>(v); }
 __device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
-template <class F>
-__device__ __forceinline__ F wave_max(F v) {
-    v = larger(v, lane_move<0x111>(v, v));
-    v = larger(v, lane_move<0x112>(v, v));
-    v = larger(v, lane_move<0x114>(v, v));
-    v = larger(v, lane_move<0x118>(v, v));
-    v = larger(v, lane_move<0x142>(v, v));
-    v = larger(v, lane_move<0x143>(v, v));
-    return read_lane(v, 63);
-}
 
 // ------------------------------------------------------------------ router
 
@@ -95,198 +114,200 @@ __device__ __forceinline__ F below(F x, F m) {
     return x == m ? F(0) : x - m;
 }
 
-// The k largest keys (-inf: not to be chosen), ties to the lowest expert;
-// choice j and its logit end up in lane j, -1 where no key is left.
-template <int EPL, class F>
-__device__ __forceinline__ void choose(F (&key)[EPL], const float (&x)[EPL], int k, int lane, int &sel, float &xs) {
+// The token's logits, masked ones -inf (NaN counts as masked), and the largest.
+// All loads go out together, from clamped addresses: none waits behind a branch.
+template <int DT, int EPL, int TEAM>
+__device__ __forceinline__ float load_logits(const RouteArgs &a, int64_t t, int lane, float (&x)[EPL]) {
+    const int64_t row = (t < a.T ? t : a.T - 1) * a.E;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = lane + TEAM * i;
+        x[i] = load_f32<DT>(a.logits, row + (e < a.E ? e : 0));
+    }
+    float m = kNegInf;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const bool is = t < a.T && lane + TEAM * i < a.E && x[i] > kNegInf;
+        x[i] = is ? x[i] : kNegInf;
+        m = __builtin_fmaxf(m, x[i]);
+    }
+    return team_max<TEAM>(m);
+}
+
+// The k largest keys (-inf: not to be chosen), ties to the lowest expert:
+// choice j ends up in lane j of the team, -1 where no key is left.
+template <int EPL, int TEAM, class F>
+__device__ __forceinline__ int choose(F (&key)[EPL], int k, int lane) {
+    constexpr int NONE = 0x7fffffff;
+    int sel = -1;
     for (int j = 0; j < k; ++j) {
         F b = key[0];
 #pragma unroll
         for (int i = 1; i < EPL; ++i) b = larger(b, key[i]);
-        b = wave_max(b);
-        if (!(b > F(kNegInf))) break;
-        int e = -1;
-        float xe = 0.0f;
+        b = team_max<TEAM>(b);
+        int e = NONE;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const uint64_t at = __ballot(key[i] == b);
-            if (e < 0 && at) {
-                const int l = __builtin_ctzll(at);
-                e = l + 64 * i;
-                xe = read_lane(x[i], l);
-            }
-        }
-        if (lane == j) {
-            sel = e;
-            xs = xe;
-        }
+        for (int i = EPL - 1; i >= 0; --i) e = key[i] == b ? lane + TEAM * i : e;
+        e = team_reduce<Lower, TEAM>(e);
+        if (lane == j && b > F(kNegInf)) sel = e;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (e == lane + 64 * i) key[i] = F(kNegInf);
+        for (int i = 0; i < EPL; ++i) key[i] = e == lane + TEAM * i ? F(kNegInf) : key[i];
     }
+    return sel;
 }
 
-// One wave per token; expert e = lane + 64*i sits in register i of its lane.
-// Keys and scores that decide a choice are 64-bit (logits are as they are: with
-// neither a bias nor sums over a run, their order decides); the weights are
-// 32-bit.
-template <int DT, int EPL>
-__global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
-    __shared__ double gkeys[4][EPL * 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const bool sums = a.groups > 1 && a.group_top == 2;
-    const int per = a.E / a.groups;
-    for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.T; t += (int64_t)gridDim.x * 4) {
-        float x[EPL];
-        float m = kNegInf;
+// A token's choice.  With neither a bias nor sums over a run the logits are
+// the keys, as they are (F fp32); else scores and keys are computed in 64 bits,
+// since a choice between two experts hangs on differences that fp32 scores do
+// not resolve.  (fp32 keys, and 64-bit ones where a margin left the choice
+// open, took as long or longer: some wave of a launch always needs both.)
+template <int EPL, int TEAM, class F>
+__device__ __forceinline__ int pick(const RouteArgs &a, const float (&x)[EPL],
+                                    const float (&bias)[EPL], float m, int per, int lane, F *gk) {
+    constexpr bool WIDE = sizeof(F) == 8;
+    const bool sums = WIDE && a.groups > 1 && a.group_top == 2;
+    F key[EPL], score[EPL];
+    if constexpr (WIDE) {
+        F z = F(0);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int e = lane + 64 * i;
-            x[i] = e < a.E ? load_f32<DT>(a.logits, t * a.E + e) : kNegInf;
-            if (!(x[i] > kNegInf)) x[i] = kNegInf;  // NaN counts as masked
-            m = __builtin_fmaxf(m, x[i]);
+            const F v = x[i];
+            score[i] = x[i] > kNegInf ? (a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(below(v, F(m)))) : 0.0;
+            z += score[i];
         }
-        m = wave_max(m);
-        double key[EPL], score[EPL];
-        if (a.bias || sums) {
-            double z = 0.0;
+        if (!a.sigmoid) {
+            z = team_sum<TEAM>(z);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const double xd = x[i];
-                score[i] = x[i] > kNegInf ? (a.sigmoid ? 1.0 / (1.0 + exp(-xd)) : exp(below(xd, (double)m))) : 0.0;
-                z += score[i];
-            }
-            if (!a.sigmoid) {
-                z = wave_sum(z);
-#pragma unroll
-                for (int i = 0; i < EPL; ++i) score[i] /= z;
-            }
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = lane + 64 * i;
-                key[i] = kNegInf;
-                if (x[i] > kNegInf) {
-                    const double v = a.bias ? score[i] + (double)a.bias[e] : (double)x[i];
-                    if (v > (double)kNegInf) key[i] = v;  // (a NaN key is no key)
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) key[i] = x[i];
+            for (int i = 0; i < EPL; ++i) score[i] /= z;
         }
-        if (a.groups > 1) {
-            // 64 / 2^ceil(log2 groups) lanes find the largest two keys of a run together
-            double *gk = gkeys[wave];
+    }
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                gk[lane + 64 * i] = key[i] > (double)kNegInf && sums && !a.bias ? score[i] : key[i];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            int team = 64;
-            while (64 / team < a.groups) team >>= 1;
-            const int g = lane / team;
-            double b1 = kNegInf, b2 = kNegInf;
-            if (g < a.groups)
-                for (int j = lane % team; j < per; j += team) {
-                    const double v = gk[g * per + j];
-                    b2 = larger(b2, v < b1 ? v : b1);
-                    b1 = larger(b1, v);
-                }
-            for (int o = 1; o < team; o <<= 1) {
-                const double o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
-                b2 = larger(larger(b2, o2), b1 < o1 ? b1 : o1);
-                b1 = larger(b1, o1);
-            }
-            double gs = a.group_top == 2 && b2 > (double)kNegInf ? b1 + b2 : b1;
-            uint64_t kept = 0;
-            for (int j = 0; j < a.top_groups; ++j) {
-                const double b = wave_max(gs);
-                if (!(b > (double)kNegInf)) break;
-                const int best = __builtin_ctzll(__ballot(gs == b)) / team;
-                kept |= 1ull << best;
-                if (g == best) gs = kNegInf;
-            }
+    for (int i = 0; i < EPL; ++i) {
+        F v = F(x[i]);
+        if (WIDE && a.bias) v = score[i] + F(bias[i]);
+        key[i] = x[i] > kNegInf && v > F(kNegInf) ? v : F(kNegInf);  // (a NaN key is no key)
+    }
+    if (a.groups > 1) {
+        // TEAM / 2^ceil(log2 groups) lanes find the largest two keys of a run together
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = lane + 64 * i;
-                if (e < a.E && !((kept >> (e / per)) & 1)) key[i] = kNegInf;
+        for (int i = 0; i < EPL; ++i)
+            gk[lane + TEAM * i] = sums && !a.bias && key[i] > F(kNegInf) ? score[i] : key[i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        int share = TEAM;
+        while (TEAM / share < a.groups) share >>= 1;
+        const int g = lane / share;
+        F b1 = F(kNegInf), b2 = F(kNegInf);
+        if (g < a.groups)
+            for (int j = lane % share; j < per; j += share) {
+                const F v = gk[g * per + j];
+                b2 = larger(b2, v < b1 ? v : b1);
+                b1 = larger(b1, v);
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+        for (int o = 1; o < share; o <<= 1) {
+            const F o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
+            b2 = larger(larger(b2, o2), b1 < o1 ? b1 : o1);
+            b1 = larger(b1, o1);
         }
-        int sel = -1;
-        float xs = kNegInf;  // the chosen expert's logit
-        if (a.bias) {
-            choose(key, x, a.k, lane, sel, xs);
-        } else {
-            float key32[EPL];
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) key32[i] = (float)key[i];  // (the logit itself, or -inf)
-            choose(key32, x, a.k, lane, sel, xs);
+        F gs = a.group_top == 2 && b2 > F(kNegInf) ? b1 + b2 : b1;
+        uint64_t kept = 0;
+        for (int j = 0; j < a.top_groups; ++j) {
+            const F b = team_max<TEAM>(gs);
+            const int best = team_reduce<Lower, TEAM>(gs == b ? g : 63);
+            if (b > F(kNegInf)) kept |= 1ull << best;
+            if (g == best) gs = F(kNegInf);
         }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = lane + TEAM * i;
+            if (e < a.E && !((kept >> (e / per)) & 1)) key[i] = F(kNegInf);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    return choose<EPL, TEAM>(key, a.k, lane);
+}
+
+// A team of lanes per token (16: four tokens to a wave, the same steps for all
+// of them); expert e = lane + TEAM*i sits in register i of its lane.  Bound by
+// the issue of the k rounds of `choose`, for few tokens by their latency.
+// Teams of 16 against whole waves: 16384 tokens of 64 experts, k 6: 5.7 and
+// 13.5 us; 256 experts in 8 runs, sigmoid, bias: 16384 tokens 34 and 42 us, 4096
+// tokens 14 both, 32 tokens 12.5 and 7.7.
+template <int DT, int EPL, int TEAM>
+__global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
+    constexpr int TOKENS = 256 / TEAM;
+    __shared__ double gkeys[TOKENS][EPL * TEAM];
+    const int lane = threadIdx.x % TEAM, slot = threadIdx.x / TEAM;
+    const int per = a.E / a.groups;
+    float bias[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = lane + TEAM * i;
+        bias[i] = a.bias ? a.bias[e < a.E ? e : 0] : 0.0f;
+    }
+    // (waves run together to the last token: no lane leaves its wave)
+    for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < a.T; t0 += (int64_t)gridDim.x * TOKENS) {
+        const int64_t t = t0 + slot;
+        const bool on = t < a.T;
+        float x[EPL];
+        const float m = load_logits<DT, EPL, TEAM>(a, t, lane, x);
+        const int sel =
+            a.bias || (a.groups > 1 && a.group_top == 2)
+                ? pick<EPL, TEAM>(a, x, bias, m, per, lane, gkeys[slot])
+                : pick<EPL, TEAM>(a, x, bias, m, per, lane, reinterpret_cast<float *>(gkeys[slot]));
+        const float xs = sel >= 0 ? load_f32<DT>(a.logits, t * a.E + sel) : kNegInf;
         float w;
         if (!a.raw) {
             // s_i / sum s = softmax of the chosen experts' log scores: no
             // quotient of two underflowed numbers
             const float l = sel < 0 ? kNegInf : a.sigmoid ? log_sigmoid(xs) : xs;
-            const float lm = wave_max(l);
+            const float lm = team_max<TEAM>(l);
             const float p = sel < 0 ? 0.0f : expf(below(l, lm));
-            w = p / wave_sum(p);
+            w = p / team_sum<TEAM>(p);
         } else if (a.sigmoid) {
             w = sigmoid_f32(xs);
         } else {
             float z = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) z += x[i] > kNegInf ? expf(below(x[i], m)) : 0.0f;
-            z = wave_sum(z);
+            z = team_sum<TEAM>(z);
             w = expf(below(xs, m)) / z;
         }
-        if (lane < a.k) {
+        if (on && lane < a.k) {
             a.experts[t * a.k + lane] = sel;
             a.weights[t * a.k + lane] = sel < 0 ? 0.0f : w * a.scale;
         }
     }
 }
 
-// The logits' gradient, one wave per token.  Renormalised weights are a
+// The logits' gradient, a team of lanes per token.  Renormalised weights are a
 // softmax over the chosen experts alone, w = scale * p: dl_i = p_i (dw_i -
 // sum dw p) scale (times 1 - s_i for the sigmoid), and 0 for the others; raw
 // softmax weights take the whole row: dl_j = s_j (ds_j - sum_i s_i ds_i).
-template <int DT, int EPL>
+template <int DT, int EPL, int TEAM>
 __global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.T; t += (int64_t)gridDim.x * 4) {
-        float x[EPL], d[EPL];
-        float m = kNegInf;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = lane + 64 * i;
-            x[i] = e < a.E ? load_f32<DT>(a.logits, t * a.E + e) : kNegInf;
-            if (!(x[i] > kNegInf)) x[i] = kNegInf;
-            m = __builtin_fmaxf(m, x[i]);
-            d[i] = 0.0f;
-        }
-        int sel = lane < a.k ? a.experts[t * a.k + lane] : -1;
-        float dw = lane < a.k ? a.dweights[t * a.k + lane] * a.scale : 0.0f;
-        float xs = kNegInf;
-        const int at = sel >= 0 && sel < a.E ? sel : 0;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const float v = __shfl(x[i], at & 63);
-            if ((at >> 6) == i) xs = v;
-        }
-        if (sel < 0 || sel >= a.E || !(xs > kNegInf)) {
+    constexpr int TOKENS = 256 / TEAM;
+    const int lane = threadIdx.x % TEAM, slot = threadIdx.x / TEAM;
+    for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < a.T; t0 += (int64_t)gridDim.x * TOKENS) {
+        const int64_t t = t0 + slot;
+        const bool on = t < a.T;
+        const bool whole = a.raw && !a.sigmoid;
+        int sel = on && lane < a.k ? a.experts[t * a.k + lane] : -1;
+        float dw = on && lane < a.k ? a.dweights[t * a.k + lane] * a.scale : 0.0f;
+        float xs = sel >= 0 && sel < a.E ? load_f32<DT>(a.logits, t * a.E + sel) : kNegInf;
+        if (!(xs > kNegInf)) {
             sel = -1;
             dw = 0.0f;
         }
         float ds;  // this lane's choice: the gradient of its score, or of its log score
         if (!a.raw) {
             const float l = sel < 0 ? kNegInf : a.sigmoid ? log_sigmoid(xs) : xs;
-            const float lm = wave_max(l);
+            const float lm = team_max<TEAM>(l);
             const float p = sel < 0 ? 0.0f : expf(below(l, lm));
-            const float z = wave_sum(p);
+            const float z = team_sum<TEAM>(p);
             const float w = sel < 0 ? 0.0f : p / z;
-            ds = w * (dw - wave_sum(dw * w));
+            ds = w * (dw - team_sum<TEAM>(dw * w));
             if (a.sigmoid) ds *= sigmoid_f32(-xs);
         } else if (a.sigmoid) {
             ds = dw * sigmoid_f32(xs) * sigmoid_f32(-xs);
@@ -294,35 +315,37 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
             ds = dw;
         }
         if (sel < 0) ds = 0.0f;
-        for (int j = 0; j < a.k; ++j) {
-            const int e = __builtin_amdgcn_readlane(sel, j);
-            const float v = read_lane(ds, j);
+        float d[EPL];
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (e == lane + 64 * i) d[i] += v;
+        for (int i = 0; i < EPL; ++i) d[i] = 0.0f;
+        for (int j = 0; j < a.k; ++j) {
+            const int e = __shfl(sel, j, TEAM);
+            const float v = __shfl(ds, j, TEAM);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) d[i] += e == lane + TEAM * i ? v : 0.0f;
         }
-        if (a.raw && !a.sigmoid) {
-            m = wave_max(m);
+        if (whole) {
             float z = 0.0f, s[EPL], c = 0.0f;
+            const float m = load_logits<DT, EPL, TEAM>(a, t, lane, s);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                s[i] = x[i] > kNegInf ? expf(below(x[i], m)) : 0.0f;
+                s[i] = s[i] > kNegInf ? expf(below(s[i], m)) : 0.0f;
                 z += s[i];
             }
-            z = wave_sum(z);
+            z = team_sum<TEAM>(z);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 s[i] = s[i] > 0.0f ? s[i] / z : 0.0f;
                 c += s[i] * d[i];
             }
-            c = wave_sum(c);
+            c = team_sum<TEAM>(c);
 #pragma unroll
             for (int i = 0; i < EPL; ++i) d[i] = s[i] * (d[i] - c);
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            const int e = lane + 64 * i;
-            if (e < a.E) store_f32<DT>(a.dlogits, t * a.E + e, d[i]);
+            const int e = lane + TEAM * i;
+            if (on && e < a.E) store_f32<DT>(a.dlogits, t * a.E + e, d[i]);
         }
     }
 }
@@ -598,7 +621,7 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(MoveArgs a) {
             }
         }
         if (a.dweights) {
-            dot = wave_sum(dot);
+            dot = team_sum<64>(dot);
             __syncthreads();
             if (lane == 0) part[wave] = dot;
             __syncthreads();

@@ -66,8 +66,7 @@ typedef struct {
  *            unmasked expert (in a kept run) is left hold -1.
  *   weights  (T,k) fp32: scale * s of the chosen, divided by their sum unless
  *            opt->raw; 0 where the expert is -1.
- * Choices are those of keys computed in 64 bits: where fp32 keys lie so near
- * to one another that their order could differ, they are recomputed.
+ * Choices are those of keys computed in 64 bits; the weights are fp32.
  * 1 <= k <= 64, k <= E <= 1024.  opt may be NULL (defaults).
  */
 fl_status fl_moe_route(const void *logits, const float *bias, int32_t *experts, float *weights, int64_t T, int64_t E,

@@ -329,3 +329,97 @@ def test_weights_beyond_31_bits():
     ref = A[3:].double().t().contiguous() @ d
     check(dW[E - 1], ref, 40 * U32 * (A[3:].double().abs().t().contiguous() @ d.abs()), torch.bfloat16)
     assert bool((dW[E - 2] == 0).all())
+
+
+# ------------------------------------------- routing and plans of many tokens
+
+@pytest.mark.parametrize("E,k,options", [
+    (200, 8, {}), (256, 8, dict(score="sigmoid", bias=True, groups=8, top_groups=4, group_top=2)),
+    (144, 16, dict(renorm=False, groups=16, top_groups=5, group_top=2)), (256, 3, dict(bias=True)), (64, 6, {}),
+    (20, 5, dict(score="sigmoid", renorm=False, bias=True))])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_route_many_tokens(E, k, options, dtype):
+    """Long batches take other lane arrangements than short ones: the choices
+    are the same, the weights up to the order of fp32 sums over at most E."""
+    T, options = 5003, dict(options)
+    g = gen(E + k)
+    x = normal(g, T, E, std=2.0, dt=DT[dtype])
+    x[torch.rand(T, E, generator=g, device="cuda") < 0.1] = -math.inf
+    x[7], x[4096] = -math.inf, math.nan
+    bias = normal(g, E, std=0.1) if options.pop("bias", False) else None
+    say("route many", E, k, options, dtype)
+    w, e = fl.moe_route(x, k, bias=bias, **options)
+    dw = normal(g, T, k)
+    how = {n: options[n] for n in ("score", "renorm") if n in options}
+    d = fl.moe_route_bwd(x, e, dw, **how)
+    parts = [fl.moe_route(x[i:i + 100].contiguous(), k, bias=bias, **options) for i in range(0, T, 100)]
+    assert torch.equal(e, torch.cat([p[1] for p in parts]))
+    other = torch.cat([p[0] for p in parts])
+    assert float((w - other).abs().max()) <= 2 * (E + 8) * U32
+    assert int((e[7] >= 0).sum()) == 0 and float(w[7].abs().max()) == 0.0 and float(w[4096].abs().max()) == 0.0
+    back = torch.cat([fl.moe_route_bwd(x[i:i + 100].contiguous(), e[i:i + 100].contiguous(), dw[i:i + 100].contiguous(), **how)
+                      for i in range(0, T, 100)])
+    # sums of terms below 5 (weights at most 1, |dw| below 5) in another order, one rounding each
+    assert float((d.double() - back.double()).abs().max()) <= 10 * (E + 8) * U32 + 2 * unit(DT[dtype]) * float(back.abs().max())
+
+
+def test_plan_of_many_slots():
+    for T, k, E in ((70001, 7, 256), (30000, 3, 1000), (100000, 8, 5)):
+        g = gen(T)
+        e = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+        say("plan many", T, k, E)
+        plan = fl.moe_plan(e, E)
+        flat = e.reshape(-1).long()
+        key = torch.where(flat < 0, E, flat)
+        order = torch.sort(key, stable=True).indices
+        n = int((flat >= 0).sum())
+        counts = torch.bincount(key, minlength=E + 1)[:E]
+        assert torch.equal(plan.offsets[1:].long(), counts.cumsum(0)) and int(plan.offsets[0]) == 0
+        assert torch.equal(plan.token_of_row[:n].long(), order[:n] // k) and bool((plan.token_of_row[n:] == -1).all())
+        rows = torch.full_like(flat, -1)
+        rows[order[:n]] = torch.arange(n, device="cuda")
+        assert torch.equal(plan.row_of_slot.reshape(-1).long(), rows)
+
+
+# ------------------------------------------------ operands off 16 bytes
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_unaligned_operands(dtype):
+    """Every operand one element past a 16-byte boundary gives the bits of the
+    aligned call."""
+    dt, g = DT[dtype], gen(31)
+    counts, K, N = [70, 0, 130, 3], 136, 264
+    offsets, S, E = offsets_of(counts), 203, 4
+
+    def off(t):
+        buf = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+        buf[1:].copy_(t.reshape(-1))
+        return buf[1:].view(t.shape)
+    A, B, bias, Y = normal(g, S, K, dt=dt), normal(g, E, K, N, dt=dt), normal(g, E, N, dt=dt), normal(g, S, N, dt=dt)
+    G, W, X, D = normal(g, S, K, dt=dt), normal(g, E, N, K, dt=dt), normal(g, S, N, dt=dt), normal(g, S, N, dt=dt)
+    index = torch.randperm(S, generator=g, device="cuda").to(torch.int32)
+    say("unaligned", dtype)
+    want = fl.grouped_linear(A, B, offsets, bias, Y, act="glu", index=index, pre=True)
+    got = fl.grouped_linear(off(A), off(B), off(offsets), off(bias), off(Y), act="glu", index=off(index),
+                            out=off(torch.zeros_like(Y)), pre=off(torch.zeros_like(Y)))
+    want += fl.grouped_linear_bwd(G, W, X, offsets, Y, act="glu")
+    got += fl.grouped_linear_bwd(off(G), off(W), off(X), offsets, off(Y), act="glu", dX=off(torch.zeros_like(Y)),
+                                 dY=off(torch.zeros_like(Y)))
+    want += fl.grouped_weight_grad(A, D, offsets)
+    got += fl.grouped_weight_grad(off(A), off(D), offsets, dW=off(torch.zeros_like(B)))
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_no_tokens():
+    x = torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda")
+    layer = RoutedExperts(64, 96, 4, 2)
+    w, e = fl.moe_route(torch.zeros(0, 4, device="cuda"), 2)
+    plan = fl.moe_plan(e, 4)
+    assert w.shape == e.shape == (0, 2) and plan.offsets.tolist() == [0] * 5
+    h = fl.grouped_linear(x, layer.W1, plan.offsets, layer.b1, act="gelu_tanh", index=plan.token_of_row)
+    assert h.shape == (0, 96)
+    assert fl.moe_combine(h, plan.row_of_slot, w).shape == (0, 96)
+    dW, db = fl.grouped_weight_grad(x, h, plan.offsets)
+    assert bool((dW == 0).all()) and bool((db == 0).all())
+    assert fl.moe_gather(x, plan.token_of_row).shape == (0, 64)
