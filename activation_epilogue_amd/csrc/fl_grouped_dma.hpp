@@ -43,6 +43,16 @@ __device__ __forceinline__ uint32_t load_u16_at(const void *p) {
     return v & 0xffffu;
 }
 
+// lds_copy16 with the streaming policy bit.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_copy16_nt(i32x4_t rsrc, uint32_t voffset, uint32_t soffset, uint32_t lds_addr) {
+    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds" ::"v"(voffset), "s"(rsrc),
+                 "s"(soffset), "s"(lds_addr)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 // One operand's tile: R rows (KC) or R columns (KR), copied by WAVES waves.
 template <int DT, int R, int WAVES, bool KC>
 struct GroupedSide {
@@ -221,7 +231,13 @@ struct GroupedTile {
                                 : FORM == kFormBwd ? (uint32_t)kt * 128
                                                    : (uint32_t)kt * 128 * (uint32_t)o.ldb;
             const bool ok = !CHECK || SideB::k(wave, lane, i) < kleft;
-            lds_copy16(o.B.rsrc, ok ? o.B.off[i] : kOob, so, buf.b + i * 1024);
+            // few rows: every weight is read once, and streams past the L2
+            // (32 tokens through 64 experts 60.7 -> 53.8 us; taller tiles, of
+            // which a run may have several, lose: 110 -> 127 us at 96 rows)
+            if constexpr (BM <= 32)
+                lds_copy16_nt(o.B.rsrc, ok ? o.B.off[i] : kOob, so, buf.b + i * 1024);
+            else
+                lds_copy16(o.B.rsrc, ok ? o.B.off[i] : kOob, so, buf.b + i * 1024);
         }
     }
     template <int C0, int C1, bool CHECK>
@@ -432,15 +448,29 @@ struct GroupedTile {
                 return io::to_f32((raw)(w[0][e >> 1] >> (16 * (e & 1))));
         }
     };
+    // Outputs are not read again here, nor are the epilogue's inputs: where
+    // rows start on 128-byte lines (a.stream) they pass the L2 by (2 to 5%
+    // faster; other rows would be written in partial lines, 10% slower).
+    static constexpr int kStream = 2;  // cache policy operand: nt
+    __device__ __forceinline__ static void store16(u32x4_t v, __amdgpu_buffer_rsrc_t r, uint32_t off, bool stream) {
+        if (stream)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, v), r, off, 0, kStream);
+        else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, v), r, off, 0, 0);
+    }
     __device__ __forceinline__ static uint32_t at(uint32_t off, int bytes, bool ok) {
         return ok && off != kOob ? off + bytes : kOob;
     }
-    __device__ __forceinline__ static Octet load8(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid) {
+    __device__ __forceinline__ static Octet load8(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid, bool stream) {
         Octet v;
 #pragma unroll
         for (int h = 0; h < ES / 2; ++h) {
             if (valid >= EPC * (h + 1)) {
-                v.w[h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at(off, h * 16, true), 0, 0));
+                const uint32_t o = at(off, h * 16, true);
+                if (stream)
+                    v.w[h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, kStream));
+                else
+                    v.w[h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
             } else {
                 v.w[h] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
@@ -453,12 +483,12 @@ struct GroupedTile {
         return v;
     }
     __device__ __forceinline__ static void store8_f32(const float (&v)[8], __amdgpu_buffer_rsrc_t r, uint32_t off,
-                                                      int valid) {
+                                                      int valid, bool stream) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const f32x4_t w = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
             if (valid >= 4 * h + 4) {
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, w), r, at(off, h * 16, true), 0, 0);
+                store16(__builtin_bit_cast(u32x4_t, w), r, at(off, h * 16, true), stream);
             } else {
 #pragma unroll
                 for (int e = 0; e < 3; ++e)
@@ -467,15 +497,16 @@ struct GroupedTile {
             }
         }
     }
-    __device__ __forceinline__ static void store8(const float (&v)[8], __amdgpu_buffer_rsrc_t r, uint32_t off, int valid) {
+    __device__ __forceinline__ static void store8(const float (&v)[8], __amdgpu_buffer_rsrc_t r, uint32_t off, int valid,
+                                                  bool stream) {
         if constexpr (ES == 4) {
-            store8_f32(v, r, off, valid);
+            store8_f32(v, r, off, valid, stream);
         } else {
             u32x4_t w;
 #pragma unroll
             for (int d = 0; d < 4; ++d) w[d] = io::pack2(v[2 * d], v[2 * d + 1]);
             if (valid >= 8) {
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, w), r, off, 0, 0);
+                store16(w, r, off, stream);
             } else {
 #pragma unroll
                 for (int e = 0; e < 7; ++e)
@@ -497,6 +528,7 @@ struct GroupedTile {
     __device__ __forceinline__ static void epilogue(const GroupedArgs &a, const Tile &t, int wave, int lane,
                                                     const f32x4_t (&acc)[NRB][NI], FL_LDS char *lds) {
         const int rows = t.rows, n0 = t.tn * BN;
+        const bool stream = !PART && a.stream;
         const int64_t row0 = FORM == kFormGrad ? (int64_t)t.e * a.K + t.m0 : t.m0;
         const int wm = row_of(wave), wn = col_of(wave);
         constexpr int CPR = TN / 8, RPP = 64 / CPR, PASSES = 16 / RPP;  // lanes per row, rows and passes per row block
@@ -523,7 +555,7 @@ struct GroupedTile {
             if (a.bias) {
                 const __amdgpu_buffer_rsrc_t rB = make_rsrc(
                     static_cast<const char *>(a.bias) + ((int64_t)t.e * a.N + n0) * ES, (size_t)(a.N - n0) * ES);
-                bias = load8(rB, valid > 0 ? (uint32_t)col * ES : kOob, valid);
+                bias = load8(rB, valid > 0 ? (uint32_t)col * ES : kOob, valid, false);
             }
         }
         constexpr bool NEED_Y = ACT == FL_ACT_GLU, NEED_X = FORM == kFormBwd && ACT != FL_ACT_NONE;
@@ -531,8 +563,8 @@ struct GroupedTile {
         auto sides = [&](int mi) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
-                if constexpr (NEED_Y) yv[mi & 1][p] = load8(rY, offset(mi, p), valid);
-                if constexpr (NEED_X) xv[mi & 1][p] = load8(rX, offset(mi, p), valid);
+                if constexpr (NEED_Y) yv[mi & 1][p] = load8(rY, offset(mi, p), valid, stream);
+                if constexpr (NEED_X) xv[mi & 1][p] = load8(rX, offset(mi, p), valid, stream);
             }
         };
         sides(0);
@@ -571,11 +603,11 @@ struct GroupedTile {
                     }
                 }
                 if (PART || (FORM == kFormGrad && a.dw_f32))
-                    store8_f32(v, rO, off, valid);
+                    store8_f32(v, rO, off, valid, stream);
                 else
-                    store8(v, rO, off, valid);
+                    store8(v, rO, off, valid, stream);
                 if (!PART && (FORM == kFormFwd ? a.out2 != nullptr : FORM == kFormBwd && ACT == FL_ACT_GLU))
-                    store8(v2, rO2, off, valid);
+                    store8(v2, rO2, off, valid, stream);
             }
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);

@@ -318,6 +318,8 @@ fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void 
     // but the work is even whatever the runs' lengths: 1780 against 1820 us
     // where an expert has 470 tiles, 233 against 210 us where it has 22.
     a.spread = (int64_t)a.S / a.E / t.bm * a.tiles_n >= 128;
+    const size_t row_bytes = (size_t)a.N * (a.dw_f32 ? 4 : elem_size(dtype));
+    a.stream = row_bytes % 128 == 0 && aligned(a.out, 128) && aligned(a.out2, 128);
     a.parts = workspace ? p.parts : 1;
     a.part = static_cast<float *>(workspace);
     const int64_t tiles_m = form == fl::kFormGrad ? a.E * (((int64_t)a.K + t.bm - 1) / t.bm) : most_row_tiles(a.S, a.E, t.bm);
