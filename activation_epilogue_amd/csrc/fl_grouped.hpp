@@ -165,7 +165,9 @@ __global__ void __launch_bounds__(1024) grouped_column_sum_kernel(GroupedArgs a)
 // ------------------------------------------------------ joining parts of K
 
 // Adds the parts' sums in order and ends as the tiles' epilogue does.  Forward:
-// a block takes 1024 columns of one row; gradient: of one row of dW.
+// a block takes 1024 columns of one row; gradient: of one row of dW.  Four parts
+// are loaded at a time (one after the other, 16 parts took 16 round trips to
+// memory: 25 against 16 us for 2 rows of 1024).
 template <int DT, int FORM>
 __global__ void __launch_bounds__(256) grouped_join_kernel(GroupedArgs a, int act) {
     using io = Io<DT>;

@@ -171,18 +171,27 @@ void launch_route(int dtype, const fl::RouteArgs &a, hipStream_t st) {
 
 // ---------------------------------------------------------------- movement
 
-#define FL_MOVE(kernel, dtype, vec, grid, block, st, a)                                            \
-    do {                                                                                           \
-        if ((dtype) == FL_F32) {                                                                   \
-            if (vec) hipLaunchKernelGGL((fl::kernel<FL_F32, true>), grid, block, 0, st, a);        \
-            else hipLaunchKernelGGL((fl::kernel<FL_F32, false>), grid, block, 0, st, a);           \
-        } else if ((dtype) == FL_F16) {                                                            \
-            if (vec) hipLaunchKernelGGL((fl::kernel<FL_F16, true>), grid, block, 0, st, a);        \
-            else hipLaunchKernelGGL((fl::kernel<FL_F16, false>), grid, block, 0, st, a);           \
-        } else {                                                                                   \
-            if (vec) hipLaunchKernelGGL((fl::kernel<FL_BF16, true>), grid, block, 0, st, a);       \
-            else hipLaunchKernelGGL((fl::kernel<FL_BF16, false>), grid, block, 0, st, a);          \
-        }                                                                                          \
+#define FL_MOVE_COLS(kernel, dtype, vec, cols, grid, st, a)                                            \
+    do {                                                                                               \
+        if ((dtype) == FL_F32) {                                                                       \
+            if (vec) hipLaunchKernelGGL((fl::kernel<FL_F32, true, cols>), grid, dim3(256), 0, st, a);  \
+            else hipLaunchKernelGGL((fl::kernel<FL_F32, false, cols>), grid, dim3(256), 0, st, a);     \
+        } else if ((dtype) == FL_F16) {                                                                \
+            if (vec) hipLaunchKernelGGL((fl::kernel<FL_F16, true, cols>), grid, dim3(256), 0, st, a);  \
+            else hipLaunchKernelGGL((fl::kernel<FL_F16, false, cols>), grid, dim3(256), 0, st, a);     \
+        } else {                                                                                       \
+            if (vec) hipLaunchKernelGGL((fl::kernel<FL_BF16, true, cols>), grid, dim3(256), 0, st, a); \
+            else hipLaunchKernelGGL((fl::kernel<FL_BF16, false, cols>), grid, dim3(256), 0, st, a);    \
+        }                                                                                              \
+    } while (0)
+#define FL_MOVE(kernel, dtype, vec, pieces, rows, st, a)                                          \
+    do {                                                                                          \
+        if ((pieces) <= 64)                                                                       \
+            FL_MOVE_COLS(kernel, dtype, vec, 64, move_grid(rows, pieces, 64), st, a);             \
+        else if ((pieces) <= 128)                                                                 \
+            FL_MOVE_COLS(kernel, dtype, vec, 128, move_grid(rows, pieces, 128), st, a);           \
+        else                                                                                      \
+            FL_MOVE_COLS(kernel, dtype, vec, 256, move_grid(rows, pieces, 256), st, a);           \
     } while (0)
 
 bool rows_aligned(int dtype, int64_t H, const void *p, const void *q, const void *r) {
@@ -190,6 +199,12 @@ bool rows_aligned(int dtype, int64_t H, const void *p, const void *q, const void
 }
 
 unsigned grid_of(int64_t n) { return (unsigned)(n < 1 ? 1 : n < 1 << 22 ? n : 1 << 22); }
+
+// Blocks of 256 / cols rows; few rows are cut along their pieces as well.
+dim3 move_grid(int64_t rows, int64_t pieces, int cols) {
+    const int64_t y = rows < 65536 ? (pieces + cols - 1) / cols : 1;
+    return dim3(grid_of((rows * cols + 255) / 256), (unsigned)(y < 64 ? y : 64));
+}
 
 // ------------------------------------------------------- experts' products
 
@@ -473,7 +488,7 @@ fl_status fl_moe_gather(const void *X, const int32_t *index, void *rows, int64_t
     a.S = S;
     a.H = H;
     const bool vec = rows_aligned(dtype, H, X, rows, nullptr);
-    FL_MOVE(gather_kernel, dtype, vec, dim3(grid_of(S)), dim3(256), static_cast<hipStream_t>(stream), a);
+    FL_MOVE(gather_kernel, dtype, vec, vec ? (int64_t)(H * es / 16) : H, S, static_cast<hipStream_t>(stream), a);
     return check_launch("moe_gather");
 }
 
@@ -503,9 +518,7 @@ fl_status fl_moe_combine(const void *rows, const int32_t *row_of_slot, const flo
     a.H = H;
     a.k = (int)k;
     const bool vec = rows_aligned(dtype, H, rows, R, out);
-    const int64_t pieces = vec ? H * es / 16 : H;
-    const dim3 grid(grid_of(T), (unsigned)((pieces + 255) / 256 < 64 ? (pieces + 255) / 256 : 64));
-    FL_MOVE(combine_kernel, dtype, vec, grid, dim3(256), static_cast<hipStream_t>(stream), a);
+    FL_MOVE(combine_kernel, dtype, vec, vec ? (int64_t)(H * es / 16) : H, T, static_cast<hipStream_t>(stream), a);
     return check_launch("moe_combine");
 }
 
@@ -539,8 +552,13 @@ fl_status fl_moe_combine_bwd(const void *dout, const void *rows, const int32_t *
     a.H = H;
     a.k = (int)k;
     const bool vec = rows_aligned(dtype, H, dout, dweights ? rows : nullptr, drows);
-    FL_MOVE(combine_bwd_kernel, dtype, vec, dim3(grid_of((int64_t)slots)), dim3(256),
-            static_cast<hipStream_t>(stream), a);
+    // a wave per slot where they fill the chip (16384 slots of 1024 bf16: 32 us,
+    // a block per slot 48), a block where there are few
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (slots >= 4096)
+        FL_MOVE_COLS(combine_bwd_kernel, dtype, vec, 64, dim3(grid_of((int64_t)(slots + 3) / 4)), st, a);
+    else
+        FL_MOVE_COLS(combine_bwd_kernel, dtype, vec, 256, dim3(grid_of((int64_t)slots)), st, a);
     return check_launch("moe_combine_bwd");
 }
 
