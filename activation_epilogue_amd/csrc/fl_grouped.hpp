@@ -33,7 +33,7 @@ struct GroupedArgs {
     int tiles_n;
     int group;               // row tiles per band of the tile order
     int spread;              // nonzero: each XCD takes its share of every expert's tiles
-    int stream;              // nonzero: rows of the outputs (and Y, X) start on 128-byte lines
+    int stream;              // nonzero: 16-bit outputs whose rows (and those of Y, X) start on 128-byte lines
     int parts;               // K is summed in 4, 8 or 16 parts by different workgroups (1: whole)
     float *part;             // parts > 1: fp32 sums, (parts, S, N) or, gradient, (parts, E*K, N)
     int max_tiles;           // limit on the tiles found from the offsets
@@ -219,19 +219,20 @@ __global__ void __launch_bounds__(256) grouped_join_kernel(GroupedArgs a, int ac
 // The tiles of grouped_dma_kernel (fl_grouped_dma.hpp).  time: of a round (one
 // workgroup in every slot, 256 CUs x per_cu), in units of the widest tile's at
 // large sizes (8192x2 rows of 8 experts, K 4096, N 14336: 1030, 950, 810, 605
-// and 370 TFLOP/s).  fp32 has one tile: 64x64 reaches 130 TFLOP/s at 4096x2
-// rows, K 2048, N 4096 (128x128: 114 to 134, and half as much where there are
-// few tiles).
+// and 370 TFLOP/s; fp32, 4096x2 rows of 8 experts, K 2048, N 4096: 130 and 100,
+// but 20 and 14 us for 100x2 rows of 6 experts, K 768, N 1000).  128x128 fp32
+// tiles: 114 to 134 TFLOP/s, and half as much where there are few.
 struct GroupedTileShape {
     int bm, bn, per_cu;
     float time;
     float stage;  // us of one stage where a CU has one workgroup
     bool grad;    // compiled for the gradient too
 };
-enum GroupedVariant { kTile256x256 = 0, kTile256x128, kTile128x128, kTile64x128, kTile32x128, kTileF32, kGroupedVariants };
+enum GroupedVariant { kTile256x256 = 0, kTile256x128, kTile128x128, kTile64x128, kTile32x128, kTileF32, kTileF32x32, kGroupedVariants };
 constexpr GroupedTileShape kGroupedTiles[kGroupedVariants] = {
     {256, 256, 1, 1.0f, 1.9f, true}, {256, 128, 1, 0.54f, 0.95f, false}, {128, 128, 2, 0.64f, 0.5f, true},
-    {64, 128, 2, 0.425f, 0.25f, false}, {32, 128, 2, 0.35f, 0.23f, false}, {64, 64, 3, 1.0f, 0.58f, true}};
+    {64, 128, 2, 0.425f, 0.25f, false}, {32, 128, 2, 0.35f, 0.23f, false}, {64, 64, 3, 1.0f, 0.58f, true},
+    {32, 64, 4, 0.8f, 0.3f, false}};
 typedef void (*grouped_launcher)(const GroupedArgs &, int act, int64_t grid, hipStream_t);
 // One dtype and form to a compiled unit.
 template <int DT, int FORM>

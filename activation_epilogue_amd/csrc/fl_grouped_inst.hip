@@ -18,7 +18,10 @@ static void launch(const GroupedArgs &a, int act, int64_t grid, hipStream_t s) {
 template <>
 grouped_launcher pick_grouped<FL_INST_DTYPE, FL_INST_FORM>(int variant) {
 #if FL_INST_DTYPE == 0
-    return variant == kTileF32 ? launch<64, 64, 2, 2, 3, 3> : nullptr;
+#if FL_INST_FORM != 2
+    if (variant == kTileF32x32) return launch<32, 64, 2, 2, 3, 4>;
+#endif
+    return launch<64, 64, 2, 2, 3, 3>;
 #else
     if (variant == kTile256x256) return launch<256, 256, 2, 4, 2, 1>;
 #if FL_INST_FORM != 2

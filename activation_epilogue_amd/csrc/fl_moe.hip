@@ -280,7 +280,7 @@ GroupedPlan plan_grouped(int dtype, int form, int64_t S, int64_t N, int64_t K, i
     double least = 0.0, tiles = 0.0;
     for (int v = 0; v < fl::kGroupedVariants; ++v) {
         const fl::GroupedTileShape &t = fl::kGroupedTiles[v];
-        if ((v == fl::kTileF32) != (dtype == FL_F32) || (form == fl::kFormGrad && !t.grad)) continue;
+        if ((v >= fl::kTileF32) != (dtype == FL_F32) || (form == fl::kFormGrad && !t.grad)) continue;
         double m;
         if (form == fl::kFormGrad) {
             m = (double)E * ((K + t.bm - 1) / t.bm);
@@ -333,8 +333,9 @@ fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void 
     // but the work is even whatever the runs' lengths: 1780 against 1820 us
     // where an expert has 470 tiles, 233 against 210 us where it has 22.
     a.spread = (int64_t)a.S / a.E / t.bm * a.tiles_n >= 128;
-    const size_t row_bytes = (size_t)a.N * (a.dw_f32 ? 4 : elem_size(dtype));
-    a.stream = row_bytes % 128 == 0 && aligned(a.out, 128) && aligned(a.out2, 128);
+    // (a lane's 8 fp32 columns are two stores, each of half its lines)
+    const bool f32 = dtype == FL_F32 || a.dw_f32;
+    a.stream = !f32 && a.N % 64 == 0 && aligned(a.out, 128) && aligned(a.out2, 128);
     a.parts = workspace ? p.parts : 1;
     a.part = static_cast<float *>(workspace);
     const int64_t tiles_m = form == fl::kFormGrad ? a.E * (((int64_t)a.K + t.bm - 1) / t.bm) : most_row_tiles(a.S, a.E, t.bm);
