@@ -31,8 +31,8 @@
 // pre-activation 1120, backward 1160, weight gradient 1170 TFLOP/s, bound by the
 // matrix cores at the clock that power leaves (a dense library product of that
 // size: 1140 to 1310); 32 tokens through 64 experts of 2048x1408: 6.5 TB/s of
-// weights, bound by memory; 4096 tokens through them: 715 TFLOP/s, bound by what
-// 256x128 tiles draw from the L2 (48 KB per 1024 cycles of MFMAs and CU).
+// weights, bound by memory; 4096 tokens through them: 715 TFLOP/s, bound by how
+// runs of 384 rows fill tiles and rounds (4.1 rounds of work take 6).
 #pragma once
 
 #include "fl_dma16.hpp"
