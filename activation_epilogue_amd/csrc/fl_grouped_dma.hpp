@@ -24,8 +24,8 @@
 //     stands before the second block, which also issues the copies of the
 //     stage NBUF ahead into the buffer that the barrier has freed.
 //   * Epilogue: 16 rows at a time, a wave's accumulators pass through LDS so
-//     that a lane then holds 8 consecutive columns of one row: Y, X, pre and
-//     out move in 16-byte pieces, whole 128-byte lines per instruction.
+//     that a lane then holds 16 bytes of one row: Y, X, pre and out move in
+//     whole 128-byte lines per instruction.
 //
 // Measured (bf16, 8192x2 rows of 8 experts, K 4096, N 14336): forward with the
 // pre-activation 1120, backward 1160, weight gradient 1170 TFLOP/s, bound by the
@@ -445,14 +445,15 @@ struct GroupedTile {
         __syncthreads();
     }
 
-    // ---- epilogue: 8 consecutive columns of a row
-    struct Octet {
-        u32x4_t w[ES / 2];
+    // ---- epilogue: 16 bytes of a row in a lane
+    static constexpr int VEC = EPC;  // columns
+    struct Piece16 {
+        u32x4_t w;
         __device__ __forceinline__ float get(int e) const {
             if constexpr (ES == 4)
-                return __builtin_bit_cast(float, (uint32_t)w[e >> 2][e & 3]);
+                return __builtin_bit_cast(float, (uint32_t)w[e]);
             else
-                return io::to_f32((raw)(w[0][e >> 1] >> (16 * (e & 1))));
+                return io::to_f32((raw)(w[e >> 1] >> (16 * (e & 1))));
         }
     };
     // Outputs are not read again here, nor are the epilogue's inputs: where
@@ -468,56 +469,53 @@ struct GroupedTile {
     __device__ __forceinline__ static uint32_t at(uint32_t off, int bytes, bool ok) {
         return ok && off != kOob ? off + bytes : kOob;
     }
-    __device__ __forceinline__ static Octet load8(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid, bool stream) {
-        Octet v;
+    __device__ __forceinline__ static Piece16 load(__amdgpu_buffer_rsrc_t r, uint32_t off, int valid, bool stream) {
+        Piece16 v{};
+        if (valid >= VEC) {
+            if (stream)
+                v.w = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kStream));
+            else
+                v.w = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+        } else {
 #pragma unroll
-        for (int h = 0; h < ES / 2; ++h) {
-            if (valid >= EPC * (h + 1)) {
-                const uint32_t o = at(off, h * 16, true);
-                if (stream)
-                    v.w[h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, kStream));
-                else
-                    v.w[h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
-            } else {
-                v.w[h] = u32x4_t{0, 0, 0, 0};
-#pragma unroll
-                for (int e = 0; e < EPC - 1; ++e) {
-                    const uint32_t x = load_elem<ES>(r, at(off, h * 16 + e * ES, h * EPC + e < valid));
-                    v.w[h][e * ES / 4] |= x << (8 * (e * ES & 3));
-                }
+            for (int e = 0; e < VEC - 1; ++e) {
+                const uint32_t x = load_elem<ES>(r, at(off, e * ES, e < valid));
+                v.w[e * ES / 4] |= x << (8 * (e * ES & 3));
             }
         }
         return v;
     }
-    __device__ __forceinline__ static void store8_f32(const float (&v)[8], __amdgpu_buffer_rsrc_t r, uint32_t off,
-                                                      int valid, bool stream) {
+    __device__ __forceinline__ static void store(const float (&v)[VEC], __amdgpu_buffer_rsrc_t r, uint32_t off, int valid,
+                                                 bool stream) {
+        u32x4_t w;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int d = 0; d < 4; ++d) {
+            if constexpr (ES == 4)
+                w[d] = __builtin_bit_cast(uint32_t, v[d]);
+            else
+                w[d] = io::pack2(v[2 * d], v[2 * d + 1]);
+        }
+        if (valid >= VEC) {
+            store16(w, r, off, stream);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC - 1; ++e)
+                store_elem<ES>((typename RawBits<ES>::T)(w[e * ES / 4] >> (8 * (e * ES & 3))), r, at(off, e * ES, e < valid));
+        }
+    }
+    // the fp32 values themselves (16-bit types: two stores)
+    __device__ __forceinline__ static void store_f32(const float (&v)[VEC], __amdgpu_buffer_rsrc_t r, uint32_t off,
+                                                     int valid) {
+#pragma unroll
+        for (int h = 0; h < VEC / 4; ++h) {
             const f32x4_t w = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
             if (valid >= 4 * h + 4) {
-                store16(__builtin_bit_cast(u32x4_t, w), r, at(off, h * 16, true), stream);
+                store16(__builtin_bit_cast(u32x4_t, w), r, at(off, h * 16, true), false);
             } else {
 #pragma unroll
                 for (int e = 0; e < 3; ++e)
                     store_elem<4>(__builtin_bit_cast(uint32_t, v[4 * h + e]), r,
                                   at(off, h * 16 + e * 4, 4 * h + e < valid));
-            }
-        }
-    }
-    __device__ __forceinline__ static void store8(const float (&v)[8], __amdgpu_buffer_rsrc_t r, uint32_t off, int valid,
-                                                  bool stream) {
-        if constexpr (ES == 4) {
-            store8_f32(v, r, off, valid, stream);
-        } else {
-            u32x4_t w;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) w[d] = io::pack2(v[2 * d], v[2 * d + 1]);
-            if (valid >= 8) {
-                store16(w, r, off, stream);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 7; ++e)
-                    store_elem<2>((uint16_t)(w[e >> 1] >> (16 * (e & 1))), r, at(off, e * 2, e < valid));
             }
         }
     }
@@ -538,7 +536,7 @@ struct GroupedTile {
         const bool stream = !PART && a.stream;
         const int64_t row0 = FORM == kFormGrad ? (int64_t)t.e * a.K + t.m0 : t.m0;
         const int wm = row_of(wave), wn = col_of(wave);
-        constexpr int CPR = TN / 8, RPP = 64 / CPR, PASSES = 16 / RPP;  // lanes per row, rows and passes per row block
+        constexpr int CPR = TN / VEC, RPP = 64 / CPR, PASSES = 16 / RPP;  // lanes per row, rows and passes per row block
         const int es = PART || (FORM == kFormGrad && a.dw_f32) ? 4 : ES;
         const int64_t org = row0 * a.N + n0;
         const size_t bytes = ((size_t)rows * a.N - n0) * es;
@@ -551,27 +549,27 @@ struct GroupedTile {
             make_rsrc(a.Y ? static_cast<const char *>(a.Y) + org * ES : nullptr, a.Y ? bytes : 0);
         const __amdgpu_buffer_rsrc_t rX =
             make_rsrc(a.X ? static_cast<const char *>(a.X) + org * ES : nullptr, a.X ? bytes : 0);
-        const int col = wn * TN + (lane % CPR) * 8, valid = a.N - n0 - col;
+        const int col = wn * TN + (lane % CPR) * VEC, valid = a.N - n0 - col;
         FL_LDS char *w = lds + wave * 16 * EPI_ROW;
         auto offset = [&](int mi, int p) -> uint32_t {
             const int row = wm * TM + mi * 16 + p * RPP + lane / CPR;
             return row < rows && valid > 0 ? (uint32_t)(row * a.N + col) * es : kOob;
         };
-        Octet bias{};
+        Piece16 bias{};
         if constexpr (FORM == kFormFwd && !PART) {
             if (a.bias) {
                 const __amdgpu_buffer_rsrc_t rB = make_rsrc(
                     static_cast<const char *>(a.bias) + ((int64_t)t.e * a.N + n0) * ES, (size_t)(a.N - n0) * ES);
-                bias = load8(rB, valid > 0 ? (uint32_t)col * ES : kOob, valid, false);
+                bias = load(rB, valid > 0 ? (uint32_t)col * ES : kOob, valid, false);
             }
         }
         constexpr bool NEED_Y = ACT == FL_ACT_GLU, NEED_X = FORM == kFormBwd && ACT != FL_ACT_NONE;
-        Octet yv[2][PASSES], xv[2][PASSES];  // of this row block and the next
+        Piece16 yv[2][PASSES], xv[2][PASSES];  // of this row block and the next
         auto sides = [&](int mi) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
-                if constexpr (NEED_Y) yv[mi & 1][p] = load8(rY, offset(mi, p), valid, stream);
-                if constexpr (NEED_X) xv[mi & 1][p] = load8(rX, offset(mi, p), valid, stream);
+                if constexpr (NEED_Y) yv[mi & 1][p] = load(rY, offset(mi, p), valid, stream);
+                if constexpr (NEED_X) xv[mi & 1][p] = load(rX, offset(mi, p), valid, stream);
             }
         };
         sides(0);
@@ -586,13 +584,15 @@ struct GroupedTile {
             asm volatile("" ::: "memory");
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
-                const FL_LDS char *s = w + (p * RPP + lane / CPR) * EPI_ROW + (lane % CPR) * 32;
-                const f32x4_t lo = *(const FL_LDS f32x4_t *)s, hi = *(const FL_LDS f32x4_t *)(s + 16);
-                const uint32_t off = offset(mi, p);
-                float v[8], v2[8];
+                const FL_LDS char *s = w + (p * RPP + lane / CPR) * EPI_ROW + (lane % CPR) * (VEC * 4);
+                f32x4_t q[VEC / 4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float d = i < 4 ? lo[i & 3] : hi[i & 3];
+                for (int h = 0; h < VEC / 4; ++h) q[h] = *(const FL_LDS f32x4_t *)(s + h * 16);
+                const uint32_t off = offset(mi, p);
+                float v[VEC], v2[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float d = q[i >> 2][i & 3];
                     const float y = NEED_Y ? yv[mi & 1][p].get(i) : 0.0f;
                     if constexpr (PART) {
                         v[i] = d;
@@ -610,11 +610,11 @@ struct GroupedTile {
                     }
                 }
                 if (PART || (FORM == kFormGrad && a.dw_f32))
-                    store8_f32(v, rO, off, valid, stream);
+                    store_f32(v, rO, off, valid);
                 else
-                    store8(v, rO, off, valid, stream);
+                    store(v, rO, off, valid, stream);
                 if (!PART && (FORM == kFormFwd ? a.out2 != nullptr : FORM == kFormBwd && ACT == FL_ACT_GLU))
-                    store8(v2, rO2, off, valid, stream);
+                    store(v2, rO2, off, valid, stream);
             }
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
