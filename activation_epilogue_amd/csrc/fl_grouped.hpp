@@ -218,21 +218,25 @@ __global__ void __launch_bounds__(256) grouped_join_kernel(GroupedArgs a, int ac
 
 // The tiles of grouped_dma_kernel (fl_grouped_dma.hpp).  time: of a round (one
 // workgroup in every slot, 256 CUs x per_cu), in units of the widest tile's at
-// large sizes (8192x2 rows of 8 experts, K 4096, N 14336: 1030, 950, 810, 605
+// large sizes (8192x2 rows of 8 experts, K 4096, N 14336: 1030, 950, 810, 525
 // and 370 TFLOP/s; fp32, 4096x2 rows of 8 experts, K 2048, N 4096: 130 and 100,
 // but 20 and 14 us for 100x2 rows of 6 experts, K 768, N 1000).  128x128 fp32
 // tiles: 114 to 134 TFLOP/s, and half as much where there are few.
 struct GroupedTileShape {
     int bm, bn, per_cu;
     float time;
-    float stage;  // us of one stage where a CU has one workgroup
-    bool grad;    // compiled for the gradient too
+    float stage;   // us of one stage where a CU has one workgroup
+    float rate;    // TB/s of weights (8 experts of 4096x14336, few rows)
+    bool grad;     // compiled for the gradient too
 };
-enum GroupedVariant { kTile256x256 = 0, kTile256x128, kTile128x128, kTile64x128, kTile32x128, kTileF32, kTileF32x32, kGroupedVariants };
+enum GroupedVariant {
+    kTile256x256 = 0, kTile256x128, kTile128x128, kTile64x256, kTile32x128, kTileF32, kTileF32x32, kGroupedVariants
+};
 constexpr GroupedTileShape kGroupedTiles[kGroupedVariants] = {
-    {256, 256, 1, 1.0f, 1.9f, true}, {256, 128, 1, 0.54f, 0.95f, false}, {128, 128, 2, 0.64f, 0.5f, true},
-    {64, 128, 2, 0.425f, 0.25f, false}, {32, 128, 2, 0.35f, 0.23f, false}, {64, 64, 3, 1.0f, 0.58f, true},
-    {32, 64, 4, 0.8f, 0.3f, false}};
+    {256, 256, 1, 1.0f, 1.9f, 4.4f, true}, {256, 128, 1, 0.565f, 0.95f, 5.0f, false},
+    {128, 128, 2, 0.64f, 0.5f, 4.9f, true}, {64, 256, 1, 0.49f, 0.5f, 6.2f, false},
+    {32, 128, 2, 0.35f, 0.23f, 6.0f, false}, {64, 64, 3, 1.0f, 0.58f, 0.0f, true},
+    {32, 64, 4, 0.8f, 0.3f, 0.0f, false}};
 typedef void (*grouped_launcher)(const GroupedArgs &, int act, int64_t grid, hipStream_t);
 // One dtype and form to a compiled unit.
 template <int DT, int FORM>

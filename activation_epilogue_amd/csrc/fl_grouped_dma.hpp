@@ -238,10 +238,10 @@ struct GroupedTile {
                                 : FORM == kFormBwd ? (uint32_t)kt * 128
                                                    : (uint32_t)kt * 128 * (uint32_t)o.ldb;
             const bool ok = !CHECK || SideB::k(wave, lane, i) < kleft;
-            // few rows: every weight is read once, and streams past the L2
-            // (32 tokens through 64 experts 60.7 -> 53.8 us; taller tiles, of
-            // which a run may have several, lose: 110 -> 127 us at 96 rows)
-            if constexpr (BM <= 32)
+            // low tiles are for runs of one tile: every weight is read once, and
+            // streams past the L2 (32 tokens through 64 experts 60.7 -> 53.8
+            // us; with two or three tiles to a run it would be read again)
+            if constexpr (BM <= 64)
                 lds_copy16_nt(o.B.rsrc, ok ? o.B.off[i] : kOob, so, buf.b + i * 1024);
             else
                 lds_copy16(o.B.rsrc, ok ? o.B.off[i] : kOob, so, buf.b + i * 1024);

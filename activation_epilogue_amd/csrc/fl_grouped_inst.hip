@@ -26,7 +26,7 @@ grouped_launcher pick_grouped<FL_INST_DTYPE, FL_INST_FORM>(int variant) {
     if (variant == kTile256x256) return launch<256, 256, 2, 4, 2, 1>;
 #if FL_INST_FORM != 2
     if (variant == kTile256x128) return launch<256, 128, 4, 2, 3, 1>;
-    if (variant == kTile64x128) return launch<64, 128, 1, 4, 3, 2>;
+    if (variant == kTile64x256) return launch<64, 256, 2, 4, 4, 1>;
     if (variant == kTile32x128) return launch<32, 128, 1, 4, 4, 2>;
 #endif
     return launch<128, 128, 2, 2, 2, 2>;

@@ -262,7 +262,9 @@ void join(int dtype, int form, const fl::GroupedArgs &a, int act, hipStream_t st
 // The tile: the one of least estimated time, in rounds of
 // a full chip.  Runs end inside a tile, so S rows in R runs make about S/bm +
 // R/2 row tiles (at least R); rounds beyond the first end ragged, half a round
-// on average.
+// on average.  It is at least the time the weights take.  Wide low tiles stream weights best where they fill the chip and
+// runs have one of them (8 experts of 4096x14336, 32 rows each: 160 us, 202 with
+// 64x128 or 32x128; 64 experts of 2048x1408, 48 rows: 76, 82 and 102).
 //
 // Where the chosen tiles leave most of the chip idle and the sum is long, it is
 // cut into 4, 8 or 16 parts for more workgroups, whose fp32 sums another launch
@@ -289,9 +291,22 @@ GroupedPlan plan_grouped(int dtype, int form, int64_t S, int64_t N, int64_t K, i
             m = (double)S / t.bm + 0.5 * runs;
             m = m > runs ? m : runs;
         }
-        m *= (N + t.bn - 1) / t.bn;
-        const double x = m / (kCus * t.per_cu);
-        const double time = t.time * (x < 0.9 ? 1.0 : x + 0.5);
+        const double n = (N + t.bn - 1) / t.bn, x = m * n / (kCus * t.per_cu);
+        double time = t.time * (x <= 1.0 ? 1.0 : x + 0.5);
+        if (dtype != FL_F32 && form != fl::kFormGrad) {
+            if (v == fl::kTile64x256) {
+                if (x < 1.0) continue;
+                if (S <= 48 * E) time *= 0.7;
+            }
+            if (x <= 0.5 && t.per_cu == 2) time *= 0.75;  // workgroups with a CU to themselves
+            // tiles that are mostly empty skip their empty half
+            if (t.bm >= 128) time *= S <= E * t.bm / 4 ? 0.7 : S <= E * t.bm / 2 ? 0.85 : 1.0;
+            // the weights: low tiles read them once each, high ones once for a run
+            const double reads = (t.bm <= 64 ? m : (double)(E < S ? E : S)) * n;
+            const double memory = reads * t.bn * 128 / (t.rate * 1e6) / 1.9;  // of a round's 1.9 us a stage
+            time = time > memory ? time : memory;
+        }
+        m *= n;
         if (best.variant < 0 || time < least) {
             least = time;
             tiles = m;
