@@ -259,20 +259,21 @@ void join(int dtype, int form, const fl::GroupedArgs &a, int act, hipStream_t st
         join_form<fl::kFormFwd>(dtype, a, act, st);
 }
 
-// The tile: the one of least estimated time, in rounds of
-// a full chip.  Runs end inside a tile, so S rows in R runs make about S/bm +
-// R/2 row tiles (at least R); rounds beyond the first end ragged, half a round
-// on average.  It is at least the time the weights take.  Wide low tiles stream weights best where they fill the chip and
-// runs have one of them (8 experts of 4096x14336, 32 rows each: 160 us, 202 with
-// 64x128 or 32x128; 64 experts of 2048x1408, 48 rows: 76, 82 and 102).
+// The tile: the one of least estimated time, in rounds of a full chip.  Runs end
+// inside a tile, so S rows in R runs make about S/bm + R/2 row tiles (at least
+// R); rounds beyond the first end ragged, half a round on average; the time is
+// at least that of the weights.  Wide low tiles stream weights best where they
+// fill the chip and runs have one of them (8 experts of 4096x14336, 32 rows
+// each: 162 us, 202 with 64x128, 231 with 32x128; 64 experts of 2048x1408, 6 rows
+// each: 67 us, 57 with 32x128).
 //
 // Where the chosen tiles leave most of the chip idle and the sum is long, it is
 // cut into 4, 8 or 16 parts for more workgroups, whose fp32 sums another launch
 // joins (4 us and a little per part), if that takes clearly less time than the
-// stages of one workgroup, as far as the memory (6 TB/s) can follow.  Measured without and
-// with: bf16, one token through 2 of 8 experts, K 4096, N 1024: 19.4 -> 14.1 us;
-// fp32: 75.8 -> 20.8 us; weight gradient of 16384 rows, 2 experts, 256x256: 67.7
-// -> 15.9 us.
+// stages of one workgroup, as far as the memory (6 TB/s) can follow.  Measured
+// without and with: bf16, one token through 2 of 8 experts, K 4096, N 1024: 19.4
+// -> 14.1 us; fp32: 75.8 -> 20.8 us; weight gradient of 16384 rows, 2 experts,
+// 256x256: 67.7 -> 15.9 us.
 struct GroupedPlan {
     int variant, parts;
 };
