@@ -27,6 +27,7 @@ import torch
 from . import ACTS, FusedLinearError, _dev_ptr, _dtype_code, load_library
 
 SCORES = {"softmax": 0, "sigmoid": 1}
+_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 MOE_EXPORTS = ("fl_moe_route", "fl_moe_route_bwd", "fl_moe_plan", "fl_moe_plan_workspace_bytes", "fl_moe_gather",
                "fl_moe_combine", "fl_moe_combine_bwd", "fl_grouped_linear", "fl_grouped_workspace_bytes",
                "fl_grouped_linear_bwd", "fl_grouped_weight_grad", "fl_grouped_weight_grad_ws",
@@ -116,10 +117,20 @@ def _out(t, name, shape, dtype, like):
 
 
 def _ptr(t, name, dtype=None, shape=None, like=None):
-    p = _dev_ptr(t, name, dtype, shape)
-    if t is not None and like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    return p
+    """The device pointer of a contiguous tensor of that dtype and shape on
+    like's device (None for None and for nothing)."""
+    if t is None:
+        return None
+    if (t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)
+            and (like is None or t.get_device() == like.get_device())):
+        return t.data_ptr() or None
+    _dev_ptr(t, name, dtype, shape)  # says what is wrong
+    raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+
+
+def _code(dtype):
+    code = _CODES.get(dtype)
+    return _dtype_code(dtype) if code is None else code
 
 
 @functools.lru_cache(maxsize=64)
@@ -150,7 +161,7 @@ def moe_route(logits, k, bias=None, score="softmax", groups=1, top_groups=1, gro
     their keys; -1 with weight 0 where no unmasked expert is left."""
     T, E = _matrix(logits, "logits")
     opt = _route_options(score, groups, top_groups, group_top, renorm, scale)
-    code = _dtype_code(logits.dtype)
+    code = _code(logits.dtype)
     with _On(logits, stream) as st:
         weights = _out(weights, "weights", (T, k), torch.float32, logits)
         experts = _out(experts, "experts", (T, k), torch.int32, logits)
@@ -165,7 +176,7 @@ def moe_route_bwd(logits, experts, dweights, score="softmax", renorm=True, scale
     T, E = _matrix(logits, "logits")
     k = _matrix(experts, "experts")[1]
     opt = _route_options(score, 1, 1, 1, renorm, scale)
-    code = _dtype_code(logits.dtype)
+    code = _code(logits.dtype)
     with _On(logits, stream) as st:
         dlogits = _out(dlogits, "dlogits", (T, E), logits.dtype, logits)
         _ok(_lib().fl_moe_route_bwd(_ptr(logits, "logits"), _ptr(experts, "experts", torch.int32, (T, k), logits),
@@ -210,7 +221,7 @@ def moe_gather(X, index, rows=None, *, stream=None):
     with _On(X, stream) as st:
         rows = _out(rows, "rows", (S, H), X.dtype, X)
         _ok(_lib().fl_moe_gather(_ptr(X, "X"), _ptr(index, "index", torch.int32, (S,), X), rows.data_ptr() or None, T,
-                                 S, H, _dtype_code(X.dtype), st))
+                                 S, H, _code(X.dtype), st))
     return rows
 
 
@@ -224,7 +235,7 @@ def moe_combine(rows, row_of_slot, weights=None, R=None, out=None, *, stream=Non
         _ok(_lib().fl_moe_combine(_ptr(rows, "rows"), _ptr(row_of_slot, "row_of_slot", torch.int32, None, rows),
                                   _ptr(weights, "weights", torch.float32, (T, k), rows),
                                   _ptr(R, "R", rows.dtype, (T, H), rows), out.data_ptr() or None, T, k, S, H,
-                                  _dtype_code(rows.dtype), st))
+                                  _code(rows.dtype), st))
     return out
 
 
@@ -241,7 +252,7 @@ def moe_combine_bwd(dout, rows, row_of_slot, weights=None, drows=None, dweights=
         _ok(_lib().fl_moe_combine_bwd(_ptr(dout, "dout"), _ptr(rows, "rows", dout.dtype, (S, H), dout),
                                       _ptr(row_of_slot, "row_of_slot", torch.int32, (T, k), dout),
                                       _ptr(weights, "weights", torch.float32, (T, k), dout), drows.data_ptr() or None,
-                                      dweights.data_ptr() or None, T, k, S, H, _dtype_code(dout.dtype), st))
+                                      dweights.data_ptr() or None, T, k, S, H, _code(dout.dtype), st))
     return drows, dweights
 
 
@@ -249,7 +260,7 @@ def moe_combine_bwd(dout, rows, row_of_slot, weights=None, drows=None, dweights=
 def grouped_workspace_bytes(S, N, K, E, dtype):
     """Bytes of workspace fl_grouped_linear needs."""
     n = ctypes.c_size_t()
-    _ok(_lib().fl_grouped_workspace_bytes(S, N, K, E, _dtype_code(dtype) if not isinstance(dtype, int) else dtype,
+    _ok(_lib().fl_grouped_workspace_bytes(S, N, K, E, _code(dtype) if not isinstance(dtype, int) else dtype,
                                           ctypes.byref(n)))
     return n.value
 
@@ -258,7 +269,7 @@ def grouped_workspace_bytes(S, N, K, E, dtype):
 def grouped_grad_workspace_bytes(S, N, K, E, dtype):
     """Bytes of workspace fl_grouped_weight_grad_ws takes."""
     n = ctypes.c_size_t()
-    _ok(_lib().fl_grouped_grad_workspace_bytes(S, N, K, E, _dtype_code(dtype) if not isinstance(dtype, int) else dtype,
+    _ok(_lib().fl_grouped_grad_workspace_bytes(S, N, K, E, _code(dtype) if not isinstance(dtype, int) else dtype,
                                                ctypes.byref(n)))
     return n.value
 
@@ -277,7 +288,7 @@ def grouped_linear(A, B, offsets, bias=None, Y=None, act="relu", out=None, *, in
     E, _, N = B.shape
     S = A_rows if index is None else index.numel()
     dt = A.dtype
-    code = _dtype_code(dt)
+    code = _code(dt)
     need = grouped_workspace_bytes(S, N, K, E, code)
     with _On(A, stream) as st:
         out = _out(out, "out", (S, N), dt, A)
@@ -314,7 +325,7 @@ def grouped_linear_bwd(G, W, X, offsets, Y=None, act="relu", dX=None, dY=None, *
         _ok(_lib().fl_grouped_linear_bwd(
             _ptr(G, "G"), _ptr(offsets, "offsets", torch.int32, (E + 1,), G), _ptr(W, "W", dt, None, G),
             _ptr(X, "X", dt, (S, N), G), _ptr(Y, "Y", dt, (S, N), G), dX.data_ptr() or None,
-            _ptr(dY, "dY", dt, (S, N), G), S, N, K, E, ACTS[act], _dtype_code(dt), st))
+            _ptr(dY, "dY", dt, (S, N), G), S, N, K, E, ACTS[act], _code(dt), st))
     return dX, dY
 
 
@@ -328,7 +339,7 @@ def grouped_weight_grad(A, G, offsets, dbias=True, dW=None, dw_dtype=None, *, st
     N = _matrix(G, "G")[1]
     E = offsets.numel() - 1
     dt = A.dtype
-    code = _dtype_code(dt)
+    code = _code(dt)
     dw_dtype = dw_dtype or (dW.dtype if dW is not None else dt)
     need = grouped_grad_workspace_bytes(S, N, K, E, code)
     with _On(A, stream) as st:
@@ -342,5 +353,5 @@ def grouped_weight_grad(A, G, offsets, dbias=True, dW=None, dw_dtype=None, *, st
         _ok(_lib().fl_grouped_weight_grad_ws(
             _ptr(A, "A"), _ptr(G, "G", dt, (S, N), A), _ptr(offsets, "offsets", torch.int32, (E + 1,), A),
             dW.data_ptr() or None, _ptr(dbias, "dbias", torch.float32, (E, N), A), S, N, K, E, code,
-            _dtype_code(dw_dtype), _ptr(workspace, "workspace", None, None, A), _bytes(workspace), st))
+            _code(dw_dtype), _ptr(workspace, "workspace", None, None, A), _bytes(workspace), st))
     return dW, dbias
