@@ -2,7 +2,7 @@
 
   out[t] = x[t] + sum_j w[t,j] * (gelu(x[t] @ W1[e] + b1[e]) @ W2[e] + b2[e]),   e = experts[t,j]
 
-The router is a linear layer; its k best experts of each token (softmax or
+The router is a linear layer without a bias; its k best experts of each token (softmax or
 sigmoid scores, an optional balance bias and expert groups) are sorted into runs
 of rows by moe_plan, the experts' products run over those runs, and moe_combine
 brings the rows back.  forward() reads token rows through the plan, so that the
@@ -18,6 +18,13 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import activation_epilogue_amd as fl  # noqa: E402
+
+
+def every_row(x):
+    """The offsets of one expert that has every row of x: [0, rows]."""
+    T = x.shape[0]
+    return (torch.arange(0, T + 1, T, dtype=torch.int32, device=x.device) if T
+            else torch.zeros(2, dtype=torch.int32, device=x.device))
 
 
 class RoutedExperts:
@@ -42,7 +49,9 @@ class RoutedExperts:
 
     def forward(self, x, keep=False):
         """out (T,hidden) for x (T,hidden); with keep=True also what backward needs."""
-        logits = fl.fused_linear(x, self.Wr, act="none")
+        # the router's product is one expert that has every token: few tokens
+        # by a narrow weight are what the experts' low tiles are for
+        logits = fl.grouped_linear(x, self.Wr[None], every_row(x), act="none")
         weights, experts = fl.moe_route(logits, self.k, **self.weighting, **self.choice)
         plan = fl.moe_plan(experts, self.E)
         h = fl.grouped_linear(x, self.W1, plan.offsets, self.b1, act="gelu_tanh", index=plan.token_of_row, pre=keep)
@@ -62,10 +71,7 @@ class RoutedExperts:
         drows, _ = fl.grouped_linear_bwd(dpre, self.W1, None, o, act="none")
         dx = fl.moe_combine(drows, plan.row_of_slot, R=dout)
         dlogits = fl.moe_route_bwd(logits, experts, dweights, **self.weighting)
-        # the router's product is one expert that has every token
-        every = torch.zeros(2, dtype=torch.int32, device=x.device)
-        every[1:] = x.shape[0]
-        dWr, _ = fl.grouped_weight_grad(x, dlogits, every, dbias=None)
+        dWr, _ = fl.grouped_weight_grad(x, dlogits, every_row(x), dbias=None)
         dx = fl.fused_linear(dlogits, self.Wr.t().contiguous(), R=dx, act="none")
         return dx, {"Wr": dWr[0], "W1": dW1, "b1": db1, "W2": dW2, "b2": db2}
 

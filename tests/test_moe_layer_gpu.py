@@ -14,7 +14,7 @@ from gpu_util import say
 from moe_util import U32, act64, act_bound, act_grad64, act_grad_bound, unit
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
-from routed_experts import RoutedExperts  # noqa: E402
+from routed_experts import RoutedExperts, every_row  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
@@ -261,7 +261,7 @@ def test_layer_on_another_stream():
         got = layer.forward(x)
     s.synchronize()
     assert torch.equal(got, want)
-    logits = fl.fused_linear(x, layer.Wr, act="none")
+    logits = fl.grouped_linear(x, layer.Wr[None], every_row(x), act="none")
     s.wait_stream(torch.cuda.current_stream())
     w, e = fl.moe_route(logits, 2, stream=s)  # the stream as an argument
     plan = fl.moe_plan(e, 8, stream=s)
