@@ -49,7 +49,6 @@ struct RunTile {
     int e;       // expert, -1 past the last tile
     int lo, hi;  // its rows
     int m;       // tile within the run
-    int total;   // row tiles of all experts
 };
 
 // Row tiles of all experts: the runs cut into tiles of bm rows (each run from
@@ -70,7 +69,7 @@ __device__ __forceinline__ int count_run_tiles(const GroupedArgs &a, int bm) {
 // from its own start): every wave scans the runs 64 at a time.
 __device__ __forceinline__ RunTile find_run_tile(const GroupedArgs &a, int bm, int tile) {
     const int lane = threadIdx.x & 63;
-    RunTile t{-1, 0, 0, 0, 0};
+    RunTile t{-1, 0, 0, 0};
     int base = 0;
     for (int e0 = 0; e0 < a.E; e0 += 64) {
         const int e = e0 + lane;
@@ -92,7 +91,6 @@ __device__ __forceinline__ RunTile find_run_tile(const GroupedArgs &a, int bm, i
         }
         base += __builtin_amdgcn_readlane(incl, 63);
     }
-    t.total = base;
     return t;
 }
 
@@ -218,10 +216,11 @@ __global__ void __launch_bounds__(256) grouped_join_kernel(GroupedArgs a, int ac
 
 // The tiles of grouped_dma_kernel (fl_grouped_dma.hpp).  time: of a round (one
 // workgroup in every slot, 256 CUs x per_cu), in units of the widest tile's at
-// large sizes (8192x2 rows of 8 experts, K 4096, N 14336: 1030, 950, 810, 525
-// and 370 TFLOP/s; fp32, 4096x2 rows of 8 experts, K 2048, N 4096: 130 and 100,
-// but 20 and 14 us for 100x2 rows of 6 experts, K 768, N 1000).  128x128 fp32
-// tiles: 114 to 134 TFLOP/s, and half as much where there are few.
+// large sizes: 8192x2 rows of 8 experts, K 4096, N 14336 run at 1030, 950, 810,
+// 525 and 370 TFLOP/s (256x128 is set 5% above its time there, which chose right
+// at the sizes between); fp32, 4096x2 rows of 8 experts, K 2048, N 4096, at 130
+// and 100, but 100x2 rows of 6 experts, K 768, N 1000 in 20 and 14 us.  128x128
+// fp32 tiles: 114 to 134 TFLOP/s, and half as much where there are few.
 struct GroupedTileShape {
     int bm, bn, per_cu;
     float time;

@@ -542,16 +542,6 @@ struct Piece {
             *q = v[0];
         }
     }
-    __device__ __forceinline__ void store(void *p, int64_t i) const {
-        raw *q = static_cast<raw *>(p) + i;
-        if constexpr (VECTOR) {
-            u32x4_t w;
-            __builtin_memcpy(&w, v, 16);
-            *reinterpret_cast<u32x4_t *>(q) = w;
-        } else {
-            *q = v[0];
-        }
-    }
     __device__ __forceinline__ float get(int t) const { return io::to_f32(v[t]); }
     __device__ __forceinline__ void set(int t, float f) { v[t] = io::from_f32(f); }
 };
