@@ -66,6 +66,9 @@ LARGE = [
     ([129, 130, 0, 127, 260, 385, 3, 500], 777, 1033),
     ([2500], 64, 3333),
     ([4] * 64, 512, 1408),
+    ([30, 64, 65, 0, 17, 1] * 11, 201, 1403),
+    ([16] * 32 + [70, 0], 328, 3000),
+    ([2300, 2200, 0, 2500], 1291, 4001),
 ]
 
 
