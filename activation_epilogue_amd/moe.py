@@ -133,14 +133,18 @@ def _code(dtype):
     return _dtype_code(dtype) if code is None else code
 
 
-@functools.lru_cache(maxsize=64)
 def _route_options(score, groups, top_groups, group_top, renorm, scale):
+    # plain values: a cache would keep a tensor's first value by its identity
+    return _route_options_of(score, int(groups), int(top_groups), int(group_top), bool(renorm), float(scale))
+
+
+@functools.lru_cache(maxsize=64)
+def _route_options_of(score, groups, top_groups, group_top, renorm, scale):
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
     if scale == 0.0:
         raise ValueError("scale must not be 0")
-    return ctypes.byref(RouteOptions(SCORES[score], int(groups), int(top_groups), int(group_top), 0 if renorm else 1,
-                                     float(scale)))
+    return ctypes.byref(RouteOptions(SCORES[score], groups, top_groups, group_top, 0 if renorm else 1, scale))
 
 
 def _bytes(t):

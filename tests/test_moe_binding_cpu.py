@@ -1,0 +1,21 @@
+"""What the routed-experts binding makes of its arguments, without a GPU."""
+import pytest
+import torch
+
+from activation_epilogue_amd import moe
+
+
+def test_route_options_follow_a_tensor_changed_in_place():
+    """Options given as 0-dim tensors count with the value they have at the
+    call, not with that of an earlier call."""
+    scale, groups, renorm = torch.tensor(2.0), torch.tensor(2), torch.tensor(True)
+    first = moe._route_options("softmax", groups, 1, 1, renorm, scale)._obj
+    assert (first.scale, first.groups, first.raw) == (2.0, 2, 0)
+    scale.fill_(3.0)
+    groups.fill_(4)
+    renorm.fill_(False)
+    again = moe._route_options("softmax", groups, 1, 1, renorm, scale)._obj
+    assert (again.scale, again.groups, again.raw) == (3.0, 4, 1)
+    scale.fill_(0.0)
+    with pytest.raises(ValueError, match="scale"):
+        moe._route_options("softmax", groups, 1, 1, renorm, scale)
