@@ -142,9 +142,10 @@ def _route_options(score, groups, top_groups, group_top, renorm, scale):
 def _route_options_of(score, groups, top_groups, group_top, renorm, scale):
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
-    if scale == 0.0:
-        raise ValueError("scale must not be 0")
-    return ctypes.byref(RouteOptions(SCORES[score], groups, top_groups, group_top, 0 if renorm else 1, scale))
+    opt = RouteOptions(SCORES[score], groups, top_groups, group_top, 0 if renorm else 1, scale)
+    if opt.scale == 0.0:  # (the library's default)
+        raise ValueError(f"scale must not be 0 in 32 bits, got {scale}")
+    return ctypes.byref(opt)
 
 
 def _bytes(t):

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import activation_epilogue_amd as fl
 from activation_epilogue_amd import moe
 
 
@@ -19,3 +20,12 @@ def test_route_options_follow_a_tensor_changed_in_place():
     scale.fill_(0.0)
     with pytest.raises(ValueError, match="scale"):
         moe._route_options("softmax", groups, 1, 1, renorm, scale)
+
+
+@pytest.mark.parametrize("scale", [1e-50, -1e-46, 2.0 ** -151])
+def test_a_scale_that_is_zero_in_32_bits_is_refused(scale):
+    """The library takes 0 for 1, so that a scale too small for a float would
+    count as none at all."""
+    with pytest.raises(ValueError, match="scale"):
+        fl.moe_route(torch.zeros(4, 8), 2, scale=scale)
+    assert moe._route_options("softmax", 1, 1, 1, True, 2.0 ** -149)._obj.scale == 2.0 ** -149
