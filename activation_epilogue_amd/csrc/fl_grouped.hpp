@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(1024) grouped_column_sum_kernel(GroupedArgs a)
     if (at >= 0) {
         constexpr int W = PER * io::size / 16;
 #pragma unroll 4
-        for (int64_t r = lo + g; r < hi; r += kRowGroups) {
+        for (int64_t r = (int64_t)lo + g; r < hi; r += kRowGroups) {
             const u32x4_unaligned *p = reinterpret_cast<const u32x4_unaligned *>(G + r * a.N + at);
             raw v[PER];
 #pragma unroll
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(1024) grouped_column_sum_kernel(GroupedArgs a)
             for (int t = 0; t < PER; ++t) sum[t] += io::to_f32(v[t]);
         }
     } else {  // fewer than 8 columns in all
-        for (int64_t r = lo + g; r < hi; r += kRowGroups)
+        for (int64_t r = (int64_t)lo + g; r < hi; r += kRowGroups)
             for (int t = 0; t < PER; ++t)
                 if (at + t >= 0) sum[t] += io::to_f32(G[r * a.N + at + t]);
     }
