@@ -45,6 +45,10 @@ __device__ __forceinline__ int run_bound(const GroupedArgs &a, int e) {
     return v < 0 ? 0 : v > a.S ? a.S : v;
 }
 
+// Row tiles of a run of `rows` rows (which may be next to 2^31, so nothing is
+// added to them).
+__device__ __forceinline__ int row_tiles(int rows, int bm) { return rows > 0 ? (rows - 1) / bm + 1 : 0; }
+
 struct RunTile {
     int e;       // expert, -1 past the last tile
     int lo, hi;  // its rows
@@ -58,7 +62,7 @@ __device__ __forceinline__ int count_run_tiles(const GroupedArgs &a, int bm) {
     int n = 0;
     for (int e = lane; e < a.E; e += 64) {
         const int lo = run_bound(a, e), hi = run_bound(a, e + 1);
-        n += hi > lo ? (hi - lo + bm - 1) / bm : 0;
+        n += row_tiles(hi - lo, bm);
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o);
@@ -74,7 +78,7 @@ __device__ __forceinline__ RunTile find_run_tile(const GroupedArgs &a, int bm, i
     for (int e0 = 0; e0 < a.E; e0 += 64) {
         const int e = e0 + lane;
         const int lo = e < a.E ? run_bound(a, e) : 0, hi = e < a.E ? run_bound(a, e + 1) : 0;
-        const int n = hi > lo ? (hi - lo + bm - 1) / bm : 0;
+        const int n = row_tiles(hi - lo, bm);
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {

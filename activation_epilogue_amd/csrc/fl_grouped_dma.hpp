@@ -227,7 +227,7 @@ struct GroupedTile {
     // the waits are on constants.
     template <int I, bool CHECK>
     __device__ __forceinline__ static void copy_one(const Ops &o, int kt, Dst buf, int wave, int lane) {
-        const int kleft = o.depth - kt * KS;
+        const int kleft = (int)((uint32_t)o.depth - (uint32_t)kt * KS);  // (kt * KS may pass 2^31 by itself)
         if constexpr (I < SideA::COPIES) {
             const uint32_t so = FORM == kFormGrad ? 0 : (uint32_t)kt * 128;
             const bool ok = !CHECK || SideA::k(wave, lane, I) < kleft;
@@ -651,7 +651,7 @@ struct GroupedTile {
             const int q = pid / a.tiles_n;
             const RunTile r = find_run_tile(a, BM, q);
             if (r.e < 0) return false;
-            const int cnt = (r.hi - r.lo + BM - 1) / BM;
+            const int cnt = row_tiles(r.hi - r.lo, BM);
             const int local = pid - (q - r.m) * a.tiles_n;
             if (r.m < 0 || r.m >= cnt || local < 0) return false;  // (offsets that are no plan's)
             grouped_tile(a.spread ? xcd_logical(local, cnt * a.tiles_n) : local, cnt, a.tiles_n, a.group, m, t.tn);

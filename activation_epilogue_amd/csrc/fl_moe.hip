@@ -356,7 +356,8 @@ fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void 
     a.part = static_cast<float *>(workspace);
     const int64_t tiles_m = form == fl::kFormGrad ? a.E * (((int64_t)a.K + t.bm - 1) / t.bm) : most_row_tiles(a.S, a.E, t.bm);
     const int64_t tiles = tiles_m * a.tiles_n, grid = tiles * a.parts, slots = kCus * t.per_cu;
-    if (grid > kMaxDim) return fail(FL_ERR_UNSUPPORTED, "too many output tiles");
+    if (grid > kMaxDim - slots)  // (a workgroup's next tile is its last plus the grid)
+        return fail(FL_ERR_UNSUPPORTED, "too many output tiles");
     a.max_tiles = (int)tiles;
     if (form == fl::kFormGrad && a.dbias) {
         if (dtype == FL_F32)

@@ -33,3 +33,31 @@ def test_bias_gradient_of_the_last_rows(N):
     want = torch.stack([tail[:5].sum(0), tail[5:295].sum(0), torch.zeros(N, device="cuda"), tail[295:].sum(0),
                         torch.zeros(N, device="cuda")])
     assert torch.equal(dbias, want)
+
+
+@pytest.mark.parametrize("form", ["forward", "backward", "gradient"])
+def test_a_run_of_every_row_up_to_the_last(form):
+    """One run of 2^31 - 1 rows: one product a row, rounded once, or one sum
+    of whole numbers below 2^8, exact in every order."""
+    say("a run of 2^31 - 1 rows", form)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    A = torch.empty(LAST, 1, dtype=torch.bfloat16, device="cuda")
+    if form == "gradient":
+        A.zero_()
+        A[:: 2 ** 24] = 1.0
+        A[-3:] = -2.0
+        G = torch.full((LAST, 1), 3.0, dtype=torch.bfloat16, device="cuda")
+        dW, _ = fl.grouped_weight_grad(A, G, offsets(0, LAST, LAST), dbias=None)
+        assert dW.flatten().tolist() == [3.0 * (128 - 6), 0.0]
+        return
+    A.normal_(generator=g)
+    w = torch.tensor([[[1.7]], [[math.nan]]], dtype=torch.bfloat16, device="cuda")
+    out = torch.full((LAST, 1), math.nan, dtype=torch.bfloat16, device="cuda")
+    o = offsets(0, LAST, LAST)
+    if form == "forward":
+        fl.grouped_linear(A, w, o, act="none", out=out)
+    else:
+        fl.grouped_linear_bwd(A, w, None, o, act="none", dX=out)
+    for lo in range(0, LAST, 2 ** 28):
+        a, got = A[lo:lo + 2 ** 28], out[lo:lo + 2 ** 28]
+        assert torch.equal(got, (a.float() * w[0, 0].float()).to(torch.bfloat16)), lo
