@@ -628,6 +628,7 @@ struct GroupedTile {
     // column.
     __device__ __forceinline__ static bool find(const GroupedArgs &a, int b, int n, Tile &t) {
         t.part = 0;
+        if (n <= 0) return false;  // (no expert has a row)
         if (a.parts > 1) {
             t.part = b / n;
             if (t.part >= a.parts) return false;

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import activation_epilogue_amd as fl
+from activation_epilogue_amd import moe
 from gpu_util import say
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +62,19 @@ def test_a_run_of_every_row_up_to_the_last(form):
     for lo in range(0, LAST, 2 ** 28):
         a, got = A[lo:lo + 2 ** 28], out[lo:lo + 2 ** 28]
         assert torch.equal(got, (a.float() * w[0, 0].float()).to(torch.bfloat16)), lo
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("indexed", [False, True])
+def test_parts_of_runs_that_are_all_empty(indexed, dtype):
+    """Sums in parts where every slot was dropped: nothing is written."""
+    S, K, N, E = 2, 4096, 64, 3
+    assert moe.grouped_workspace_bytes(S, N, K, E, dtype) > 0
+    say("parts of empty runs", indexed, dtype)
+    A = torch.ones(S, K, dtype=dtype, device="cuda")
+    B = torch.ones(E, K, N, dtype=dtype, device="cuda")
+    index = offsets(-1, -1) if indexed else None
+    for first in (0, 1, S):
+        out, pre = (torch.full((S, N), math.nan, dtype=dtype, device="cuda") for _ in range(2))
+        fl.grouped_linear(A, B, offsets(*[first] * (E + 1)), act="relu", out=out, pre=pre, index=index)
+        assert bool(torch.isnan(out).all()) and bool(torch.isnan(pre).all())
