@@ -115,8 +115,7 @@ __global__ void __launch_bounds__(1024) grouped_column_sum_kernel(GroupedArgs a)
     // end of a row it loads the row's last 8 and keeps its own
     constexpr int PER = 8;
     __shared__ float part[kRowGroups][kColumns];
-    const int blocks_n = (a.N + kColumns - 1) / kColumns;
-    const int e = blockIdx.x / blocks_n, c0 = (blockIdx.x % blocks_n) * kColumns;
+    const int e = blockIdx.y, c0 = blockIdx.x * kColumns;
     const int g = threadIdx.x / (kColumns / PER), c = c0 + (threadIdx.x % (kColumns / PER)) * PER;
     const int lo = run_bound(a, e), hi = run_bound(a, e + 1);
     const raw *G = static_cast<const raw *>(a.B);

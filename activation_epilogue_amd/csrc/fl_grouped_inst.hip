@@ -36,8 +36,9 @@ grouped_launcher pick_grouped<FL_INST_DTYPE, FL_INST_FORM>(int variant) {
 #if FL_INST_FORM == 2
 template <>
 void launch_column_sum<FL_INST_DTYPE>(const GroupedArgs &a, hipStream_t s) {
-    const unsigned blocks = (unsigned)a.E * (unsigned)((a.N + kColumns - 1) / kColumns);
-    hipLaunchKernelGGL((grouped_column_sum_kernel<FL_INST_DTYPE>), dim3(blocks), dim3(1024), 0, s, a);
+    // (a dimension of a launch has less than 2^32 threads: not both in one)
+    const dim3 grid((unsigned)((a.N + kColumns - 1) / kColumns), (unsigned)a.E);
+    hipLaunchKernelGGL((grouped_column_sum_kernel<FL_INST_DTYPE>), grid, dim3(1024), 0, s, a);
 }
 #endif
 

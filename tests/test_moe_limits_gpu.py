@@ -78,3 +78,17 @@ def test_parts_of_runs_that_are_all_empty(indexed, dtype):
         out, pre = (torch.full((S, N), math.nan, dtype=dtype, device="cuda") for _ in range(2))
         fl.grouped_linear(A, B, offsets(*[first] * (E + 1)), act="relu", out=out, pre=pre, index=index)
         assert bool(torch.isnan(out).all()) and bool(torch.isnan(pre).all())
+
+
+def test_bias_gradient_of_many_experts_and_columns():
+    """1024 experts by 2^19 columns: 2^22 blocks of 1024 threads."""
+    S, N, E = 4, 2 ** 19, 1024
+    say("bias gradient of", E, "experts,", N, "columns")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    G = torch.randint(-8, 9, (S, N), generator=g, device="cuda").to(torch.bfloat16)
+    A = torch.ones(S, 0, dtype=torch.bfloat16, device="cuda")
+    o = offsets(0, *[1] * (E - 1), S)
+    dbias = torch.full((E, N), math.nan, device="cuda")
+    fl.grouped_weight_grad(A, G, o, dbias=dbias)
+    assert torch.equal(dbias[0], G[0].float()) and torch.equal(dbias[-1], G[1:].float().sum(0))
+    assert bool((dbias[1:-1] == 0).all())
