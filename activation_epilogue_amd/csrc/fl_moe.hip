@@ -442,7 +442,7 @@ fl_status fl_moe_plan_workspace_bytes(int64_t T, int64_t k, int64_t E, size_t *b
         return fail(FL_ERR_UNSUPPORTED, "E (%lld) must be 1 to %d", (long long)E, fl::kMaxExperts);
     if ((s = check_slots(T, k)) != FL_OK) return s;
     const int64_t blocks = (T * k + fl::kPlanChunk - 1) / fl::kPlanChunk;
-    *bytes = blocks > 1 ? (size_t)blocks * E * 4 : 0;
+    *bytes = blocks > 1 ? (size_t)(blocks + (blocks > fl::kPlanDirect)) * E * 4 : 0;
     return FL_OK;
 }
 
@@ -473,6 +473,13 @@ fl_status fl_moe_plan(const int32_t *experts, int32_t *offsets, int32_t *token_o
     const dim3 grid((unsigned)(blocks ? blocks : 1));
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (need) hipLaunchKernelGGL(fl::plan_count_kernel, grid, dim3(1024), 0, st, a);
+    a.summed = blocks > fl::kPlanDirect;
+    if (a.summed) {
+        int cols = 64;
+        while (cols > 8 && cols / 2 >= E) cols /= 2;
+        hipLaunchKernelGGL(fl::plan_sum_kernel, dim3((unsigned)((E + cols - 1) / cols)), dim3(1024), 0, st, a,
+                           (int)blocks, cols);
+    }
     if (a.S <= fl::kPlanSmall) {
         if (E <= 256)
             hipLaunchKernelGGL((fl::plan_kernel<4, 256>), grid, dim3(256), 0, st, a);

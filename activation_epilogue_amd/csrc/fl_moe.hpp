@@ -362,6 +362,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
 // (6.3 MB).
 constexpr int kPlanRun = 256;
 constexpr int kPlanSmall = 4 * kPlanRun, kPlanChunk = 16 * kPlanRun;
+constexpr int kPlanDirect = 512;
 
 struct PlanArgs {
     const int32_t *experts;
@@ -369,6 +370,7 @@ struct PlanArgs {
     int32_t *counts;  // (blocks, E), null for one block
     int64_t S;
     int k, E;
+    int summed;       // counts hold the rows before each block instead, and a line of totals
 };
 
 __device__ __forceinline__ int slot_expert(const PlanArgs &a, int64_t s) {
@@ -388,6 +390,39 @@ __global__ void __launch_bounds__(1024) plan_count_kernel(PlanArgs a) {
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += 1024) a.counts[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+}
+
+// Turns counts, (blocks, E), into every expert's rows before each block, with
+// a line of totals behind them: a block takes `cols` experts (a power of two, at
+// most 64), cut into 1024 / cols runs of lines.
+__global__ void __launch_bounds__(1024) plan_sum_kernel(PlanArgs a, int blocks, int cols) {
+    __shared__ int sums[1024];
+    const int x = threadIdx.x % cols, part = threadIdx.x / cols, parts = 1024 / cols;
+    const int e = blockIdx.x * cols + x;
+    const int per = (blocks + parts - 1) / parts;
+    const int b0 = part * per < blocks ? part * per : blocks, b1 = b0 + per < blocks ? b0 + per : blocks;
+    int sum = 0;
+    if (e < a.E) {
+#pragma unroll 8
+        for (int b = b0; b < b1; ++b) sum += a.counts[(int64_t)b * a.E + e];
+    }
+    sums[threadIdx.x] = sum;
+    __syncthreads();
+    if (e >= a.E) return;
+    int at = 0;
+    for (int p = 0; p < part; ++p) at += sums[p * cols + x];
+    constexpr int AHEAD = 8;  // lines loaded before they are written over
+    for (int b = b0; b < b1; b += AHEAD) {
+        int c[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) c[i] = b + i < b1 ? a.counts[(int64_t)(b + i) * a.E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (b + i < b1) a.counts[(int64_t)(b + i) * a.E + e] = at;
+            at += c[i];
+        }
+    }
+    if (part == parts - 1) a.counts[(int64_t)blocks * a.E + e] = at;
 }
 
 // EC: an upper limit of E, a power of two.
@@ -411,7 +446,7 @@ __global__ void __launch_bounds__(64 * WAVES) plan_kernel(PlanArgs a) {
         if (ex[i] >= 0) atomicAdd(&run[wave][ex[i]], 1);
     __syncthreads();
     // every expert's rows in earlier blocks, and in all of them
-    if (a.counts) {
+    if (a.counts && !a.summed) {
         const int part = tid / EC;
         for (int e = tid % EC; e < a.E; e += PARTS == 1 ? THREADS : EC) {
             int all = 0, prev = 0;
@@ -428,7 +463,10 @@ __global__ void __launch_bounds__(64 * WAVES) plan_kernel(PlanArgs a) {
     }
     for (int e = tid; e < a.E; e += THREADS) {
         int all = 0, prev = 0;
-        if (a.counts) {
+        if (a.summed) {
+            all = a.counts[(int64_t)gridDim.x * a.E + e];
+            prev = a.counts[(int64_t)blockIdx.x * a.E + e];
+        } else if (a.counts) {
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
                 all += sums[p][e];
