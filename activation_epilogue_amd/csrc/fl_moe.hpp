@@ -360,9 +360,14 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(RouteArgs a) {
 // several, a launch before them counts every block's slots.  Bound by the
 // latency of its phases: 192 slots 4.0 us, 524288 slots of 256 experts 3 + 10 us
 // (6.3 MB).
+// Up to kPlanDirect blocks each adds the counts of all of them by itself, which
+// saves a launch but grows with their square; above, a launch between sums them
+// (256 experts, all launches: 256 blocks 18.5 us each adding and 19.2 summed, 512
+// blocks 36 and 30, 2048 blocks 277 and 91; 1024 experts: 2048 blocks 893 and
+// 141; 2^28 slots of 256 experts 3.3 ms).
 constexpr int kPlanRun = 256;
 constexpr int kPlanSmall = 4 * kPlanRun, kPlanChunk = 16 * kPlanRun;
-constexpr int kPlanDirect = 512;
+constexpr int kPlanDirect = 256;
 
 struct PlanArgs {
     const int32_t *experts;

@@ -43,7 +43,7 @@ def check_plan(e, E, plan, k):
 
 
 @pytest.mark.parametrize("T,k,E", [
-    (4096 * 512, 1, 8), (4096 * 512 + 1, 1, 8), (1_048_577, 2, 3), (700_001, 7, 256), (600_000, 5, 1024),
+    (4096 * 256, 1, 8), (4096 * 256 + 1, 1, 8), (4096 * 512, 1, 8), (4096 * 512 + 1, 1, 8), (1_048_577, 2, 3), (700_001, 7, 256), (600_000, 5, 1024),
     (3_000_000, 1, 65), (9_000_001, 2, 1), (2_500_000, 8, 200)])
 def test_plan_of_many_blocks(T, k, E):
     g = torch.Generator(device="cuda").manual_seed(E)
