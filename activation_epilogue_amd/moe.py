@@ -83,8 +83,8 @@ def _ok(status):
 
 
 class _On:
-    """The stream a call runs on: the given one, or the current one of t's
-    device; that device and stream are current while the call allocates and
+    """The stream a call runs on: the given one (of t's device), or the current
+    one of t's device; that device and stream are current while the call allocates and
     launches, so its temporary and result tensors belong to that stream."""
     __slots__ = ("ctx", "index")
 
@@ -94,6 +94,8 @@ class _On:
         self.ctx = None
         self.index = t.device.index
         if stream is not None:
+            if stream.device != t.device:
+                raise ValueError(f"stream is on {stream.device}, expected {t.device}")
             self.ctx = torch.cuda.stream(stream)
         elif self.index != torch.cuda.current_device():
             self.ctx = torch.cuda.device(self.index)

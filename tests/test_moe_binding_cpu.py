@@ -1,4 +1,6 @@
 """What the routed-experts binding makes of its arguments, without a GPU."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -29,3 +31,12 @@ def test_a_scale_that_is_zero_in_32_bits_is_refused(scale):
     with pytest.raises(ValueError, match="scale"):
         fl.moe_route(torch.zeros(4, 8), 2, scale=scale)
     assert moe._route_options("softmax", 1, 1, 1, True, 2.0 ** -149)._obj.scale == 2.0 ** -149
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The call would run on the operands' device's current stream instead, in
+    no order with the stream that was asked for."""
+    operand = SimpleNamespace(is_cuda=True, device=torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="stream is on cuda:1, expected cuda:0"):
+        moe._On(operand, SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0))
+    assert moe._On(operand, SimpleNamespace(device=torch.device("cuda", 0), cuda_stream=0)).index == 0
