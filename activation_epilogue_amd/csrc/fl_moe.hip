@@ -555,8 +555,10 @@ fl_status fl_moe_combine_bwd(const void *dout, const void *rows, const int32_t *
     if (s != FL_OK) return s;
     if ((s = check_sizes({T, k, S, H})) != FL_OK) return s;
     if ((s = check_slots(T, k)) != FL_OK) return s;
-    if (!drows && !dweights) return fail(FL_ERR_INVALID_ARG, "drows and dweights are both NULL");
     const size_t es = elem_size(dtype), slots = (size_t)T * k;
+    // (an empty output has no address)
+    if (!drows && !dweights && slots && S && H)
+        return fail(FL_ERR_INVALID_ARG, "drows and dweights are both NULL");
     const Operand ops[] = {{"dout", dout, (size_t)T * H * es, es, false, false, nullptr},
                            {"rows", rows, dweights ? (size_t)S * H * es : 0, es, false, !dweights, nullptr},
                            {"row_of_slot", row_of_slot, slots * 4, 4, false, false, nullptr},
@@ -564,7 +566,7 @@ fl_status fl_moe_combine_bwd(const void *dout, const void *rows, const int32_t *
                            {"drows", drows, (size_t)S * H * es, es, true, true, rows},
                            {"dweights", dweights, slots * 4, 4, true, true, nullptr}};
     if ((s = check_operands(ops)) != FL_OK) return s;
-    if (slots == 0) return FL_OK;
+    if (slots == 0 || (!drows && !dweights)) return FL_OK;
     fl::MoveArgs a{};
     a.src = dout;
     a.src2 = rows;
