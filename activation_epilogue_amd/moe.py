@@ -249,17 +249,20 @@ def moe_combine(rows, row_of_slot, weights=None, R=None, out=None, *, stream=Non
 def moe_combine_bwd(dout, rows, row_of_slot, weights=None, drows=None, dweights=None, *, stream=None):
     """The gradients of moe_combine's rows and weights (fl_moe_combine_bwd).
     Rows that no slot points at keep what drows held (unset where it is
-    allocated here)."""
+    allocated here).  drows=False or dweights=False leaves one of them out (None
+    in its place); rows are read for dweights only."""
     T, H = _matrix(dout, "dout")
     S = _matrix(rows, "rows")[0]
     k = _matrix(row_of_slot, "row_of_slot")[1]
     with _On(dout, stream) as st:
-        drows = _out(drows, "drows", (S, H), dout.dtype, dout)
-        dweights = _out(dweights, "dweights", (T, k), torch.float32, dout)
+        drows = None if drows is False else _out(drows, "drows", (S, H), dout.dtype, dout)
+        dweights = None if dweights is False else _out(dweights, "dweights", (T, k), torch.float32, dout)
         _ok(_lib().fl_moe_combine_bwd(_ptr(dout, "dout"), _ptr(rows, "rows", dout.dtype, (S, H), dout),
                                       _ptr(row_of_slot, "row_of_slot", torch.int32, (T, k), dout),
-                                      _ptr(weights, "weights", torch.float32, (T, k), dout), drows.data_ptr() or None,
-                                      dweights.data_ptr() or None, T, k, S, H, _code(dout.dtype), st))
+                                      _ptr(weights, "weights", torch.float32, (T, k), dout),
+                                      None if drows is None else drows.data_ptr() or None,
+                                      None if dweights is None else dweights.data_ptr() or None, T, k, S, H,
+                                      _code(dout.dtype), st))
     return drows, dweights
 
 
