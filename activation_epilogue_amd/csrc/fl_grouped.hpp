@@ -240,9 +240,10 @@ constexpr GroupedTileShape kGroupedTiles[kGroupedVariants] = {
     {32, 128, 2, 0.35f, 0.23f, 6.0f, false}, {64, 64, 3, 1.0f, 0.58f, 0.0f, true},
     {32, 64, 4, 0.8f, 0.3f, 0.0f, false}};
 typedef void (*grouped_launcher)(const GroupedArgs &, int act, int64_t grid, hipStream_t);
-// One dtype and form to a compiled unit.
+// One dtype and form to a compiled unit.  nt: the weights pass the L2 by (tiles of
+// at most 64 rows only).
 template <int DT, int FORM>
-grouped_launcher pick_grouped(int variant);
+grouped_launcher pick_grouped(int variant, bool nt);
 template <int DT>
 void launch_column_sum(const GroupedArgs &a, hipStream_t s);
 template <int DT, int FORM>

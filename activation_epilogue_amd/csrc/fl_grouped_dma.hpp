@@ -179,8 +179,9 @@ struct GroupedSide {
     }
 };
 
-// One tile of BM x BN outputs on WM x WN waves.  NBUF stages of LDS.
-template <int DT, int FORM, int BM_, int BN_, int WM, int WN, int NBUF_>
+// One tile of BM x BN outputs on WM x WN waves.  NBUF stages of LDS.  NT: the
+// weights stream past the L2.
+template <int DT, int FORM, int BM_, int BN_, int WM, int WN, int NBUF_, bool NT>
 struct GroupedTile {
     using io = Io<DT>;
     using raw = typename io::raw;
@@ -238,10 +239,7 @@ struct GroupedTile {
                                 : FORM == kFormBwd ? (uint32_t)kt * 128
                                                    : (uint32_t)kt * 128 * (uint32_t)o.ldb;
             const bool ok = !CHECK || SideB::k(wave, lane, i) < kleft;
-            // low tiles are for runs of one tile: every weight is read once, and
-            // streams past the L2 (32 tokens through 64 experts 60.7 -> 53.8
-            // us; with two or three tiles to a run it would be read again)
-            if constexpr (BM <= 64)
+            if constexpr (NT)
                 lds_copy16_nt(o.B.rsrc, ok ? o.B.off[i] : kOob, so, buf.b + i * 1024);
             else
                 lds_copy16(o.B.rsrc, ok ? o.B.off[i] : kOob, so, buf.b + i * 1024);
@@ -785,9 +783,9 @@ struct GroupedTile {
     }
 };
 
-template <int DT, int FORM, int BM, int BN, int WM, int WN, int NBUF, int OCC>
+template <int DT, int FORM, int BM, int BN, int WM, int WN, int NBUF, int OCC, bool NT>
 __global__ void __launch_bounds__(64 * WM * WN, OCC) grouped_dma_kernel(GroupedArgs a, int act) {
-    using T = GroupedTile<DT, FORM, BM, BN, WM, WN, NBUF>;
+    using T = GroupedTile<DT, FORM, BM, BN, WM, WN, NBUF, NT>;
     __shared__ __attribute__((aligned(1024))) char smem[T::SMEM];
     T::run(a, act, smem);
 }

@@ -9,27 +9,35 @@
 
 namespace fl {
 
-template <int BM, int BN, int WM, int WN, int NBUF, int OCC>
+template <int BM, int BN, int WM, int WN, int NBUF, int OCC, bool NT>
 static void launch(const GroupedArgs &a, int act, int64_t grid, hipStream_t s) {
-    hipLaunchKernelGGL((grouped_dma_kernel<FL_INST_DTYPE, FL_INST_FORM, BM, BN, WM, WN, NBUF, OCC>),
+    hipLaunchKernelGGL((grouped_dma_kernel<FL_INST_DTYPE, FL_INST_FORM, BM, BN, WM, WN, NBUF, OCC, NT>),
                        dim3((unsigned)grid), dim3(64 * WM * WN), 0, s, a, act);
 }
 
+template <int BM, int BN, int WM, int WN, int NBUF, int OCC>
+static grouped_launcher low(bool nt) {
+    return nt ? launch<BM, BN, WM, WN, NBUF, OCC, true> : launch<BM, BN, WM, WN, NBUF, OCC, false>;
+}
+
 template <>
-grouped_launcher pick_grouped<FL_INST_DTYPE, FL_INST_FORM>(int variant) {
+grouped_launcher pick_grouped<FL_INST_DTYPE, FL_INST_FORM>(int variant, bool nt) {
+#if FL_INST_FORM == 2  // (every operand is read by several tiles)
 #if FL_INST_DTYPE == 0
-#if FL_INST_FORM != 2
-    if (variant == kTileF32x32) return launch<32, 64, 2, 2, 3, 4>;
-#endif
-    return launch<64, 64, 2, 2, 3, 3>;
+    return launch<64, 64, 2, 2, 3, 3, false>;
 #else
-    if (variant == kTile256x256) return launch<256, 256, 2, 4, 2, 1>;
-#if FL_INST_FORM != 2
-    if (variant == kTile256x128) return launch<256, 128, 4, 2, 3, 1>;
-    if (variant == kTile64x256) return launch<64, 256, 2, 4, 4, 1>;
-    if (variant == kTile32x128) return launch<32, 128, 1, 4, 4, 2>;
+    if (variant == kTile256x256) return launch<256, 256, 2, 4, 2, 1, false>;
+    return launch<128, 128, 2, 2, 2, 2, false>;
 #endif
-    return launch<128, 128, 2, 2, 2, 2>;
+#elif FL_INST_DTYPE == 0
+    if (variant == kTileF32x32) return low<32, 64, 2, 2, 3, 4>(nt);
+    return low<64, 64, 2, 2, 3, 3>(nt);
+#else
+    if (variant == kTile256x256) return launch<256, 256, 2, 4, 2, 1, false>;
+    if (variant == kTile256x128) return launch<256, 128, 4, 2, 3, 1, false>;
+    if (variant == kTile64x256) return low<64, 256, 2, 4, 4, 1>(nt);
+    if (variant == kTile32x128) return low<32, 128, 1, 4, 4, 2>(nt);
+    return launch<128, 128, 2, 2, 2, 2, false>;
 #endif
 }
 

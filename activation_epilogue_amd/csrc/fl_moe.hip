@@ -230,16 +230,16 @@ int64_t most_row_tiles(int64_t S, int64_t E, int64_t bm) {
 }
 
 template <int DT>
-fl::grouped_launcher pick_grouped_dt(int form, int variant) {
-    return form == fl::kFormFwd   ? fl::pick_grouped<DT, fl::kFormFwd>(variant)
-           : form == fl::kFormBwd ? fl::pick_grouped<DT, fl::kFormBwd>(variant)
-                                  : fl::pick_grouped<DT, fl::kFormGrad>(variant);
+fl::grouped_launcher pick_grouped_dt(int form, int variant, bool nt) {
+    return form == fl::kFormFwd   ? fl::pick_grouped<DT, fl::kFormFwd>(variant, nt)
+           : form == fl::kFormBwd ? fl::pick_grouped<DT, fl::kFormBwd>(variant, nt)
+                                  : fl::pick_grouped<DT, fl::kFormGrad>(variant, nt);
 }
 
-fl::grouped_launcher pick_grouped(int dtype, int form, int variant) {
-    return dtype == FL_F32   ? pick_grouped_dt<FL_F32>(form, variant)
-           : dtype == FL_F16 ? pick_grouped_dt<FL_F16>(form, variant)
-                             : pick_grouped_dt<FL_BF16>(form, variant);
+fl::grouped_launcher pick_grouped(int dtype, int form, int variant, bool nt) {
+    return dtype == FL_F32   ? pick_grouped_dt<FL_F32>(form, variant, nt)
+           : dtype == FL_F16 ? pick_grouped_dt<FL_F16>(form, variant, nt)
+                             : pick_grouped_dt<FL_BF16>(form, variant, nt);
 }
 
 template <int FORM>
@@ -370,7 +370,13 @@ fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void 
         if (s != FL_OK) return s;
     }
     if (grid == 0) return FL_OK;
-    pick_grouped(dtype, form, p.variant)(a, act, grid < slots ? grid : slots, st);
+    // Weights that are read once, by runs of one low tile each, stream past the
+    // L2: 64 experts of 2048x1408, 192 rows 58 and 66 us; fp32, 8 experts of
+    // 4096x4096, 16 rows 91 and 99.  Runs of several tiles read them again, from
+    // the L2: 2 experts of 4096x1024, 1000 rows 31 us past it, 22 through it; one
+    // of 4096x4096, 300 rows 54 and 34.
+    const bool nt = t.bm <= 64 && a.S <= (int64_t)t.bm * (a.E < a.S ? a.E : a.S);
+    pick_grouped(dtype, form, p.variant, nt)(a, act, grid < slots ? grid : slots, st);
     if (a.parts > 1) {
         const fl_status s = check_launch(what);
         if (s != FL_OK) return s;
