@@ -33,7 +33,7 @@ struct GroupedArgs {
     int tiles_n;
     int group;               // row tiles per band of the tile order
     int spread;              // nonzero: each XCD takes its share of every expert's tiles
-    int stream;              // nonzero: rows of the outputs (and of Y, X) start on 128-byte lines
+    int stream;              // nonzero: rows of the outputs in the dtype (and of Y, X) start on 128-byte lines
     int parts;               // K is summed in 4, 8 or 16 parts by different workgroups (1: whole)
     float *part;             // parts > 1: fp32 sums, (parts, S, N) or, gradient, (parts, E*K, N)
     int max_tiles;           // limit on the tiles found from the offsets

@@ -501,7 +501,8 @@ struct GroupedTile {
                 store_elem<ES>((typename RawBits<ES>::T)(w[e * ES / 4] >> (8 * (e * ES & 3))), r, at(off, e * ES, e < valid));
         }
     }
-    // the fp32 values themselves (16-bit types: two stores)
+    // the fp32 values themselves (16-bit types: two stores, halves of a line), which
+    // keep to the L2 (fp32 gradients past it: 1135 and 1138 us, 37.1 and 37.6, 43.1 both)
     __device__ __forceinline__ static void store_f32(const float (&v)[VEC], __amdgpu_buffer_rsrc_t r, uint32_t off,
                                                      int valid) {
 #pragma unroll

@@ -349,9 +349,7 @@ fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void 
     // but the work is even whatever the runs' lengths: 1780 against 1820 us
     // where an expert has 470 tiles, 233 against 210 us where it has 22.
     a.spread = (int64_t)a.S / a.E / t.bm * a.tiles_n >= 128;
-    // (fp32 gradients of 16-bit operands are stored in two halves of a line)
-    const bool halves = a.dw_f32 && dtype != FL_F32;
-    a.stream = !halves && (size_t)a.N * elem_size(dtype) % 128 == 0 && aligned(a.out, 128) && aligned(a.out2, 128);
+    a.stream = (size_t)a.N * elem_size(dtype) % 128 == 0 && aligned(a.out, 128) && aligned(a.out2, 128);
     a.parts = workspace ? p.parts : 1;
     a.part = static_cast<float *>(workspace);
     const int64_t tiles_m = form == fl::kFormGrad ? a.E * (((int64_t)a.K + t.bm - 1) / t.bm) : most_row_tiles(a.S, a.E, t.bm);
