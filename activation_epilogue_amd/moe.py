@@ -135,16 +135,27 @@ def _code(dtype):
     return _dtype_code(dtype) if code is None else code
 
 
-def _route_options(score, groups, top_groups, group_top, renorm, scale):
-    # plain values: a cache would keep a tensor's first value by its identity
-    return _route_options_of(score, int(groups), int(top_groups), int(group_top), bool(renorm), float(scale))
+_options = {}
 
 
-@functools.lru_cache(maxsize=64)
-def _route_options_of(score, groups, top_groups, group_top, renorm, scale):
+def _route_options(*how):
+    """The RouteOptions of (score, groups, top_groups, group_top, renorm,
+    scale), by reference.  Kept for plain values only: a tensor among them would
+    be found again by its identity, whatever it holds by then."""
+    opt = _options.get(how)
+    if opt is None:
+        opt = _new_route_options(*how)
+        if all(type(v) in (str, int, float, bool) for v in how):
+            if len(_options) >= 64:
+                _options.clear()
+            _options[how] = opt
+    return opt
+
+
+def _new_route_options(score, groups, top_groups, group_top, renorm, scale):
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
-    opt = RouteOptions(SCORES[score], groups, top_groups, group_top, 0 if renorm else 1, scale)
+    opt = RouteOptions(SCORES[score], int(groups), int(top_groups), int(group_top), 0 if renorm else 1, float(scale))
     if opt.scale == 0.0:  # (the library's default)
         raise ValueError(f"scale must not be 0 in 32 bits, got {scale}")
     return ctypes.byref(opt)
