@@ -217,18 +217,21 @@ __global__ void __launch_bounds__(256) grouped_join_kernel(GroupedArgs a, int ac
     }
 }
 
-// The tiles of grouped_dma_kernel (fl_grouped_dma.hpp).  time: of a round (one
-// workgroup in every slot, 256 CUs x per_cu), in units of the widest tile's at
-// large sizes: 8192x2 rows of 8 experts, K 4096, N 14336 run at 1030, 950, 810,
-// 525 and 370 TFLOP/s (256x128 is set 5% above its time there, which chose right
-// at the sizes between); fp32, 4096x2 rows of 8 experts, K 2048, N 4096, at 130
-// and 100, but 100x2 rows of 6 experts, K 768, N 1000 in 20 and 14 us.  128x128
-// fp32 tiles: 114 to 134 TFLOP/s, and half as much where there are few.
+// The tiles of grouped_dma_kernel (fl_grouped_dma.hpp) and the figures of the model
+// that chooses among them (plan_grouped), fitted to measured choices.  At 45 sizes
+// from 2 rows to a training step, forward and backward, the chosen tile is within
+// 2% of the best one 67 times of 90, within 15% 88 times, and at worst 32% behind
+// (300 rows of one 4096x4096 expert).  time: of a round (one workgroup in every
+// slot, 256 CUs x per_cu), in units of the widest tile's.  For scale, 16384 rows of
+// 8 experts, K 4096, N 14336, forward: 1554, 1922, 1942, 2322 and 7310 us; fp32, 8192
+// rows of 8 experts, K 2048, N 4096: 1052 us (131 TFLOP/s) and 1109, but 200 rows of
+// 6 experts, K 768, N 1000: 18.9 and 13.4.  128x128 fp32 tiles: 114 to 134 TFLOP/s,
+// and half as much where there are few.
 struct GroupedTileShape {
     int bm, bn, per_cu;
     float time;
     float stage;   // us of one stage where a CU has one workgroup
-    float rate;    // TB/s of weights (8 experts of 4096x14336, few rows)
+    float rate;    // TB/s of weights (few rows of 8 experts of 4096x14336: 0.94 GB, more than the last-level cache)
     bool grad;     // compiled for the gradient too
 };
 enum GroupedVariant {

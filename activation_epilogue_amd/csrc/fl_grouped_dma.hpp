@@ -28,11 +28,14 @@
 //     whole 128-byte lines per instruction.
 //
 // Measured (bf16, 8192x2 rows of 8 experts, K 4096, N 14336): forward with the
-// pre-activation 1120, backward 1160, weight gradient 1170 TFLOP/s, bound by the
-// matrix cores at the clock that power leaves (a dense library product of that
-// size: 1140 to 1310); 32 tokens through 64 experts of 2048x1408: 6.5 TB/s of
-// weights, bound by memory; 4096 tokens through them: 715 TFLOP/s, bound by how
-// runs of 384 rows fill tiles and rounds (4.1 rounds of work take 6).
+// pre-activation 1120 to 1180, backward 1170, weight gradient 1160 to 1175
+// TFLOP/s (a dense library product of that size: 1370, 1570 with its right operand
+// K-contiguous).  No one limit is reached: the matrix cores are busy 57 to 61% of
+// the cycles, the waves wait 35 to 38% of theirs, and 6.7 GB a product (3.7 the
+// gradient) come past the L2s, 4.1 TB/s.  32 tokens through 64 experts of
+// 2048x1408, of which they meet 52: 5.5 TB/s of weights, bound by reading them;
+// 4096 tokens through all: 730 TFLOP/s, bound by how runs of 384 rows fill tiles
+// and rounds (4.1 rounds of work take 6).
 #pragma once
 
 #include "fl_dma16.hpp"

@@ -263,9 +263,9 @@ void join(int dtype, int form, const fl::GroupedArgs &a, int act, hipStream_t st
 // inside a tile, so S rows in R runs make about S/bm + R/2 row tiles (at least
 // R); rounds beyond the first end ragged, half a round on average; the time is
 // at least that of the weights.  Wide low tiles stream weights best where they
-// fill the chip and runs have one of them (8 experts of 4096x14336, 32 rows
-// each: 162 us, 202 with 64x128, 231 with 32x128; 64 experts of 2048x1408, 6 rows
-// each: 67 us, 57 with 32x128).
+// fill the chip and runs have one of them (8 experts of 4096x14336, 256 rows: 160
+// us, 207 with 32x128; but 64 experts of 2048x1408, 384 rows: 67 us, 59 with
+// 32x128).
 //
 // Where the chosen tiles leave most of the chip idle and the sum is long, it is
 // cut into 4, 8 or 16 parts for more workgroups, whose fp32 sums another launch
@@ -302,7 +302,7 @@ GroupedPlan plan_grouped(int dtype, int form, int64_t S, int64_t N, int64_t K, i
             if (x <= 0.5 && t.per_cu == 2) time *= 0.75;  // workgroups with a CU to themselves
             // tiles that are mostly empty skip their empty half
             if (t.bm >= 128) time *= S <= E * t.bm / 4 ? 0.7 : S <= E * t.bm / 2 ? 0.85 : 1.0;
-            // the weights: low tiles read them once each, high ones once for a run
+            // the weights: at most once for a low tile, once for a run of high ones
             const double reads = (t.bm <= 64 ? m : (double)(E < S ? E : S)) * n;
             const double memory = reads * t.bn * 128 / (t.rate * 1e6) / 1.9;  // of a round's 1.9 us a stage
             time = time > memory ? time : memory;
@@ -347,7 +347,8 @@ fl_status launch_grouped(fl::GroupedArgs &a, int form, int act, int dtype, void 
     a.group = form == fl::kFormGrad ? 4 : 8;
     // Spread over the XCDs, an expert's tiles load its weights into every L2
     // but the work is even whatever the runs' lengths: 1780 against 1820 us
-    // where an expert has 470 tiles, 233 against 210 us where it has 22.
+    // where an expert has 470 tiles, 233 against 210 us where it has 22 (the
+    // border lies somewhere between).
     a.spread = (int64_t)a.S / a.E / t.bm * a.tiles_n >= 128;
     a.stream = (size_t)a.N * elem_size(dtype) % 128 == 0 && aligned(a.out, 128) && aligned(a.out2, 128);
     a.parts = workspace ? p.parts : 1;

@@ -114,8 +114,8 @@ fl_status fl_moe_combine(const void *rows, const int32_t *row_of_slot, const flo
  * dout[t,:] (each rounded once; rows no slot points at are left alone) and
  * dweights[t,j] = sum_h dout[t,h] * rows[row_of_slot[t,j],h] in fp32 (0 for a
  * slot without a row).  Every row may belong to one slot at most.  drows or
- * dweights may be NULL (not both); rows is only read for dweights; weights
- * NULL: all 1.  drows may equal rows. */
+ * dweights may be NULL (not both, unless T*k, S or H is 0); rows is only read
+ * for dweights; weights NULL: all 1.  drows may equal rows. */
 fl_status fl_moe_combine_bwd(const void *dout, const void *rows, const int32_t *row_of_slot, const float *weights,
                              void *drows, float *dweights, int64_t T, int64_t k, int64_t S, int64_t H, fl_dtype dtype,
                              void *stream);
