@@ -28,6 +28,9 @@ Routed experts (C ABI in ``include/fused_moe.h``, binding in ``moe.py``):
   moe_plan                                # the choices sorted by expert
   moe_gather, moe_combine, moe_combine_bwd  # rows into expert order and back
   grouped_linear, grouped_linear_bwd, grouped_weight_grad  # the fused linear layer of every expert
+
+Layer norm (C ABI in ``include/fused_norm.h``, binding in ``norm.py``):
+  layer_norm, layer_norm_bwd              # the norm of every row and its gradients
 """
 from __future__ import annotations
 
@@ -423,16 +426,21 @@ def version():
     return load_library().fl_version()
 
 
-# the routed-experts operators need torch at import; loaded on first use, so
-# that importing the package stays as light as it was
-_MOE_NAMES = ("Plan", "moe_route", "moe_route_bwd", "moe_plan", "moe_plan_workspace_bytes", "moe_gather", "moe_combine",
-              "moe_combine_bwd", "grouped_linear", "grouped_linear_bwd", "grouped_weight_grad",
-              "grouped_workspace_bytes", "grouped_grad_workspace_bytes")
+# the operators in modules of their own need torch at import; loaded on first
+# use, so that importing the package stays as light as it was
+_MODULES = {
+    "moe": ("Plan", "moe_route", "moe_route_bwd", "moe_plan", "moe_plan_workspace_bytes", "moe_gather", "moe_combine",
+            "moe_combine_bwd", "grouped_linear", "grouped_linear_bwd", "grouped_weight_grad",
+            "grouped_workspace_bytes", "grouped_grad_workspace_bytes"),
+    "norm": ("layer_norm", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes"),
+}
 
 
 def __getattr__(name):
-    if name in _MOE_NAMES:
-        from . import moe
-        globals().update({n: getattr(moe, n) for n in _MOE_NAMES})
-        return globals()[name]
+    for module, names in _MODULES.items():
+        if name in names:
+            import importlib
+            m = importlib.import_module(f"{__name__}.{module}")
+            globals().update({n: getattr(m, n) for n in names})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

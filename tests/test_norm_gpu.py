@@ -1,0 +1,273 @@
+"""Layer norm and its gradients on the GPU against the 64-bit plain forms."""
+import pytest
+import torch
+
+import activation_epilogue_amd as fl
+from activation_epilogue_amd import norm
+from gpu_util import say
+from norm_util import DT, backward64, forward64, inside
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(M, H, dtype, seed, offset=0.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, H, generator=g) * torch.exp(0.5 * torch.randn(M, 1, generator=g)) + offset
+    return (x.to(dtype), (1 + 0.3 * torch.randn(H, generator=g)).to(dtype), (0.3 * torch.randn(H, generator=g)).to(dtype),
+            torch.randn(M, H, generator=g).to(dtype), torch.randn(M, H, generator=g).to(dtype))
+
+
+def guarded(*shape, dtype):
+    """(a tensor, the buffer around it): NaN in front and behind, odd to 16 bytes."""
+    n = 1
+    for s in shape:
+        n *= s
+    buf = torch.full((n + 128,), float("nan"), dtype=dtype, device="cuda")
+    return buf[33:33 + n].view(*shape), buf
+
+
+def untouched(buf, n):
+    assert torch.isnan(buf[:33]).all() and torch.isnan(buf[33 + n:]).all()
+
+
+def check(M, H, dtype, seed, affine=True, residual=True, offset=0.0, eps=1e-5):
+    dt = DT[dtype]
+    x, w, b, dy, res = rows(M, H, dt, seed, offset)
+    w, b = (w, b) if affine else (None, None)
+    res = res if residual else None
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    say("layer norm", M, H, dtype, affine, residual)
+    out, buf = guarded(M, H, dtype=dt)
+    y, mean, rstd = fl.layer_norm(dev(x), dev(w), dev(b), eps=eps, out=out, stats=True)
+    assert y is out
+    untouched(buf, M * H)
+    y64, mean64, rstd64, (e_y, e_mean, e_rstd) = forward64(x, w, b, eps)
+    inside(y, y64, e_y)
+    inside(mean, mean64, e_mean)
+    inside(rstd, rstd64, e_rstd)
+    assert torch.equal(fl.layer_norm(dev(x), dev(w), dev(b), eps=eps), y)
+    say("its gradients")
+    out, buf = guarded(M, H, dtype=dt)
+    dx, dw, db = fl.layer_norm_bwd(dev(dy), dev(x), mean, rstd, dev(w), R=dev(res), dX=out)
+    untouched(buf, M * H)
+    dx64, dw64, db64, (e_dx, e_w, e_b) = backward64(dy, x, mean.cpu(), rstd.cpu(), w, res)
+    inside(dx, dx64, e_dx)
+    inside(dw, dw64, e_w)
+    inside(db, db64, e_b)
+    only, none, _ = fl.layer_norm_bwd(dev(dy), dev(x), mean, rstd, dev(w), R=dev(res), dweight=False, dbias=None)
+    assert none is None and torch.equal(only, dx)
+    _, one, none = fl.layer_norm_bwd(dev(dy), dev(x), mean, rstd, dev(w), R=dev(res), dbias=False)
+    assert none is None and torch.equal(one, dw)
+
+
+# every team and its neighbours, whole pieces and ragged ones, one row and more than the blocks take at once
+WIDTHS = (1, 2, 7, 8, 9, 31, 64, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1000, 1024, 1537, 2048, 2049, 4095, 4096,
+          4097, 8191, 8192, 8193, 16383, 16384, 16385, 32768, 32769, 40001)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("H", WIDTHS)
+def test_widths(H, dtype):
+    for M in (1, 5) + ((67,) if H < 20000 else ()):
+        check(M, H, dtype, seed=H + M)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,H", [(2, 512), (31, 512), (33, 64), (1025, 96), (2049, 260), (5000, 130), (300, 4096),
+                                 (4097, 1537), (9001, 64), (700, 8192)])
+def test_rows(M, H, dtype):
+    check(M, H, dtype, seed=M)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [100, 4096, 20000, 40001])
+def test_without_weight_or_residual(H, dtype):
+    check(9, H, dtype, seed=1, affine=False, residual=False)
+    check(9, H, dtype, seed=2, affine=True, residual=False)
+    check(9, H, dtype, seed=3, affine=False, residual=True)
+
+
+@pytest.mark.parametrize("H", [64, 1000, 4096, 40001])
+def test_a_mean_far_from_zero(H):
+    """Squares of x would lose all of a deviation of 1 at a mean of 4000."""
+    check(33, H, "f32", seed=H, offset=4000.0)
+
+
+def test_one_of_weight_and_bias():
+    x, w, b, _, _ = rows(12, 300, torch.float32, 5)
+    for ww, bb in ((w, None), (None, b)):
+        y = fl.layer_norm(x.cuda(), None if ww is None else ww.cuda(), None if bb is None else bb.cuda())
+        y64, _, _, (e_y, _, _) = forward64(x, ww, bb, 1e-5)
+        inside(y, y64, e_y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("H", [40, 1000, 4096, 9000, 40001])
+def test_values_that_are_not_finite_stay_in_their_row(H, dtype):
+    x, w, b, dy, _ = rows(8, H, DT[dtype], 11)
+    y0 = fl.layer_norm(x.cuda(), w.cuda(), b.cuda())
+    x[2, H // 2], x[5, 0], x[6, H - 1] = float("nan"), float("inf"), float("-inf")
+    say("not finite", H, dtype)
+    y, mean, rstd = fl.layer_norm(x.cuda(), w.cuda(), b.cuda(), stats=True)
+    bad = [2, 5, 6]
+    good = [r for r in range(8) if r not in bad]
+    assert torch.isnan(y[bad]).all() and torch.equal(y[good], y0[good])
+    dx, _, db = fl.layer_norm_bwd(dy.cuda(), x.cuda(), mean, rstd, w.cuda())
+    assert torch.isnan(dx[bad]).all() and torch.isfinite(dx[good]).all() and torch.isfinite(db).all()
+
+
+def test_rows_of_equal_values():
+    """Nothing is left of them: the bias; with eps 0 it is 0 * infinity."""
+    x, b = torch.full((3, 777), 2.5, device="cuda"), torch.randn(777, device="cuda")
+    assert torch.equal(fl.layer_norm(x, None, b), b.expand(3, 777))
+    y, mean, rstd = fl.layer_norm(x, eps=0.0, stats=True)
+    assert torch.isnan(y).all() and torch.isinf(rstd).all() and (mean == 2.5).all()
+
+
+@pytest.mark.parametrize("M,H", [(0, 100), (3, 0), (0, 0)])
+def test_nothing(M, H):
+    x = torch.zeros(M, H, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(H, device="cuda", dtype=torch.bfloat16)
+    y, mean, rstd = fl.layer_norm(x, w, w, stats=True)
+    assert y.shape == (M, H)
+    mean.zero_(), rstd.zero_()
+    dw = torch.full((H,), 3.0, device="cuda")
+    dx, dw, db = fl.layer_norm_bwd(x, x, mean, rstd, w, dweight=dw)
+    assert dx.shape == (M, H) and (dw == 0).all() and (db == 0).all()
+
+
+@pytest.mark.parametrize("H", [65, 4096, 40001])
+def test_in_place(H):
+    x, w, b, dy, res = (t.cuda() for t in rows(20, H, torch.bfloat16, 3))
+    y, mean, rstd = fl.layer_norm(x, w, b, stats=True)
+    z = x.clone()
+    assert fl.layer_norm(z, w, b, out=z) is z and torch.equal(z, y)
+    want = fl.layer_norm_bwd(dy, x, mean, rstd, w, R=res)
+    for name in ("dout", "X", "R"):
+        args = {"dout": dy.clone(), "X": x.clone(), "R": res.clone()}
+        got = fl.layer_norm_bwd(args["dout"], args["X"], mean, rstd, w, R=args["R"], dX=args[name])
+        assert got[0] is args[name] and all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_gradients_against_differences():
+    """The loss sum(dy * y): its slope along each direction, by differences in
+    64 bits of the formula, is what the gradients say."""
+    M, H, eps = 6, 50, 1e-3
+    x, w, b, dy, _ = rows(M, H, torch.float32, 17)
+    y, mean, rstd = fl.layer_norm(x.cuda(), w.cuda(), b.cuda(), eps=eps, stats=True)
+    dx, dw, db = (t.cpu().double() for t in fl.layer_norm_bwd(dy.cuda(), x.cuda(), mean, rstd, w.cuda()))
+
+    def loss(x, w, b):
+        d = x - x.mean(1, keepdim=True)
+        return float((dy.double() * (d * ((d * d).mean(1, keepdim=True) + eps) ** -0.5 * w + b)).sum())
+    x, w, b = x.double(), w.double(), b.double()
+    g = torch.Generator().manual_seed(1)
+    h = 1e-4  # a central difference is off by h^2 of the third derivative, and 2^-52 of the loss over h
+    for at, grad in ((0, dx), (1, dw), (2, db)):
+        for _ in range(5):
+            v = torch.randn(grad.shape, generator=g, dtype=torch.float64)
+            up, down = [x, w, b], [x, w, b]
+            up[at], down[at] = up[at] + h * v, down[at] - h * v
+            slope = (loss(*up) - loss(*down)) / (2 * h)
+            # fp32 gradients: 300 terms of size |grad * v|, each good to 100 roundings
+            room = 100 * 2.0 ** -24 * float((grad * v).abs().sum()) + 1e-4
+            assert abs(slope - float((grad * v).sum())) <= room
+
+
+def test_the_same_bits_again_and_on_another_stream():
+    x, w, b, dy, res = (t.cuda() for t in rows(3001, 1537, torch.bfloat16, 9))
+    y, mean, rstd = fl.layer_norm(x, w, b, stats=True)
+    first = fl.layer_norm_bwd(dy, x, mean, rstd, w, R=res)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    again = fl.layer_norm(x, w, b, stats=True, stream=s) + fl.layer_norm_bwd(dy, x, mean, rstd, w, R=res, stream=s)
+    s.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip((y, mean, rstd, *first), again))
+
+
+def test_workspace():
+    M, H = 3001, 1537
+    x, w, b, dy, _ = (t.cuda() for t in rows(M, H, torch.float16, 9))
+    _, mean, rstd = fl.layer_norm(x, w, b, stats=True)
+    need = fl.layer_norm_bwd_workspace_bytes(M, H, torch.float16)
+    assert need > 0
+    buf = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    got = fl.layer_norm_bwd(dy, x, mean, rstd, w, workspace=buf[:need])
+    assert (buf[need:] == 255).all()
+    assert all(torch.equal(p, q) for p, q in zip(got, fl.layer_norm_bwd(dy, x, mean, rstd, w)))
+    with pytest.raises(fl.FusedLinearError, match="needed"):
+        fl.layer_norm_bwd(dy, x, mean, rstd, w, workspace=buf[:need - 1])
+
+
+def test_captured_and_replayed():
+    """A block's norm forward and backward in a graph, with new inputs and eager
+    work between the replays."""
+    M, H = 515, 2050
+    x, w, b, dy, res = (t.cuda() for t in rows(M, H, torch.bfloat16, 21))
+    ws = torch.empty(norm.layer_norm_bwd_workspace_bytes(M, H, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    kept = {}
+
+    def work():
+        kept["f"] = fl.layer_norm(x, w, b, stats=True)
+        kept["b"] = fl.layer_norm_bwd(dy, x, kept["f"][1], kept["f"][2], w, R=res, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for seed in range(3):
+        for t, new in zip((x, w, b, dy, res), rows(M, H, torch.bfloat16, 30 + seed)):
+            t.copy_(new)
+        f = fl.layer_norm(x, w, b, stats=True)
+        want = (*f, *fl.layer_norm_bwd(dy, x, f[1], f[2], w, R=res))
+        for t in (*kept["f"], *kept["b"]):
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip((*kept["f"], *kept["b"]), want))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 bytes of rows, the last of them as the same rows alone."""
+    M, H = 600_011, 4096
+    x = torch.empty(M, H, dtype=torch.bfloat16, device="cuda")
+    x[:1000].normal_()
+    x[1000:-1000] = 1.0
+    x[-1000:].normal_()
+    say("layer norm past 2^32 bytes")
+    y, mean, rstd = fl.layer_norm(x, stats=True)
+    tail = fl.layer_norm(x[-1000:], stats=True)
+    assert torch.equal(y[-1000:], tail[0]) and torch.equal(mean[-1000:], tail[1])
+    dy = y.clone()
+    dx, _, db = fl.layer_norm_bwd(dy, x, mean, rstd)
+    assert torch.equal(dx[-1000:], fl.layer_norm_bwd(dy[-1000:], x[-1000:], mean[-1000:], rstd[-1000:])[0])
+    assert torch.isfinite(db).all()
+
+
+def test_refusals():
+    x = torch.zeros(4, 8, device="cuda")
+    one = torch.zeros(4, device="cuda")
+    with pytest.raises(ValueError, match="matrix"):
+        fl.layer_norm(one)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        fl.layer_norm(x.double())
+    with pytest.raises(ValueError, match="contiguous"):
+        fl.layer_norm(x.t())
+    with pytest.raises(TypeError, match="weight has dtype"):
+        fl.layer_norm(x, torch.zeros(8, device="cuda", dtype=torch.float16))
+    with pytest.raises(ValueError, match="bias has shape"):
+        fl.layer_norm(x, None, torch.zeros(9, device="cuda"))
+    with pytest.raises(ValueError, match="device"):
+        fl.layer_norm(torch.zeros(4, 8))
+    with pytest.raises(ValueError, match="stats"):
+        fl.layer_norm(x, mean=one)
+    with pytest.raises(fl.FusedLinearError, match="eps"):
+        fl.layer_norm(x, eps=-1.0)
+    with pytest.raises(ValueError, match="mean has shape"):
+        fl.layer_norm_bwd(x, x, one[:3], one)
+    with pytest.raises(fl.FusedLinearError, match="mean is NULL"):
+        fl.layer_norm_bwd(x, x, None, one)
