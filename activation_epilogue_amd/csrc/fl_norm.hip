@@ -9,9 +9,7 @@
 
 namespace {
 
-// Blocks of the backward kernel: each leaves one row of partial sums (8 H
-// bytes), so no more than fill the chip.
-constexpr int kBwdBlocks = 256;
+constexpr int kBwdBlocks = 512;  // of 512 threads, two of which a CU holds
 constexpr int64_t kGridMax = 1 << 20;
 
 fl_status check_norm(int64_t M, int64_t H, int dtype) {
@@ -30,6 +28,10 @@ void launch_fwd(const fl::NormArgs &a, hipStream_t st) {
                        dim3(threads), 0, st, a);
 }
 
+// The smallest team whose lanes hold the row in 16 to 64 bytes each, 128 where it
+// takes many: rows of 1024 bf16 take 11.6 us with 64 lanes and 21.4 with 256
+// (16384 rows), of 2048 21.9 and 22.9, of 4096 40.6 and 38.6; 256 columns 11.6 with 16
+// lanes, 19.5 with 64 (65536 rows).
 template <int DT>
 void launch_fwd_dt(const fl::NormArgs &a, hipStream_t st) {
     const int64_t p = pieces_of(a.H, DT);
@@ -44,7 +46,7 @@ void launch_fwd_dt(const fl::NormArgs &a, hipStream_t st) {
     else if (p <= 256)
         launch_fwd<DT, 64, 4>(a, st);
     else if (p <= 512)
-        launch_fwd<DT, 64, 8>(a, st);
+        launch_fwd<DT, 256, 2>(a, st);
     else if (p <= 1024)
         launch_fwd<DT, 256, 4>(a, st);
     else if (p <= 2048)
@@ -56,7 +58,14 @@ void launch_fwd_dt(const fl::NormArgs &a, hipStream_t st) {
                            dim3(1024), 0, st, a);
 }
 
-// The rows of partial sums that M rows of H values leave (1: none are kept).
+// The team of the backward kernel, and its blocks where they keep sums: each
+// leaves a row of partial sums (8 H bytes), so no more of them than are resident
+// at once (16384x4096 bf16: 103 us with 512, 129 with 256, 111 with 1024; teams of
+// 1024 lanes 119 us with 256 at 8192x8192, 130 with 512).  Few rows go one to a
+// team all the same: 512x4096 14 us, 17 with four to a team.  The sums of a lane
+// take two registers an element, so teams are larger than the forward's: 2048
+// columns 55 us with 256 lanes, 66 with 64; 8192 columns 119 us with 1024 lanes, 129
+// with 256; but 512 columns 29 us with 64 lanes, 75 with 256.
 struct BwdShape {
     int team, nv, blocks;  // team 0: the long kernels
 };
@@ -66,17 +75,17 @@ BwdShape bwd_shape(int64_t M, int64_t H, int dtype) {
     BwdShape b{};
     if (p <= 32)
         b = {16, p <= 16 ? 1 : 2, 0};
+    else if (p <= 128)
+        b = {64, p <= 64 ? 1 : 2, 0};
     else if (p <= 512)
-        b = {64, p <= 64 ? 1 : p <= 128 ? 2 : p <= 256 ? 4 : 8, 0};
-    else if (p <= 1024)
-        b = {256, 4, 0};
+        b = {256, p <= 256 ? 1 : 2, 0};
     else if (p <= 2048)
-        b = {1024, 2, 0};
+        b = {1024, p <= 1024 ? 1 : 2, 0};
     else if (p <= 4096 && dtype == FL_F32)
         b = {1024, 4, 0};
-    const int teams = b.team == 0 ? 1 : b.team > 512 ? 1 : 512 / b.team;
-    const int64_t blocks = (M + teams - 1) / teams;
-    b.blocks = (int)(blocks < kBwdBlocks ? (blocks > 1 ? blocks : 1) : kBwdBlocks);
+    const int64_t rows = b.team && b.team < 512 ? 512 / b.team : 1;  // of a block at once
+    const int64_t blocks = (M + rows - 1) / rows, most = b.team == 1024 ? kBwdBlocks / 2 : kBwdBlocks;
+    b.blocks = (int)(blocks < most ? (blocks > 1 ? blocks : 1) : most);
     return b;
 }
 
@@ -113,9 +122,9 @@ void launch_bwd_dt(const fl::NormArgs &a, const BwdShape &b, bool sums, float *c
     FL_BWD(16, 2);
     FL_BWD(64, 1);
     FL_BWD(64, 2);
-    FL_BWD(64, 4);
-    FL_BWD(64, 8);
-    FL_BWD(256, 4);
+    FL_BWD(256, 1);
+    FL_BWD(256, 2);
+    FL_BWD(1024, 1);
     FL_BWD(1024, 2);
     else if constexpr (DT == FL_F32) launch_bwd<DT, 1024, 4>(a, b.blocks, sums, st);
 #undef FL_BWD
@@ -225,7 +234,7 @@ fl_status fl_layer_norm_bwd(const void *dY, const void *X, const void *weight, c
     else
         launch_bwd_dt<FL_BF16>(a, b, sums, c, st);
     if (join)
-        hipLaunchKernelGGL(fl::column_join_kernel, dim3((unsigned)((H + 63) / 64), 2), dim3(1024), 0, st, a, b.blocks);
+        hipLaunchKernelGGL(fl::column_join_kernel, dim3((unsigned)((H + 31) / 32), 2), dim3(1024), 0, st, a, b.blocks);
     return check_launch("fl_layer_norm_bwd");
 }
 

@@ -15,6 +15,12 @@
 // rows; a block adds its teams' through the LDS and writes one row of partial
 // sums, which column_join_kernel adds in a fixed order: no atomics.
 //
+// Measured, 16384x4096 bf16: forward 38.6 us (7.0 TB/s of the 268 MB, some of
+// which the last-level cache serves), backward with a residual 103 us (5.2 TB/s of
+// 537 MB; 89 us, 6.0 TB/s, without the weight's and bias's sums: their 16 MB of
+// partial sums written and read and one more launch are the rest).  Outputs that
+// pass the L2 by: forward 40.6 -> 42.6 us without.
+//
 // Pieces are read and written 16 bytes wide whatever the rows' alignment (the
 // hardware takes any that suits the elements); what is left behind the last
 // whole piece goes an element to a lane.
@@ -535,23 +541,25 @@ __global__ void __launch_bounds__(256) layer_norm_bwd_columns_kernel(NormArgs a,
     }
 }
 
-// The sum of `rows` rows of partial sums (rows, 2, H): 64 columns to a block, 16
-// runs of rows side by side.  blockIdx.y: 0 the weight's, 1 the bias's.
+// The sum of `rows` rows of partial sums (rows, 2, H): 32 columns to a block, 32
+// runs of rows side by side, whose loads go out eight at a time.  blockIdx.y: 0
+// the weight's, 1 the bias's.
 __global__ void __launch_bounds__(1024) column_join_kernel(NormArgs a, int rows) {
-    __shared__ float sums[16][64];
+    __shared__ float sums[32][32];
     float *out = blockIdx.y ? a.dbias : a.dweight;
     if (!out) return;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-    const int64_t i = (int64_t)blockIdx.x * 64 + x;
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * 32 + x;
     float s = 0.0f;
     if (i < a.H) {
-#pragma unroll 4
-        for (int r = y; r < rows; r += 16) s += a.part[((int64_t)r * 2 + blockIdx.y) * a.H + i];
+#pragma unroll 8
+        for (int r = y; r < rows; r += 32) s += a.part[((int64_t)r * 2 + blockIdx.y) * a.H + i];
     }
     sums[y][x] = s;
     __syncthreads();
     if (y || i >= a.H) return;
-    for (int k = 1; k < 16; ++k) s += sums[k][x];
+#pragma unroll
+    for (int k = 1; k < 32; ++k) s += sums[k][x];
     out[i] = s;
 }
 
