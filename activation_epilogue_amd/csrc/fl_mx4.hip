@@ -1,0 +1,200 @@
+// fl_mx4.hip -- host side of the C ABI declared in include/fused_mx4.h:
+// argument validation, the choice of kernels and their launches on the
+// caller's stream.  Device code is in fl_mx4.hpp and fl_mx4_linear.hpp.
+#include "fl_check.hpp"
+#include "fl_mx4_linear.hpp"
+#include "fused_mx4.h"
+
+namespace {
+
+int64_t blocks_of(int64_t K) { return (K + 31) / 32; }
+
+template <int DT>
+void launch_quantize(const fl::Mx4Args &a, bool transposed, hipStream_t st) {
+    if (transposed) {
+        const int64_t per_block = 32 * (DT == FL_F32 ? 4 : 8);
+        hipLaunchKernelGGL((fl::quantize_mx4_transposed_kernel<DT>),
+                           dim3((unsigned)((a.rows + per_block - 1) / per_block), (unsigned)((a.blocks + 7) / 8)),
+                           dim3(256), 0, st, a);
+    } else {
+        const int64_t units = a.rows * a.blocks * 4, per_block = 256 * fl::kMx4Units;
+        hipLaunchKernelGGL((fl::quantize_mx4_kernel<DT>), dim3((unsigned)((units + per_block - 1) / per_block)),
+                           dim3(256), 0, st, a);
+    }
+}
+
+void quantize(const fl::Mx4Args &a, bool transposed, int dtype, hipStream_t st) {
+    if (dtype == FL_F32)
+        launch_quantize<FL_F32>(a, transposed, st);
+    else if (dtype == FL_F16)
+        launch_quantize<FL_F16>(a, transposed, st);
+    else
+        launch_quantize<FL_BF16>(a, transposed, st);
+}
+
+// rows x K values, their codes and scales.
+fl_status check_matrix(int64_t rows, int64_t K, int dtype) {
+    fl_status s = check_dtype(dtype);
+    if (s != FL_OK) return s;
+    if ((s = check_sizes({rows, K})) != FL_OK) return s;
+    // units of 1024 to a launch's block, blocks of 8 K blocks in its second dimension
+    if (rows && blocks_of(K) > ((int64_t)1 << 38) / rows)
+        return fail(FL_ERR_UNSUPPORTED, "more than 2^38 blocks");
+    if (blocks_of(K) > 8 * 65535) return fail(FL_ERR_UNSUPPORTED, "K (%lld) above 2^24 - 256", (long long)K);
+    return FL_OK;
+}
+
+template <int DT, int MT, int NT, int WAVES, int U>
+void launch_stream(const fl::Mx4LinearArgs &a, hipStream_t st) {
+    const dim3 grid((unsigned)(((a.N + 16 * NT - 1) / (16 * NT)) * ((a.M + 16 * MT - 1) / (16 * MT))));
+    if (a.a_raw)
+        hipLaunchKernelGGL((fl::mx4_stream_kernel<DT, MT, NT, WAVES, U, true>), grid, dim3(64 * WAVES), 0, st, a);
+    else
+        hipLaunchKernelGGL((fl::mx4_stream_kernel<DT, MT, NT, WAVES, U, false>), grid, dim3(64 * WAVES), 0, st, a);
+}
+
+template <int DT>
+void launch_linear(const fl::Mx4LinearArgs &a, hipStream_t st) {
+    launch_stream<DT, 1, 1, 4, 2>(a, st);
+}
+
+// Bytes of the workspace: A's codes, then its scales.
+size_t linear_bytes(int64_t M, int64_t N, int64_t K, bool values) {
+    (void)M, (void)N, (void)K, (void)values;
+    return 0;
+}
+
+fl_status check_linear(int64_t M, int64_t N, int64_t K, int dtype) {
+    fl_status s = check_matrix(M, K, dtype);
+    if (s != FL_OK || (s = check_matrix(N, K, dtype)) != FL_OK) return s;
+    const size_t es = elem_size(dtype);
+    if ((size_t)blocks_of(K) * 16 * 256 >= kTwoGiB || (size_t)K * es * 256 >= kTwoGiB || (size_t)N * es * 256 >= kTwoGiB)
+        return fail(FL_ERR_UNSUPPORTED, "K or N too large (256 rows must span < 2 GiB)");
+    if (((N + 15) / 16) * ((M + 15) / 16) > kMaxDim)
+        return fail(FL_ERR_UNSUPPORTED, "more than 2^31-1 tiles of 16x16 outputs");
+    return FL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+const char *fl_mx4_last_error(void) { return g_err; }
+
+fl_status fl_quantize_mx4(const void *X, uint8_t *codes, uint8_t *scales, int64_t rows, int64_t K, int32_t transposed,
+                          fl_dtype dtype, void *stream) {
+    clear_error();
+    fl_status s = check_matrix(rows, K, dtype);
+    if (s != FL_OK) return s;
+    if (transposed != 0 && transposed != 1) return fail(FL_ERR_INVALID_ARG, "transposed must be 0 or 1");
+    const size_t es = elem_size(dtype), blocks = (size_t)blocks_of(K);
+    if ((s = check_operands({{"X", X, (size_t)rows * K * es, es, false, false, nullptr},
+                             {"codes", codes, rows * blocks * 16, 16, true, false, nullptr},
+                             {"scales", scales, rows * blocks, 1, true, false, nullptr}})) != FL_OK)
+        return s;
+    if (rows == 0 || K == 0) return FL_OK;
+    fl::Mx4Args a{};
+    a.x = X;
+    a.codes = codes;
+    a.scales = scales;
+    a.rows = rows;
+    a.K = (int)K;
+    a.blocks = (int)blocks;
+    quantize(a, transposed, dtype, static_cast<hipStream_t>(stream));
+    return check_launch("fl_quantize_mx4");
+}
+
+fl_status fl_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, void *X, int64_t rows, int64_t K,
+                            fl_dtype dtype, void *stream) {
+    clear_error();
+    fl_status s = check_matrix(rows, K, dtype);
+    if (s != FL_OK) return s;
+    const size_t es = elem_size(dtype), blocks = (size_t)blocks_of(K);
+    if ((s = check_operands({{"codes", codes, rows * blocks * 16, 16, false, false, nullptr},
+                             {"scales", scales, rows * blocks, 1, false, false, nullptr},
+                             {"X", X, (size_t)rows * K * es, es, true, false, nullptr}})) != FL_OK)
+        return s;
+    if (rows == 0 || K == 0) return FL_OK;
+    fl::Mx4Args a{};
+    a.y = X;
+    a.codes = const_cast<uint8_t *>(codes);
+    a.scales = const_cast<uint8_t *>(scales);
+    a.rows = rows;
+    a.K = (int)K;
+    a.blocks = (int)blocks;
+    const int64_t units = rows * (int64_t)blocks * 4, per_block = 256 * fl::kMx4Units;
+    const dim3 grid((unsigned)((units + per_block - 1) / per_block));
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (dtype == FL_F32)
+        hipLaunchKernelGGL((fl::dequantize_mx4_kernel<FL_F32>), grid, dim3(256), 0, st, a);
+    else if (dtype == FL_F16)
+        hipLaunchKernelGGL((fl::dequantize_mx4_kernel<FL_F16>), grid, dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((fl::dequantize_mx4_kernel<FL_BF16>), grid, dim3(256), 0, st, a);
+    return check_launch("fl_dequantize_mx4");
+}
+
+fl_status fl_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t values, fl_dtype dtype, size_t *bytes) {
+    clear_error();
+    fl_status s = check_linear(M, N, K, dtype);
+    if (s != FL_OK) return s;
+    if (values != 0 && values != 1) return fail(FL_ERR_INVALID_ARG, "values must be 0 or 1");
+    if (!bytes) return fail(FL_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = linear_bytes(M, N, K, values);
+    return FL_OK;
+}
+
+fl_status fl_fused_linear_mx4(const void *A, const uint8_t *A_scales, const uint8_t *B, const uint8_t *B_scales,
+                              const void *bias, const void *Y, const void *R, void *out, int64_t M, int64_t N,
+                              int64_t K, fl_act act, fl_dtype dtype, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+    clear_error();
+    fl_status s = check_linear(M, N, K, dtype);
+    if (s != FL_OK) return s;
+    if (act < FL_ACT_NONE || act > FL_ACT_GLU) return fail(FL_ERR_INVALID_ARG, "unknown activation %d", act);
+    if (act == FL_ACT_GLU && !Y && M && N) return fail(FL_ERR_INVALID_ARG, "the gate needs Y");
+    if (act != FL_ACT_GLU && Y) return fail(FL_ERR_INVALID_ARG, "Y is only used by the gate (FL_ACT_GLU)");
+    const bool values = !A_scales;
+    const size_t need = linear_bytes(M, N, K, values);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(FL_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
+    const size_t es = elem_size(dtype), blocks = (size_t)blocks_of(K), outs = (size_t)M * N * es;
+    const bool live = M && N;  // nothing is read otherwise
+    const void *same = out == Y ? Y : R;
+    if ((s = check_operands({{"A", A, !live ? 0 : values ? (size_t)M * K * es : M * blocks * 16, values ? es : 16, false, false, nullptr},
+                             {"A_scales", A_scales, live && !values ? M * blocks : 0, 1, false, false, nullptr},
+                             {"B", B, live ? N * blocks * 16 : 0, 16, false, false, nullptr},
+                             {"B_scales", B_scales, live ? N * blocks : 0, 1, false, false, nullptr},
+                             {"bias", bias, live ? (size_t)N * es : 0, es, false, true, nullptr},
+                             {"Y", Y, outs, es, false, true, nullptr},
+                             {"R", R, outs, es, false, true, nullptr},
+                             {"out", out, outs, es, true, false, same},
+                             {"workspace", workspace, need, 16, true, true, nullptr}})) != FL_OK)
+        return s;
+    if (!live) return FL_OK;
+    fl::Mx4LinearArgs a{};
+    a.a_codes = values ? nullptr : static_cast<const uint8_t *>(A);
+    a.a_scales = A_scales;
+    a.a_raw = values ? A : nullptr;
+    a.b_codes = B;
+    a.b_scales = B_scales;
+    a.bias = bias;
+    a.Y = Y;
+    a.R = R;
+    a.out = out;
+    a.M = M;
+    a.N = N;
+    a.K = (int)K;
+    a.blocks = (int)blocks;
+    a.act = act;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (dtype == FL_F32)
+        launch_linear<FL_F32>(a, st);
+    else if (dtype == FL_F16)
+        launch_linear<FL_F16>(a, st);
+    else
+        launch_linear<FL_BF16>(a, st);
+    return check_launch("fl_fused_linear_mx4");
+}
+
+}  // extern "C"
