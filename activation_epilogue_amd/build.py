@@ -1,13 +1,14 @@
 """Build libfused_linear.so for gfx950 with hipcc, in-tree.
 
-Twenty-two translation units compiled in parallel: the host/ABI unit (with the
+Twenty-five translation units compiled in parallel: the host/ABI unit (with the
 elementwise kernels), one unit of fused GEMM kernels per dtype, one of
 quantized-output kernels per 16-bit dtype, one of FP8-input kernels per
 16-bit output dtype and one of backward-epilogue kernels per 16-bit dtype;
 and, for the routed experts, the host/ABI unit (with the router, plan and
 row-movement kernels) and one unit of the experts' products per dtype and
-form; and a unit of layer norm and one of
-microscaled 4-bit floating point.
+form; a unit of layer norm; and, for
+microscaled 4-bit floating point, the host/ABI unit (with quantising) and one
+unit of the linear layer's kernels per dtype.
 Every device compile carries -Xclang -target-feature -Xclang -packed-fp32-ops so
 that no packed fp32 instructions are generated.
 """
@@ -46,6 +47,7 @@ UNITS = [
       for form in (0, 1, 2) for dt in (0, 1, 2)),
     ("fl_norm.hip", []),
     ("fl_mx4.hip", []),
+    *(("fl_mx4_inst.hip", [f"-DFL_INST_DTYPE={dt}"]) for dt in (0, 1, 2)),
 ]
 
 

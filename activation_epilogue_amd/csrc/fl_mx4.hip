@@ -1,8 +1,9 @@
 // fl_mx4.hip -- host side of the C ABI declared in include/fused_mx4.h:
 // argument validation, the choice of kernels and their launches on the
-// caller's stream.  Device code is in fl_mx4.hpp and fl_mx4_linear.hpp.
+// caller's stream.  Device code is in fl_mx4.hpp (quantising), fl_mx4_linear.hpp
+// and fl_mx4_tile.hpp (the linear layer; its kernels are built by fl_mx4_inst.hip).
 #include "fl_check.hpp"
-#include "fl_mx4_linear.hpp"
+#include "fl_mx4_tile.hpp"
 #include "fused_mx4.h"
 
 namespace {
@@ -44,24 +45,66 @@ fl_status check_matrix(int64_t rows, int64_t K, int dtype) {
     return FL_OK;
 }
 
-template <int DT, int MT, int NT, int WAVES, int U>
-void launch_stream(const fl::Mx4LinearArgs &a, hipStream_t st) {
-    const dim3 grid((unsigned)(((a.N + 16 * NT - 1) / (16 * NT)) * ((a.M + 16 * MT - 1) / (16 * MT))));
-    if (a.a_raw)
-        hipLaunchKernelGGL((fl::mx4_stream_kernel<DT, MT, NT, WAVES, U, true>), grid, dim3(64 * WAVES), 0, st, a);
-    else
-        hipLaunchKernelGGL((fl::mx4_stream_kernel<DT, MT, NT, WAVES, U, false>), grid, dim3(64 * WAVES), 0, st, a);
+// How a linear layer runs: the streaming kernel for few rows, else tiles of a
+// size, K in parts where there are few of them.
+struct LinearPlan {
+    bool stream, quantize;  // quantize: A's values first, into the workspace
+    int variant, parts, part_stages;
+    size_t codes, scales, sums;  // bytes of the workspace, in this order
+};
+
+size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
+    LinearPlan p{};
+    const int64_t blocks = blocks_of(K);
+    p.parts = 1;
+    p.part_stages = (int)((blocks + 7) / 8);
+    if (!M || !N || !K) {
+        p.stream = true;
+        return p;
+    }
+    p.stream = M <= 64;
+    p.variant = ((M + 255) / 256) * ((N + 255) / 256) >= 200 ? fl::kMx4Tile256 : fl::kMx4Tile128;
+    p.quantize = values && !p.stream;
+    if (p.quantize) {
+        p.codes = (size_t)(M * blocks * 16);
+        p.scales = align16((size_t)(M * blocks));
+    }
+    if (p.parts > 1) p.sums = (size_t)p.parts * M * N * 4;
+    return p;
 }
+
+size_t linear_bytes(const LinearPlan &p) { return p.codes + p.scales + p.sums; }
 
 template <int DT>
-void launch_linear(const fl::Mx4LinearArgs &a, hipStream_t st) {
-    launch_stream<DT, 1, 1, 4, 2>(a, st);
-}
-
-// Bytes of the workspace: A's codes, then its scales.
-size_t linear_bytes(int64_t M, int64_t N, int64_t K, bool values) {
-    (void)M, (void)N, (void)K, (void)values;
-    return 0;
+void launch_linear(const LinearPlan &p, fl::Mx4LinearArgs l, uint8_t *ws, hipStream_t st) {
+    if (p.quantize) {
+        fl::Mx4Args q{};
+        q.x = l.a_raw;
+        q.codes = ws;
+        q.scales = ws + p.codes;
+        q.rows = l.M;
+        q.K = l.K;
+        q.blocks = l.blocks;
+        launch_quantize<DT>(q, false, st);
+        l.a_raw = nullptr;
+        l.a_codes = q.codes;
+        l.a_scales = q.scales;
+    }
+    if (p.stream) {
+        fl::launch_mx4_stream<DT>(p.variant, l, st);
+        return;
+    }
+    fl::Mx4TileArgs a{};
+    const fl::Mx4TileShape &t = fl::kMx4TileShapes[p.variant];
+    a.l = l;
+    a.part = reinterpret_cast<float *>(ws + p.codes + p.scales);
+    a.parts = p.parts;
+    a.part_stages = p.part_stages;
+    a.tiles_m = (int)((l.M + t.bm - 1) / t.bm);
+    a.tiles_n = (int)((l.N + t.bn - 1) / t.bn);
+    fl::launch_mx4_tile<DT>(p.variant, a, st);
 }
 
 fl_status check_linear(int64_t M, int64_t N, int64_t K, int dtype) {
@@ -140,7 +183,7 @@ fl_status fl_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t values
     if (s != FL_OK) return s;
     if (values != 0 && values != 1) return fail(FL_ERR_INVALID_ARG, "values must be 0 or 1");
     if (!bytes) return fail(FL_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = linear_bytes(M, N, K, values);
+    *bytes = linear_bytes(plan_linear(M, N, K, values));
     return FL_OK;
 }
 
@@ -155,7 +198,8 @@ fl_status fl_fused_linear_mx4(const void *A, const uint8_t *A_scales, const uint
     if (act == FL_ACT_GLU && !Y && M && N) return fail(FL_ERR_INVALID_ARG, "the gate needs Y");
     if (act != FL_ACT_GLU && Y) return fail(FL_ERR_INVALID_ARG, "Y is only used by the gate (FL_ACT_GLU)");
     const bool values = !A_scales;
-    const size_t need = linear_bytes(M, N, K, values);
+    const LinearPlan plan = plan_linear(M, N, K, values);
+    const size_t need = linear_bytes(plan);
     if (need && (!workspace || workspace_bytes < need))
         return fail(FL_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
     const size_t es = elem_size(dtype), blocks = (size_t)blocks_of(K), outs = (size_t)M * N * es;
@@ -188,12 +232,13 @@ fl_status fl_fused_linear_mx4(const void *A, const uint8_t *A_scales, const uint
     a.blocks = (int)blocks;
     a.act = act;
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     if (dtype == FL_F32)
-        launch_linear<FL_F32>(a, st);
+        launch_linear<FL_F32>(plan, a, ws, st);
     else if (dtype == FL_F16)
-        launch_linear<FL_F16>(a, st);
+        launch_linear<FL_F16>(plan, a, ws, st);
     else
-        launch_linear<FL_BF16>(a, st);
+        launch_linear<FL_BF16>(plan, a, ws, st);
     return check_launch("fl_fused_linear_mx4");
 }
 

@@ -1,0 +1,386 @@
+// fl_mx4_tile.hpp -- gfx950 device code of the 4-bit linear layer for many rows:
+// output tiles whose operands are staged through the LDS.
+//
+//   * A stage is 256 values of K: 128 bytes of codes of each of the tile's rows of
+//     A and of B, copied straight into the LDS (16 bytes a lane), 8 chunks to a row
+//     with chunk c of row r at c ^ fa(r), so that the operand reads of 16
+//     neighbouring rows touch all banks.  Two stages are held: while one is
+//     computed the copies of the next land.
+//   * A stage's scales, 8 bytes of each row, come along the same way (as 16: the
+//     copies have no 8).  Where the last stage has fewer, they are gathered before
+//     the loop into a place of their own, zeros behind them: what follows a row's
+//     scales in memory is the next row's, and may stand for NaN.
+//   * A wave owns 16 MI x 16 NI outputs.  Operands of the next half stage are read
+//     while the matrix instructions of this one run, those of A into the registers
+//     whose row of products is done; the one barrier of a stage sits between its
+//     halves, when its second half is in registers: behind it the stage's place is
+//     free for the copies of the stage after next.
+//   * The rows of B are placed so that the eight results that a lane has of an output
+//     row in NI accumulators (two elements of four, one of eight) are neighbours,
+//     and with them the four lanes of a row: 16-byte stores of 64 bytes in a row,
+//     straight from the accumulators.
+#pragma once
+
+#include "fl_dma16.hpp"
+#include "fl_mx4_linear.hpp"
+
+namespace fl {
+
+struct Mx4TileArgs {
+    Mx4LinearArgs l;
+    float *part;      // parts > 1: sums (parts, M, N)
+    int parts;        // K is cut into this many runs of stages
+    int part_stages;  // stages of a run
+    int tiles_m, tiles_n;
+};
+
+template <int DT, int MI, int NI, int WM, int WN, int PER_CU>
+struct Mx4Tile {
+    static constexpr int WAVES = WM * WN, BM = 16 * MI * WM, BN = 16 * NI * WN;
+    static constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128, SCALES = (BM + BN) * 16;
+    static constexpr int LDS = 2 * (STAGE + SCALES) + SCALES;  // two stages, the last scales
+    static constexpr int NA = BM / 8 / WAVES, NB = BN / 8 / WAVES;  // copies of a wave and stage
+    static constexpr int NS = (BM + BN) / 64 / WAVES;               // and of scales
+    static constexpr int COPIES = NA + NB + NS;
+    static_assert(NA * 8 * WAVES == BM && NB * 8 * WAVES == BN, "whole copies");
+    static_assert(NS * 64 * WAVES == BM + BN && BM % 64 == 0, "whole copies of scales");
+
+    __device__ __forceinline__ static int fa(int r) { return ((r >> 1) ^ ((r & 1) << 2)) & 7; }
+    static constexpr int GROUP = 8 / NI;  // elements of an accumulator to eight columns
+    static_assert(NI == 4 || NI == 8, "eight columns of a lane from whole accumulators");
+    // the column of a wave's 16 NI that element r of accumulator ni has in the lanes of group q
+    __device__ __forceinline__ static int wave_column(int q, int r, int ni) {
+        return r / GROUP * 32 + q * 8 + r % GROUP * NI + ni;
+    }
+    // the tile's column at place p of its rows of B (row d of an operand becomes element d % 4 of lane group d / 4)
+    __device__ __forceinline__ static int column(int p) {
+        const int d = p & 15;
+        return p / (16 * NI) * (16 * NI) + wave_column(d >> 2, d & 3, (p >> 4) % NI);
+    }
+
+    struct Operands {
+        u32x4_t a[MI], b[2][NI];  // b: of this half and the next
+        uint32_t sa[MI], sb[2][NI];  // sb: of this stage and the next
+    };
+
+    const Mx4LinearArgs &l;
+    char *lds;
+    i32x4_t ra, rb, ras, rbs;
+    uint32_t va[NA], vb[NB], vs[NS];
+    int ca[2], cb[2];  // blocks within a stage of a wave's copies of A and B, by their parity
+    uint32_t fa_at[2], fb_at[2], sa_at, sb_at;  // operand reads of the halves, scales
+    int first, stages;  // of this run of K
+    int wave, lane;
+    int rest;  // the stage that has its scales in the third place, or -1
+
+    __device__ __forceinline__ Mx4Tile(const Mx4LinearArgs &args, char *mem, int64_t m0, int64_t n0, int first_stage,
+                                       int n_stages)
+        : l(args), lds(mem), first(first_stage), stages(n_stages) {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        lane = threadIdx.x & 63;
+        const size_t pitch = (size_t)l.blocks * 16;
+        const int64_t m_left = l.M - m0 < BM ? l.M - m0 : BM, n_left = l.N - n0 < BN ? l.N - n0 : BN;
+        ra = sgpr_rsrc(l.a_codes + m0 * pitch, m_left * pitch);
+        rb = sgpr_rsrc(l.b_codes + n0 * pitch, n_left * pitch);
+        ras = sgpr_rsrc(l.a_scales + m0 * l.blocks, m_left * l.blocks);
+        rbs = sgpr_rsrc(l.b_scales + n0 * l.blocks, n_left * l.blocks);
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int row = (wave * NA + i) * 8 + (lane >> 3), c = (lane & 7) ^ fa(row);
+            va[i] = row < m_left ? (uint32_t)row * (uint32_t)pitch + c * 16 : kOob;
+            if (i < 2) ca[i] = c;
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int p = (wave * NB + i) * 8 + (lane >> 3), c = (lane & 7) ^ fa(p), n = column(p);
+            vb[i] = n < n_left ? (uint32_t)n * (uint32_t)pitch + c * 16 : kOob;
+            if (i < 2) cb[i] = c;
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int p = (wave * NS + i) * 64 + lane;  // A's rows, then B's places
+            vs[i] = p < BM ? (p < m_left ? (uint32_t)p * (uint32_t)l.blocks : kOob)
+                           : (column(p - BM) < n_left ? (uint32_t)column(p - BM) * (uint32_t)l.blocks : kOob);
+        }
+        const int d = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            fa_at[h] = (wm * MI * 16 + d) * 128 + ((2 * q + h) ^ fa(d)) * 16;
+            fb_at[h] = A_BYTES + (wn * NI * 16 + d) * 128 + ((2 * q + h) ^ fa(d)) * 16;
+        }
+        sa_at = 2 * STAGE + (wm * MI * 16 + d) * 16 + 2 * q;
+        sb_at = 2 * STAGE + (BM + wn * NI * 16 + d) * 16 + 2 * q;
+        rest = (first + stages) * 8 > l.blocks ? stages - 1 : -1;
+    }
+
+    __device__ __forceinline__ uint32_t lds_at(uint32_t off) const {
+        return (uint32_t)(uintptr_t)(FL_LDS char *)lds + off;
+    }
+
+    // Copy i of a wave of stage j: A's codes, B's, the scales.  Past the last block
+    // zeros are copied, so no stage needs a branch.
+    __device__ __forceinline__ void copy(int j, int i) const {
+        const int s = first + j;
+        if (i < NA) {
+            const uint32_t v = s * 8 + ca[i & 1] < l.blocks ? va[i] : kOob;
+            lds_copy16(ra, v, (uint32_t)s * 128, lds_at((j & 1) * STAGE + (wave * NA + i) * 1024));
+        } else if (i < NA + NB) {
+            const int k = i - NA;
+            const uint32_t v = s * 8 + cb[k & 1] < l.blocks ? vb[k] : kOob;
+            lds_copy16(rb, v, (uint32_t)s * 128, lds_at((j & 1) * STAGE + A_BYTES + (wave * NB + k) * 1024));
+        } else {
+            const int k = i - NA - NB;
+            // the stage in the lane's offset: 16 bytes may pass the array's end, which only that is checked against
+            const uint32_t v = s * 8 + 8 <= l.blocks ? vs[k] + s * 8 : kOob;
+            lds_copy16((wave * NS + k) * 64 < BM ? ras : rbs, v, 0, lds_at(2 * STAGE + (j & 1) * SCALES + (wave * NS + k) * 1024));
+        }
+    }
+    // The last scales of the rows, byte by byte, into the third place.
+    __device__ __forceinline__ void gather_rest(int64_t m0, int64_t n0) const {
+        const int block = l.blocks / 8 * 8, n = l.blocks - block;
+        for (int p = threadIdx.x; p < BM + BN; p += 64 * WAVES) {
+            const int64_t row = p < BM ? m0 + p : n0 + column(p - BM);
+            const uint8_t *s = (p < BM ? l.a_scales : l.b_scales) + row * l.blocks + block;
+            const bool on = row < (p < BM ? l.M : l.N);
+            uint32_t w[2] = {0, 0};
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+                if (on && b < n) w[b / 4] |= (uint32_t)s[b] << (8 * (b % 4));
+            *reinterpret_cast<u32x2_t *>(lds + 2 * STAGE + 2 * SCALES + p * 16) = u32x2_t{w[0], w[1]};
+        }
+    }
+    __device__ __forceinline__ u32x4_t read16(uint32_t off) const { return *reinterpret_cast<const u32x4_t *>(lds + off); }
+    __device__ __forceinline__ u32x4_t read_a(int j, int h, int mi) const {
+        return read16((j & 1) * STAGE + fa_at[h] + mi * 2048);
+    }
+    __device__ __forceinline__ u32x4_t read_b(int j, int h, int ni) const {
+        return read16((j & 1) * STAGE + fb_at[h] + ni * 2048);
+    }
+    __device__ __forceinline__ uint32_t read_scale(uint32_t at, int j) const {
+        return *reinterpret_cast<const uint16_t *>(lds + (j == rest ? 2 : j & 1) * SCALES + at);
+    }
+
+    // Everything of this wave has landed or been read, then everybody's.
+    __device__ __forceinline__ static void meet() {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+
+    __device__ __forceinline__ void run(f32x4_t (&acc)[MI][NI], int64_t m0, int64_t n0) const {
+        if (stages == 0) return;
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) copy(0, i);
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) copy(1, i);
+        if (rest >= 0) gather_rest(m0, n0);
+        meet();
+        Operands o;
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) {
+            o.b[0][ni] = read_b(0, 0, ni);
+            o.sb[0][ni] = read_scale(sb_at + ni * 256, 0);
+        }
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+            o.a[mi] = read_a(0, 0, mi);
+            o.sa[mi] = read_scale(sa_at + mi * 256, 0);
+        }
+#pragma unroll 1
+        for (int j = 0; j < stages; ++j) {
+            half<0, 0>(acc, o, j);
+            // stage j is in registers, everyone's: its place is free; stage j + 1 has landed
+            meet();
+            half<1, 0>(acc, o, j);
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni) o.sb[0][ni] = o.sb[1][ni];
+        }
+        meet();  // the copies past the end
+    }
+
+    // The matrix instructions of half H of stage j, row by row of the wave's blocks, and
+    // between them the operand reads of the half after it and, in the second, the
+    // copies of stage j + 2.  The rows go forth and back: neighbours share an operand.
+    template <int H, int I>
+    __device__ __forceinline__ void half(f32x4_t (&acc)[MI][NI], Operands &o, int j) const {
+        if constexpr (I < MI * NI) {
+            constexpr int SLOTS = MI * NI;
+            constexpr int mi = I / NI, ni = mi & 1 ? NI - 1 - I % NI : I % NI;
+            acc[mi][ni] = mfma_mx4(o.b[H][ni], o.a[mi], acc[mi][ni], o.sb[0][ni], o.sa[mi], H);
+            if constexpr (H == 1 && I * COPIES / SLOTS != (I + 1) * COPIES / SLOTS) copy(j + 2, I * COPIES / SLOTS);
+            if constexpr (I * NI / SLOTS != (I + 1) * NI / SLOTS) {
+                constexpr int k = I * NI / SLOTS;
+                o.b[1 - H][k] = read_b(j + H, 1 - H, k);
+                if constexpr (H == 1) o.sb[1][k] = read_scale(sb_at + k * 256, j + 1);
+            }
+            if constexpr (I % NI == NI - 1) {
+                o.a[mi] = read_a(j + H, 1 - H, mi);
+                if constexpr (H == 1) o.sa[mi] = read_scale(sa_at + mi * 256, j + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            half<H, I + 1>(acc, o, j);
+        }
+    }
+};
+
+// Eight neighbouring elements, all there, 16 bytes at a time.
+template <int DT>
+__device__ __forceinline__ void load_wide(const void *p, int64_t at, float (&f)[8]) {
+    RowValues<DT, 8> v;
+    v.load(p, at, 8);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        const uint32_t w = v.w[DT == FL_F32 ? t : t / 2];
+        f[t] = DT == FL_F32    ? __builtin_bit_cast(float, w)
+               : DT == FL_BF16 ? __builtin_bit_cast(float, t & 1 ? w & 0xffff0000u : w << 16)
+                               : Io<FL_F16>::to_f32((uint16_t)(t & 1 ? w >> 16 : w));
+    }
+}
+template <int DT>
+__device__ __forceinline__ void store_wide(void *p, int64_t at, const float (&f)[8]) {
+    using io = Io<DT>;
+    typename io::raw *q = static_cast<typename io::raw *>(p) + at;
+    uint32_t w[8 * io::size / 4];
+#pragma unroll
+    for (int t = 0; t < 8 * io::size / 4; ++t) {
+        if constexpr (DT == FL_F32)
+            w[t] = __builtin_bit_cast(uint32_t, f[t]);
+        else
+            w[t] = io::pack2(f[2 * t], f[2 * t + 1]);
+    }
+#pragma unroll
+    for (int t = 0; t < io::size / 2; ++t)
+        reinterpret_cast<typename RowValues<DT, 8>::wide *>(q)[t] =
+            typename RowValues<DT, 8>::wide{w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]};
+}
+
+// A wave's tile that lies inside the output, straight from the accumulators, eight
+// columns at a time: ACT, or -1 for the sums of a part.
+template <class T, int DT, int ACT, int MI, int NI>
+__device__ __forceinline__ void store_tile(const Mx4LinearArgs &l, float *part, const f32x4_t (&acc)[MI][NI], int64_t m1,
+                                           int64_t n1, int q) {
+    constexpr int RUNS = 4 / T::GROUP;
+    float b[RUNS][8];
+#pragma unroll
+    for (int g = 0; g < RUNS; ++g) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) b[g][t] = 0.0f;
+        if (ACT >= 0 && l.bias) load_wide<DT>(l.bias, n1 + 32 * g + q * 8, b[g]);
+    }
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+        const int64_t at = (m1 + mi * 16) * l.N + n1 + q * 8;
+#pragma unroll
+        for (int g = 0; g < RUNS; ++g) {
+            float x[8], y[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) x[t] = acc[mi][t % NI][g * T::GROUP + t / NI] + b[g][t];
+            if constexpr (ACT < 0) {
+                store_wide<FL_F32>(part, at + 32 * g, x);
+            } else {
+                if (l.R) {
+                    load_wide<DT>(l.R, at + 32 * g, y);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) x[t] += y[t];
+                }
+                if constexpr (ACT == FL_ACT_GLU) load_wide<DT>(l.Y, at + 32 * g, y);
+                activate_all<ACT>(x, y);
+                store_wide<DT>(l.out, at + 32 * g, x);
+            }
+        }
+    }
+}
+
+template <int DT, int MI, int NI, int WM, int WN, int PER_CU>
+__global__ void __launch_bounds__(64 * WM * WN, PER_CU) mx4_tile_kernel(Mx4TileArgs a) {
+    using T = Mx4Tile<DT, MI, NI, WM, WN, PER_CU>;
+    __shared__ __align__(1024) char lds[T::LDS];
+    const int tiles = a.tiles_m * a.tiles_n;
+    const int part = (int)(blockIdx.x / (unsigned)tiles), pid = (int)(blockIdx.x % (unsigned)tiles);
+    int tm, tn;
+    grouped_tile(xcd_logical(pid, tiles), a.tiles_m, a.tiles_n, 4, tm, tn);
+    const int64_t m0 = (int64_t)tm * T::BM, n0 = (int64_t)tn * T::BN;
+    const int all = (a.l.blocks + 7) / 8, first = part * a.part_stages;
+    const int stages = all - first < a.part_stages ? all - first : a.part_stages;
+    f32x4_t acc[MI][NI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const T t(a.l, lds, m0, n0, first, stages);
+    t.run(acc, m0, n0);
+    const int d = t.lane & 15, q = t.lane >> 4, wm = t.wave / WN, wn = t.wave % WN;
+    float *sums = a.parts > 1 ? a.part + (int64_t)part * a.l.M * a.l.N : nullptr;
+    if (m0 + T::BM <= a.l.M && n0 + T::BN <= a.l.N) {
+        const int64_t m1 = m0 + wm * (16 * MI) + d, n1 = n0 + wn * (16 * NI);
+        if (sums)
+            store_tile<T, DT, -1>(a.l, sums, acc, m1, n1, q);
+        else if (a.l.act == FL_ACT_NONE)
+            store_tile<T, DT, FL_ACT_NONE>(a.l, sums, acc, m1, n1, q);
+        else if (a.l.act == FL_ACT_RELU)
+            store_tile<T, DT, FL_ACT_RELU>(a.l, sums, acc, m1, n1, q);
+        else if (a.l.act == FL_ACT_GELU_TANH)
+            store_tile<T, DT, FL_ACT_GELU_TANH>(a.l, sums, acc, m1, n1, q);
+        else
+            store_tile<T, DT, FL_ACT_GLU>(a.l, sums, acc, m1, n1, q);
+        return;
+    }
+    // A tile across the output's edge: row by row through the stages' place, 16 MI / 2
+    // rows of every wave at a time, each wave its own.
+    constexpr int HALF = MI / 2, COLS = 16 * NI;
+    static_assert(T::WAVES * HALF * 16 * COLS * 4 <= T::LDS, "half a wave's tile fits its part of the LDS");
+    float *mine = reinterpret_cast<float *>(lds) + t.wave * (HALF * 16 * COLS);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int mi = 0; mi < HALF; ++mi)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int ni = 0; ni < NI; ++ni)
+                    mine[(mi * 16 + d) * COLS + T::wave_column(q, r, ni)] = acc[h * HALF + mi][ni][r];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        for (int i = t.lane; i < HALF * 16 * COLS / 4; i += 64) {
+            const int row = i / (COLS / 4), col = i % (COLS / 4) * 4;
+            const int64_t m = m0 + wm * (16 * MI) + h * HALF * 16 + row, n = n0 + wn * COLS + col;
+            const f32x4_t v = *reinterpret_cast<const f32x4_t *>(mine + row * COLS + col);
+            float x[4] = {v[0], v[1], v[2], v[3]};
+            if (m >= a.l.M || n >= a.l.N) continue;
+            if (sums) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < a.l.N) sums[m * a.l.N + n + e] = x[e];
+            } else {
+                finish_columns<DT>(a.l, m, n, x);
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+}
+
+// The sums of the parts in their order, then the epilogue: four columns to a thread.
+template <int DT>
+__global__ void __launch_bounds__(256) mx4_join_kernel(Mx4TileArgs a) {
+    const int64_t across = (a.l.N + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= across * a.l.M) return;
+    const int64_t m = i / across, n = (i - m * across) * 4;
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 0; p < a.parts; ++p) {
+        float f[4];
+        load_floats<FL_F32>(a.part, ((int64_t)p * a.l.M + m) * a.l.N + n, a.l.N - n, f);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x[t] = p ? x[t] + f[t] : f[t];
+    }
+    finish_columns<DT>(a.l, m, n, x);
+}
+
+// The kernels of one type (fl_mx4_inst.hip).
+enum { kMx4Tile256, kMx4Tile128, kMx4Tiles };
+struct Mx4TileShape {
+    int bm, bn;
+};
+constexpr Mx4TileShape kMx4TileShapes[kMx4Tiles] = {{256, 256}, {128, 128}};
+template <int DT>
+void launch_mx4_stream(int variant, const Mx4LinearArgs &a, hipStream_t st);
+template <int DT>
+void launch_mx4_tile(int variant, const Mx4TileArgs &a, hipStream_t st);
+
+}  // namespace fl
