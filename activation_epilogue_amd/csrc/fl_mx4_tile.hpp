@@ -3,18 +3,20 @@
 //
 //   * A stage is 256 values of K: 128 bytes of codes of each of the tile's rows of
 //     A and of B, copied straight into the LDS (16 bytes a lane), 8 chunks to a row
-//     with chunk c of row r at c ^ fa(r), so that the operand reads of 16
-//     neighbouring rows touch all banks.  Two stages are held: while one is
-//     computed the copies of the next land.
-//   * A stage's scales, 8 bytes of each row, come along the same way (as 16: the
-//     copies have no 8).  Where the last stage has fewer, they are gathered before
-//     the loop into a place of their own, zeros behind them: what follows a row's
-//     scales in memory is the next row's, and may stand for NaN.
+//     with chunk c of row r at c ^ fa(r), so that an operand read asks no bank
+//     twice.  Two stages are held: while one is computed the copies of the next land.
+//     A copy costs by the lines it touches, 2 clocks each (a wave's copy of 64-byte
+//     pieces takes twice the time of 128-byte ones).
+//   * Scales are copied for four stages at a time, 32 bytes of each row (8 bytes of a
+//     row for every stage would touch as many lines as the codes do).  A last stage
+//     of fewer than 8 blocks goes by itself, after the others, with its scales
+//     gathered byte by byte and zeros behind them: what follows a row's scales in
+//     memory is the next row's, and may stand for NaN.
 //   * A wave owns 16 MI x 16 NI outputs.  Operands of the next half stage are read
 //     while the matrix instructions of this one run, those of A into the registers
-//     whose row of products is done; the one barrier of a stage sits between its
-//     halves, when its second half is in registers: behind it the stage's place is
-//     free for the copies of the stage after next.
+//     whose row of products is done; the one barrier of a stage comes when its second
+//     half is in registers: behind it the stage's place is free for the copies of
+//     the stage after next.
 //   * The rows of B are placed so that the eight results that a lane has of an output
 //     row in NI accumulators (two elements of four, one of eight) are neighbours,
 //     and with them the four lanes of a row: 16-byte stores of 64 bytes in a row,
@@ -25,6 +27,25 @@
 #include "fl_mx4_linear.hpp"
 
 namespace fl {
+
+// lds_copy16 where `on` (uniform) is not 0, without a branch that the compiler sees: it
+// would move the matrix instructions around it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_copy16_if(uint32_t on, i32x4_t rsrc, uint32_t voffset, uint32_t lds_addr) {
+    asm volatile("s_cmp_eq_u32 %3, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_mov_b32 m0, %2\n\t"
+                 "buffer_load_dwordx4 %0, %1, 0 offen lds\n.Lskip%=:" ::"v"(voffset),
+                 "s"(rsrc), "s"(lds_addr), "s"(__builtin_amdgcn_readfirstlane(on))
+                 : "memory", "m0", "scc");
+}
+#pragma clang diagnostic pop
+
+// v + step, not to be computed before a loop and kept.
+__device__ __forceinline__ uint32_t add_now(uint32_t v, uint32_t step) {
+    uint32_t r;
+    asm volatile("v_add_u32 %0, %2, %1" : "=v"(r) : "v"(v), "s"(__builtin_amdgcn_readfirstlane(step)));
+    return r;
+}
 
 struct Mx4TileArgs {
     Mx4LinearArgs l;
@@ -37,15 +58,18 @@ struct Mx4TileArgs {
 template <int DT, int MI, int NI, int WM, int WN, int PER_CU>
 struct Mx4Tile {
     static constexpr int WAVES = WM * WN, BM = 16 * MI * WM, BN = 16 * NI * WN;
-    static constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128, SCALES = (BM + BN) * 16;
-    static constexpr int LDS = 2 * (STAGE + SCALES) + SCALES;  // two stages, the last scales
+    static constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128, SCALES = (BM + BN) * 32;
+    static constexpr int LDS = 2 * (STAGE + SCALES);                // two stages, the scales of twice four
     static constexpr int NA = BM / 8 / WAVES, NB = BN / 8 / WAVES;  // copies of a wave and stage
-    static constexpr int NS = (BM + BN) / 64 / WAVES;               // and of scales
-    static constexpr int COPIES = NA + NB + NS;
+    static constexpr int NS = (BM + BN) / 32 / WAVES;               // and of four stages' scales
+    static constexpr int COPIES = NA + NB;
     static_assert(NA * 8 * WAVES == BM && NB * 8 * WAVES == BN, "whole copies");
-    static_assert(NS * 64 * WAVES == BM + BN && BM % 64 == 0, "whole copies of scales");
 
-    __device__ __forceinline__ static int fa(int r) { return ((r >> 1) ^ ((r & 1) << 2)) & 7; }
+    // A 16-byte read is served 16 lanes at a time, lanes 0-3, 12-15 and 20-27 first
+    // (measured): eight rows of a chunk c and the eight others of chunk c + 2.  Rows
+    // of 128 bytes take half of the banks each; with bit 1 left alone the two sets'
+    // chunks are the two halves of the row's eight, and no bank is asked twice.
+    __device__ __forceinline__ static int fa(int r) { return (r >> 1 & 1) | (r & 4); }
     static constexpr int GROUP = 8 / NI;  // elements of an accumulator to eight columns
     static_assert(NI == 4 || NI == 8, "eight columns of a lane from whole accumulators");
     // the column of a wave's 16 NI that element r of accumulator ni has in the lanes of group q
@@ -59,84 +83,77 @@ struct Mx4Tile {
     }
 
     struct Operands {
-        u32x4_t a[MI], b[2][NI];  // b: of this half and the next
-        uint32_t sa[MI], sb[2][NI];  // sb: of this stage and the next
+        u32x4_t a[MI], b[2][NI];     // b: of this half and the next
+        uint32_t sa[MI], sb[2][NI];  // two bytes, the halves'; sb: of this stage and the next
     };
 
     const Mx4LinearArgs &l;
     char *lds;
-    i32x4_t ra, rb, ras, rbs;
-    uint32_t va[NA], vb[NB], vs[NS];
-    int ca[2], cb[2];  // blocks within a stage of a wave's copies of A and B, by their parity
-    uint32_t fa_at[2], fb_at[2], sa_at, sb_at;  // operand reads of the halves, scales
-    int first, stages;  // of this run of K
+    i32x4_t ra, rb, rs;
+    // Offsets of the lane's first copies of A, B and scales.  The others lie uniform steps
+    // on; rows past the operand's last are past its descriptor's range.
+    uint32_t va, vb, vs, step_s;
+    int chunk;                             // of a row, that the lane copies
+    uint32_t pitch;                        // of a row of codes
+    uint32_t fa_at, fb_at, sa_at, sb_at;   // operand reads of the first half (the second's: one chunk on), scales
     int wave, lane;
-    int rest;  // the stage that has its scales in the third place, or -1
 
-    __device__ __forceinline__ Mx4Tile(const Mx4LinearArgs &args, char *mem, int64_t m0, int64_t n0, int first_stage,
-                                       int n_stages)
-        : l(args), lds(mem), first(first_stage), stages(n_stages) {
+    __device__ __forceinline__ Mx4Tile(const Mx4LinearArgs &args, char *mem, int64_t m0, int64_t n0) : l(args), lds(mem) {
+        static_assert(NB % 2 == 0 && NB / 2 <= NI && 32 * WAVES * NS == BM + BN && NS <= 2 && BM % (32 * NS) == 0,
+                      "the steps of copy and copy_scales");
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         lane = threadIdx.x & 63;
-        const size_t pitch = (size_t)l.blocks * 16;
+        pitch = (uint32_t)l.blocks * 16;
         const int64_t m_left = l.M - m0 < BM ? l.M - m0 : BM, n_left = l.N - n0 < BN ? l.N - n0 : BN;
-        ra = sgpr_rsrc(l.a_codes + m0 * pitch, m_left * pitch);
-        rb = sgpr_rsrc(l.b_codes + n0 * pitch, n_left * pitch);
-        ras = sgpr_rsrc(l.a_scales + m0 * l.blocks, m_left * l.blocks);
-        rbs = sgpr_rsrc(l.b_scales + n0 * l.blocks, n_left * l.blocks);
-#pragma unroll
-        for (int i = 0; i < NA; ++i) {
-            const int row = (wave * NA + i) * 8 + (lane >> 3), c = (lane & 7) ^ fa(row);
-            va[i] = row < m_left ? (uint32_t)row * (uint32_t)pitch + c * 16 : kOob;
-            if (i < 2) ca[i] = c;
-        }
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int p = (wave * NB + i) * 8 + (lane >> 3), c = (lane & 7) ^ fa(p), n = column(p);
-            vb[i] = n < n_left ? (uint32_t)n * (uint32_t)pitch + c * 16 : kOob;
-            if (i < 2) cb[i] = c;
-        }
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            const int p = (wave * NS + i) * 64 + lane;  // A's rows, then B's places
-            vs[i] = p < BM ? (p < m_left ? (uint32_t)p * (uint32_t)l.blocks : kOob)
-                           : (column(p - BM) < n_left ? (uint32_t)column(p - BM) * (uint32_t)l.blocks : kOob);
-        }
+        ra = sgpr_rsrc(l.a_codes + m0 * pitch, (size_t)m_left * pitch);
+        rb = sgpr_rsrc(l.b_codes + n0 * pitch, (size_t)n_left * pitch);
+        chunk = (lane & 7) ^ fa(lane >> 3);
+        va = (uint32_t)(wave * NA * 8 + (lane >> 3)) * pitch + chunk * 16;
+        vb = (uint32_t)column(wave * NB * 8 + (lane >> 3)) * pitch + chunk * 16;
+        const int p = wave * NS * 32 + (lane >> 1);  // A's rows, then B's places
+        const bool of_a = wave * NS * 32 < BM;
+        rs = of_a ? sgpr_rsrc(l.a_scales + m0 * l.blocks, (size_t)m_left * l.blocks)
+                  : sgpr_rsrc(l.b_scales + n0 * l.blocks, (size_t)n_left * l.blocks);
+        vs = (uint32_t)(of_a ? p : column(p - BM)) * (uint32_t)l.blocks + (lane & 1) * 16;
+        step_s = (uint32_t)(of_a ? 32 : 2) * (uint32_t)l.blocks;
         const int d = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            fa_at[h] = (wm * MI * 16 + d) * 128 + ((2 * q + h) ^ fa(d)) * 16;
-            fb_at[h] = A_BYTES + (wn * NI * 16 + d) * 128 + ((2 * q + h) ^ fa(d)) * 16;
-        }
-        sa_at = 2 * STAGE + (wm * MI * 16 + d) * 16 + 2 * q;
-        sb_at = 2 * STAGE + (BM + wn * NI * 16 + d) * 16 + 2 * q;
-        rest = (first + stages) * 8 > l.blocks ? stages - 1 : -1;
+        fa_at = (wm * MI * 16 + d) * 128 + (2 * q ^ fa(d)) * 16;
+        fb_at = A_BYTES + (wn * NI * 16 + d) * 128 + (2 * q ^ fa(d)) * 16;
+        sa_at = 2 * STAGE + (wm * MI * 16 + d) * 32 + 2 * q;
+        sb_at = 2 * STAGE + (BM + wn * NI * 16 + d) * 32 + 2 * q;
     }
 
     __device__ __forceinline__ uint32_t lds_at(uint32_t off) const {
         return (uint32_t)(uintptr_t)(FL_LDS char *)lds + off;
     }
 
-    // Copy i of a wave of stage j: A's codes, B's, the scales.  Past the last block
-    // zeros are copied, so no stage needs a branch.
-    __device__ __forceinline__ void copy(int j, int i) const {
-        const int s = first + j;
+    // Copy i of a wave of stage s of K, the j-th of its run: A's codes (8 rows on with
+    // every copy), then B's (8 places on: lane group q + 2, 16 columns, or the next
+    // accumulator, one column).  Past the last block zeros are copied, so no stage
+    // needs a branch.
+    __device__ __forceinline__ void copy(int s, int j, int i) const {
+        const bool on = s * 8 + chunk < l.blocks;
+        const uint32_t v = i < NA ? add_now(va, i * 8 * pitch) : add_now(vb, ((i - NA & 1) * 16 + (i - NA) / 2) * pitch);
         if (i < NA) {
-            const uint32_t v = s * 8 + ca[i & 1] < l.blocks ? va[i] : kOob;
-            lds_copy16(ra, v, (uint32_t)s * 128, lds_at((j & 1) * STAGE + (wave * NA + i) * 1024));
-        } else if (i < NA + NB) {
-            const int k = i - NA;
-            const uint32_t v = s * 8 + cb[k & 1] < l.blocks ? vb[k] : kOob;
-            lds_copy16(rb, v, (uint32_t)s * 128, lds_at((j & 1) * STAGE + A_BYTES + (wave * NB + k) * 1024));
+            lds_copy16(ra, on ? v : kOob, (uint32_t)s * 128,
+                       lds_at((j & 1) * STAGE + (wave * NA + i) * 1024));
         } else {
-            const int k = i - NA - NB;
-            // the stage in the lane's offset: 16 bytes may pass the array's end, which only that is checked against
-            const uint32_t v = s * 8 + 8 <= l.blocks ? vs[k] + s * 8 : kOob;
-            lds_copy16((wave * NS + k) * 64 < BM ? ras : rbs, v, 0, lds_at(2 * STAGE + (j & 1) * SCALES + (wave * NS + k) * 1024));
+            const int k = i - NA;
+            lds_copy16(rb, on ? v : kOob, (uint32_t)s * 128,
+                       lds_at((j & 1) * STAGE + A_BYTES + (wave * NB + k) * 1024));
         }
     }
-    // The last scales of the rows, byte by byte, into the third place.
-    __device__ __forceinline__ void gather_rest(int64_t m0, int64_t n0) const {
+    // Copy i of a wave of the scales of stages s to s + 3, the t-th four of a run (32
+    // rows or places, two accumulators, on).  The stage is in the lane's offset: 16 bytes
+    // may pass the array's end, which only that is checked against.
+    __device__ __forceinline__ void copy_scales(uint32_t on, int s, int t, int i) const {
+        const bool some = s * 8 + (lane & 1) * 16 < l.blocks;
+        const uint32_t v = add_now(vs, i * step_s + s * 8);
+        lds_copy16_if(on, rs, some ? v : kOob,
+                      lds_at(2 * STAGE + (t & 1) * SCALES + (wave * NS + i) * 1024));
+    }
+    // The scales of a last stage of fewer than 8 blocks, as a run's first.
+    __device__ __forceinline__ void gather_scales(int64_t m0, int64_t n0) const {
         const int block = l.blocks / 8 * 8, n = l.blocks - block;
         for (int p = threadIdx.x; p < BM + BN; p += 64 * WAVES) {
             const int64_t row = p < BM ? m0 + p : n0 + column(p - BM);
@@ -146,50 +163,54 @@ struct Mx4Tile {
 #pragma unroll
             for (int b = 0; b < 8; ++b)
                 if (on && b < n) w[b / 4] |= (uint32_t)s[b] << (8 * (b % 4));
-            *reinterpret_cast<u32x2_t *>(lds + 2 * STAGE + 2 * SCALES + p * 16) = u32x2_t{w[0], w[1]};
+            *reinterpret_cast<u32x2_t *>(lds + 2 * STAGE + p * 32) = u32x2_t{w[0], w[1]};
         }
     }
     __device__ __forceinline__ u32x4_t read16(uint32_t off) const { return *reinterpret_cast<const u32x4_t *>(lds + off); }
     __device__ __forceinline__ u32x4_t read_a(int j, int h, int mi) const {
-        return read16((j & 1) * STAGE + fa_at[h] + mi * 2048);
+        return read16((j & 1) * STAGE + (fa_at ^ h * 16) + mi * 2048);
     }
     __device__ __forceinline__ u32x4_t read_b(int j, int h, int ni) const {
-        return read16((j & 1) * STAGE + fb_at[h] + ni * 2048);
+        return read16((j & 1) * STAGE + (fb_at ^ h * 16) + ni * 2048);
     }
-    __device__ __forceinline__ uint32_t read_scale(uint32_t at, int j) const {
-        return *reinterpret_cast<const uint16_t *>(lds + (j == rest ? 2 : j & 1) * SCALES + at);
+    __device__ __forceinline__ uint32_t read_scale(uint32_t at, int j, int i) const {
+        return *reinterpret_cast<const uint16_t *>(lds + (j >> 2 & 1) * SCALES + (j & 3) * 8 + at + i * 512);
     }
 
-    // Everything of this wave has landed or been read, then everybody's.
+    // What this wave has asked for has landed and been read; then everybody's.
     __device__ __forceinline__ static void meet() {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
 
-    __device__ __forceinline__ void run(f32x4_t (&acc)[MI][NI], int64_t m0, int64_t n0) const {
-        if (stages == 0) return;
+    // A run of stages of whole blocks, or the last stage by itself.
+    __device__ __forceinline__ void run(f32x4_t (&acc)[MI][NI], int first, int stages, bool last, int64_t m0,
+                                        int64_t n0) const {
+        if (last) {
+            gather_scales(m0, n0);
+        } else {
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) copy(0, i);
+            for (int i = 0; i < NS; ++i) copy_scales(1, first, 0, i);
+        }
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) copy(1, i);
-        if (rest >= 0) gather_rest(m0, n0);
-        meet();
+        for (int i = 0; i < COPIES; ++i) copy(first, 0, i);
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) copy(first + 1, 1, i);
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(COPIES) : "memory");
         Operands o;
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) {
             o.b[0][ni] = read_b(0, 0, ni);
-            o.sb[0][ni] = read_scale(sb_at + ni * 256, 0);
+            o.sb[0][ni] = read_scale(sb_at, 0, ni);
         }
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi) {
             o.a[mi] = read_a(0, 0, mi);
-            o.sa[mi] = read_scale(sa_at + mi * 256, 0);
+            o.sa[mi] = read_scale(sa_at, 0, mi);
         }
 #pragma unroll 1
         for (int j = 0; j < stages; ++j) {
-            half<0, 0>(acc, o, j);
-            // stage j is in registers, everyone's: its place is free; stage j + 1 has landed
-            meet();
-            half<1, 0>(acc, o, j);
+            half<0, 0>(acc, o, j, first, stages);
+            half<1, 0>(acc, o, j, first, stages);
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni) o.sb[0][ni] = o.sb[1][ni];
         }
@@ -197,27 +218,36 @@ struct Mx4Tile {
     }
 
     // The matrix instructions of half H of stage j, row by row of the wave's blocks, and
-    // between them the operand reads of the half after it and, in the second, the
-    // copies of stage j + 2.  The rows go forth and back: neighbours share an operand.
+    // between them the operand reads of the half after it; in the second half also the
+    // next stage's scales, the copies of stage j + 2 and, in the first NS of four
+    // stages, a copy of the scales of the next four.  The rows go forth and back:
+    // neighbours share an operand.
+    static constexpr int SLOTS = MI * NI, MEET = 0;
     template <int H, int I>
-    __device__ __forceinline__ void half(f32x4_t (&acc)[MI][NI], Operands &o, int j) const {
-        if constexpr (I < MI * NI) {
-            constexpr int SLOTS = MI * NI;
+    __device__ __forceinline__ void half(f32x4_t (&acc)[MI][NI], Operands &o, int j, int first, int stages) const {
+        if constexpr (I < SLOTS) {
             constexpr int mi = I / NI, ni = mi & 1 ? NI - 1 - I % NI : I % NI;
+            constexpr int from = H == 1 ? MEET : 0, at = I - from;
+            if constexpr (H == 1 && at == 0) meet();
             acc[mi][ni] = mfma_mx4(o.b[H][ni], o.a[mi], acc[mi][ni], o.sb[0][ni], o.sa[mi], H);
-            if constexpr (H == 1 && I * COPIES / SLOTS != (I + 1) * COPIES / SLOTS) copy(j + 2, I * COPIES / SLOTS);
-            if constexpr (I * NI / SLOTS != (I + 1) * NI / SLOTS) {
-                constexpr int k = I * NI / SLOTS;
-                o.b[1 - H][k] = read_b(j + H, 1 - H, k);
-                if constexpr (H == 1) o.sb[1][k] = read_scale(sb_at + k * 256, j + 1);
+            if constexpr (H == 1 && at >= 0 && at < COPIES) copy(first + j + 2, j, at);
+            if constexpr (H == 1 && at >= COPIES && at < COPIES + NS)
+                copy_scales((j & 3) == 0 && j + 4 < stages, first + j + 4, (j >> 2) + 1, at - COPIES);
+            // B's operands first, all of them are needed at once; A's where their row is done
+            if constexpr (at >= 0 && at < NI) {
+                o.b[1 - H][at] = read_b(j + H, 1 - H, at);
+                if constexpr (H == 1) o.sb[1][at] = read_scale(sb_at, j + 1, at);
             }
-            if constexpr (I % NI == NI - 1) {
-                o.a[mi] = read_a(j + H, 1 - H, mi);
-                if constexpr (H == 1) o.sa[mi] = read_scale(sa_at + mi * 256, j + 1);
-            }
+            if constexpr (H == 1 && at > 0 && at <= MEET / NI) next_a<H>(o, j, at - 1);
+            if constexpr (at >= 0 && I % NI == NI - 1) next_a<H>(o, j, mi);
             __builtin_amdgcn_sched_barrier(0);
-            half<H, I + 1>(acc, o, j);
+            half<H, I + 1>(acc, o, j, first, stages);
         }
+    }
+    template <int H>
+    __device__ __forceinline__ void next_a(Operands &o, int j, int mi) const {
+        o.a[mi] = read_a(j + H, 1 - H, mi);
+        if constexpr (H == 1) o.sa[mi] = read_scale(sa_at, j + 1, mi);
     }
 };
 
@@ -305,9 +335,15 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) mx4_tile_kernel(Mx4TileA
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const T t(a.l, lds, m0, n0, first, stages);
-    t.run(acc, m0, n0);
-    const int d = t.lane & 15, q = t.lane >> 4, wm = t.wave / WN, wn = t.wave % WN;
+    const T t(a.l, lds, m0, n0);
+    const int whole = (first + stages) * 8 > a.l.blocks ? stages - 1 : stages;
+#pragma unroll 1
+    for (int pass = whole > 0 ? 0 : 1; pass < (stages > whole ? 2 : 1); ++pass)
+        t.run(acc, pass ? first + whole : first, pass ? 1 : whole, pass, m0, n0);
+    // what follows is per lane and not to be computed before the loop and kept
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int d = lane & 15, q = lane >> 4, wm = t.wave / WN, wn = t.wave % WN;
     float *sums = a.parts > 1 ? a.part + (int64_t)part * a.l.M * a.l.N : nullptr;
     if (m0 + T::BM <= a.l.M && n0 + T::BN <= a.l.N) {
         const int64_t m1 = m0 + wm * (16 * MI) + d, n1 = n0 + wn * (16 * NI);
@@ -338,7 +374,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) mx4_tile_kernel(Mx4TileA
                 for (int ni = 0; ni < NI; ++ni)
                     mine[(mi * 16 + d) * COLS + T::wave_column(q, r, ni)] = acc[h * HALF + mi][ni][r];
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        for (int i = t.lane; i < HALF * 16 * COLS / 4; i += 64) {
+        for (int i = lane; i < HALF * 16 * COLS / 4; i += 64) {
             const int row = i / (COLS / 4), col = i % (COLS / 4) * 4;
             const int64_t m = m0 + wm * (16 * MI) + h * HALF * 16 + row, n = n0 + wn * COLS + col;
             const f32x4_t v = *reinterpret_cast<const f32x4_t *>(mine + row * COLS + col);
