@@ -70,6 +70,9 @@ struct Mx4Tile {
     // of 128 bytes take half of the banks each; with bit 1 left alone the two sets'
     // chunks are the two halves of the row's eight, and no bank is asked twice.
     __device__ __forceinline__ static int fa(int r) { return (r >> 1 & 1) | (r & 4); }
+    // Of the 32 bytes of scales of row r, the first 16 come second where this is 1: rows 8
+    // apart are in the same banks.
+    __device__ __forceinline__ static int fs(int r) { return r >> 3 & 1; }
     static constexpr int GROUP = 8 / NI;  // elements of an accumulator to eight columns
     static_assert(NI == 4 || NI == 8, "eight columns of a lane from whole accumulators");
     // the column of a wave's 16 NI that element r of accumulator ni has in the lanes of group q
@@ -114,14 +117,17 @@ struct Mx4Tile {
         const bool of_a = wave * NS * 32 < BM;
         rs = of_a ? sgpr_rsrc(l.a_scales + m0 * l.blocks, (size_t)m_left * l.blocks)
                   : sgpr_rsrc(l.b_scales + n0 * l.blocks, (size_t)n_left * l.blocks);
-        vs = (uint32_t)(of_a ? p : column(p - BM)) * (uint32_t)l.blocks + (lane & 1) * 16;
+        vs = (uint32_t)(of_a ? p : column(p - BM)) * (uint32_t)l.blocks + piece() * 16;
         step_s = (uint32_t)(of_a ? 32 : 2) * (uint32_t)l.blocks;
         const int d = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
         fa_at = (wm * MI * 16 + d) * 128 + (2 * q ^ fa(d)) * 16;
         fb_at = A_BYTES + (wn * NI * 16 + d) * 128 + (2 * q ^ fa(d)) * 16;
-        sa_at = 2 * STAGE + (wm * MI * 16 + d) * 32 + 2 * q;
-        sb_at = 2 * STAGE + (BM + wn * NI * 16 + d) * 32 + 2 * q;
+        sa_at = 2 * STAGE + (wm * MI * 16 + d) * 32 + fs(d) * 16 + 2 * q;
+        sb_at = 2 * STAGE + (BM + wn * NI * 16 + d) * 32 + fs(d) * 16 + 2 * q;
     }
+
+    // Which 16 bytes of a row's scales the lane copies.
+    __device__ __forceinline__ int piece() const { return (lane & 1) ^ fs(lane >> 1); }
 
     __device__ __forceinline__ uint32_t lds_at(uint32_t off) const {
         return (uint32_t)(uintptr_t)(FL_LDS char *)lds + off;
@@ -147,7 +153,7 @@ struct Mx4Tile {
     // rows or places, two accumulators, on).  The stage is in the lane's offset: 16 bytes
     // may pass the array's end, which only that is checked against.
     __device__ __forceinline__ void copy_scales(uint32_t on, int s, int t, int i) const {
-        const bool some = s * 8 + (lane & 1) * 16 < l.blocks;
+        const bool some = s * 8 + piece() * 16 < l.blocks;
         const uint32_t v = add_now(vs, i * step_s + s * 8);
         lds_copy16_if(on, rs, some ? v : kOob,
                       lds_at(2 * STAGE + (t & 1) * SCALES + (wave * NS + i) * 1024));
@@ -163,7 +169,7 @@ struct Mx4Tile {
 #pragma unroll
             for (int b = 0; b < 8; ++b)
                 if (on && b < n) w[b / 4] |= (uint32_t)s[b] << (8 * (b % 4));
-            *reinterpret_cast<u32x2_t *>(lds + 2 * STAGE + p * 32) = u32x2_t{w[0], w[1]};
+            *reinterpret_cast<u32x2_t *>(lds + 2 * STAGE + p * 32 + fs(p) * 16) = u32x2_t{w[0], w[1]};
         }
     }
     __device__ __forceinline__ u32x4_t read16(uint32_t off) const { return *reinterpret_cast<const u32x4_t *>(lds + off); }
@@ -174,7 +180,7 @@ struct Mx4Tile {
         return read16((j & 1) * STAGE + (fb_at ^ h * 16) + ni * 2048);
     }
     __device__ __forceinline__ uint32_t read_scale(uint32_t at, int j, int i) const {
-        return *reinterpret_cast<const uint16_t *>(lds + (j >> 2 & 1) * SCALES + (j & 3) * 8 + at + i * 512);
+        return *reinterpret_cast<const uint16_t *>(lds + (j >> 2 & 1) * SCALES + (j & 1) * 8 + (at ^ (j & 2) * 8) + i * 512);
     }
 
     // What this wave has asked for has landed and been read; then everybody's.
@@ -221,33 +227,30 @@ struct Mx4Tile {
     // between them the operand reads of the half after it; in the second half also the
     // next stage's scales, the copies of stage j + 2 and, in the first NS of four
     // stages, a copy of the scales of the next four.  The rows go forth and back:
-    // neighbours share an operand.
-    static constexpr int SLOTS = MI * NI, MEET = 0;
+    // neighbours share an operand.  Copies every second product measured the same as every
+    // third, 2% faster than one after another.
+    static constexpr int SLOTS = MI * NI, PACE = 2 * COPIES + NS <= SLOTS ? 2 : 1;  // products to a copy
     template <int H, int I>
     __device__ __forceinline__ void half(f32x4_t (&acc)[MI][NI], Operands &o, int j, int first, int stages) const {
         if constexpr (I < SLOTS) {
             constexpr int mi = I / NI, ni = mi & 1 ? NI - 1 - I % NI : I % NI;
-            constexpr int from = H == 1 ? MEET : 0, at = I - from;
-            if constexpr (H == 1 && at == 0) meet();
+            if constexpr (H == 1 && I == 0) meet();
             acc[mi][ni] = mfma_mx4(o.b[H][ni], o.a[mi], acc[mi][ni], o.sb[0][ni], o.sa[mi], H);
-            if constexpr (H == 1 && at >= 0 && at < COPIES) copy(first + j + 2, j, at);
-            if constexpr (H == 1 && at >= COPIES && at < COPIES + NS)
-                copy_scales((j & 3) == 0 && j + 4 < stages, first + j + 4, (j >> 2) + 1, at - COPIES);
+            if constexpr (H == 1 && I % PACE == 0 && I / PACE < COPIES) copy(first + j + 2, j, I / PACE);
+            if constexpr (H == 1 && I >= SLOTS - NS)
+                copy_scales((j & 3) == 0 && j + 4 < stages, first + j + 4, (j >> 2) + 1, I - SLOTS + NS);
             // B's operands first, all of them are needed at once; A's where their row is done
-            if constexpr (at >= 0 && at < NI) {
-                o.b[1 - H][at] = read_b(j + H, 1 - H, at);
-                if constexpr (H == 1) o.sb[1][at] = read_scale(sb_at, j + 1, at);
+            if constexpr (I < NI) {
+                o.b[1 - H][I] = read_b(j + H, 1 - H, I);
+                if constexpr (H == 1) o.sb[1][I] = read_scale(sb_at, j + 1, I);
             }
-            if constexpr (H == 1 && at > 0 && at <= MEET / NI) next_a<H>(o, j, at - 1);
-            if constexpr (at >= 0 && I % NI == NI - 1) next_a<H>(o, j, mi);
+            if constexpr (I % NI == NI - 1) {
+                o.a[mi] = read_a(j + H, 1 - H, mi);
+                if constexpr (H == 1) o.sa[mi] = read_scale(sa_at, j + 1, mi);
+            }
             __builtin_amdgcn_sched_barrier(0);
             half<H, I + 1>(acc, o, j, first, stages);
         }
-    }
-    template <int H>
-    __device__ __forceinline__ void next_a(Operands &o, int j, int mi) const {
-        o.a[mi] = read_a(j + H, 1 - H, mi);
-        if constexpr (H == 1) o.sa[mi] = read_scale(sa_at, j + 1, mi);
     }
 };
 
