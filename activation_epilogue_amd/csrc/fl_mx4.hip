@@ -49,24 +49,71 @@ fl_status check_matrix(int64_t rows, int64_t K, int dtype) {
 // size, K in parts where there are few of them.
 struct LinearPlan {
     bool stream, quantize;  // quantize: A's values first, into the workspace
+    fl::Mx4StreamShape shape;
     int variant, parts, part_stages;
     size_t codes, scales, sums;  // bytes of the workspace, in this order
 };
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b); }
 
+// The least estimated time, in us, of (measured at M 1 to 8192, N and K 1024 to
+// 21568; the estimates meet them to 10 to 25%):
+//   streaming   3.4 + 0.25 a round of the chip, 16 rows of A or B and 1024 values of K.  One token
+//               by 14336x4096: 7.7 us, tiles 33; 64 by 4096x14336: 17.5, tiles 19; 128 by
+//               14336x4096: 22, tiles 15.
+//   256x256     a round 6 + 1.75 a stage of 256 values of K.
+//   128x128     two to a CU: a round 4 + 1.24 a stage, 0.7 where they have a CU to
+//               themselves.  1024x21568x4096 80 us, 92 with 256x256; 8192x8192x8192 327
+//               and 260.
+//   parts of K  a join of 4, and the sums written and read at 5 TB/s: 128 by 4096x14336
+//               43 us in one part, 18.7 in 6.
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
     LinearPlan p{};
-    const int64_t blocks = blocks_of(K);
+    const int64_t blocks = blocks_of(K), stages = (blocks + 7) / 8;
     p.parts = 1;
-    p.part_stages = (int)((blocks + 7) / 8);
-    if (!M || !N || !K) {
-        p.stream = true;
-        return p;
+    p.part_stages = (int)stages;
+    p.stream = true;
+    p.shape = {1, 1, 8};
+    if (!M || !N || !K) return p;
+    double least = 1e30;
+    for (int mt = 1; mt <= 4 && M <= 512; mt *= 2)
+        for (int nt = 1; nt <= 4; nt *= 2) {
+            if (mt == 4 && nt == 1) continue;                    // 2 by 2 has its products with fewer rows
+            if ((mt > 1 && M <= 8 * mt) || (M <= 2 && nt > 1) || (M <= 4 && nt > 2)) continue;  // measured slower
+            const double x = ceil_div(N, 16 * nt) * ceil_div(M, 16 * mt) / 256;
+            const double rows = M < 16 * mt ? M / 16.0 : mt;  // of A, in units of 16
+            const double time = 3.4 + 0.25 * (x < 1 ? 1 : x) * (rows + nt) * K / 1024;
+            if (time < least) {
+                least = time;
+                p.shape = {mt, nt, 8};
+            }
+        }
+    if (p.shape.mt == 1 && p.shape.nt == 1 && N <= 256 * 16) p.shape.waves = 16;  // a block to a CU
+    for (int v = 0; v < fl::kMx4Tiles; ++v) {
+        const fl::Mx4TileShape &t = fl::kMx4TileShapes[v];
+        const double tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
+        for (int parts = 1; parts <= 16; ++parts) {
+            const int64_t run = (stages + parts - 1) / parts;
+            if (parts > 1 && (run < 2 || tiles * parts > 512 || (stages + run - 1) / run != parts)) continue;
+            const double x = tiles * parts;
+            double time = 3.4 + (parts > 1 ? 4 + parts * (double)M * N * 8 / 5e6 : 0);
+            if (v == fl::kMx4Tile256)
+                time += ceil_div(x, 256) * (6 + 1.75 * run);
+            else
+                time += x <= 256 ? 4 + 0.7 * run : ceil_div(x, 512) * (4 + 1.24 * run);
+            if (time < least) {
+                least = time;
+                p.stream = false;
+                p.variant = v;
+                p.parts = parts;
+                p.part_stages = (int)run;
+            }
+        }
     }
-    p.stream = M <= 64;
-    p.variant = ((M + 255) / 256) * ((N + 255) / 256) >= 200 ? fl::kMx4Tile256 : fl::kMx4Tile128;
-    p.quantize = values && !p.stream;
+    // up to four rows every block quantises them faster than another launch does (4
+    // by 14336x4096: 10.0 us, 11.0; 8: 12.5, 11.5)
+    p.quantize = values && !(p.stream && M <= 4);
     if (p.quantize) {
         p.codes = (size_t)(M * blocks * 16);
         p.scales = align16((size_t)(M * blocks));
@@ -93,7 +140,7 @@ void launch_linear(const LinearPlan &p, fl::Mx4LinearArgs l, uint8_t *ws, hipStr
         l.a_scales = q.scales;
     }
     if (p.stream) {
-        fl::launch_mx4_stream<DT>(p.variant, l, st);
+        fl::launch_mx4_stream<DT>(p.shape, l, st);
         return;
     }
     fl::Mx4TileArgs a{};
@@ -219,7 +266,7 @@ fl_status fl_fused_linear_mx4(const void *A, const uint8_t *A_scales, const uint
     fl::Mx4LinearArgs a{};
     a.a_codes = values ? nullptr : static_cast<const uint8_t *>(A);
     a.a_scales = A_scales;
-    a.a_raw = values ? A : nullptr;
+    a.a_raw = values && K ? A : nullptr;
     a.b_codes = B;
     a.b_scales = B_scales;
     a.bias = bias;

@@ -6,13 +6,19 @@ namespace fl {
 
 namespace {
 
-template <int DT, int MT, int NT, int WAVES, int U>
-void launch_stream(const Mx4LinearArgs &a, hipStream_t st) {
-    const dim3 grid((unsigned)(((a.N + 16 * NT - 1) / (16 * NT)) * ((a.M + 16 * MT - 1) / (16 * MT))));
-    if (a.a_raw)
-        hipLaunchKernelGGL((mx4_stream_kernel<DT, MT, NT, WAVES, U, true>), grid, dim3(64 * WAVES), 0, st, a);
-    else
-        hipLaunchKernelGGL((mx4_stream_kernel<DT, MT, NT, WAVES, U, false>), grid, dim3(64 * WAVES), 0, st, a);
+template <int DT, int MT, int NT, int WAVES, bool VALUES>
+void launch_stream_of(const Mx4LinearArgs &l, hipStream_t st) {
+    // the largest panel whose scales (and codes of A's values) take 48 KB
+    const int64_t rows = VALUES ? l.M : 16 * MT;
+    int64_t panel = 256;
+    auto bytes = [&](int64_t n) {
+        return 16 * NT * (n + kMx4ScalePad) + rows * (n + kMx4ScalePad) + (VALUES ? rows * n * 16 : 0);
+    };
+    while (panel < l.blocks && bytes(panel + 256) <= 49152) panel += 256;
+    const int64_t sums = (int64_t)WAVES * MT * NT * 1024, lds = bytes(panel) > sums ? bytes(panel) : sums;
+    const dim3 grid((unsigned)(((l.N + 16 * NT - 1) / (16 * NT)) * ((l.M + 16 * MT - 1) / (16 * MT))));
+    hipLaunchKernelGGL((mx4_stream_kernel<DT, MT, NT, WAVES, VALUES>), grid, dim3(64 * WAVES), (size_t)lds, st,
+                       Mx4StreamArgs{l, (int)panel});
 }
 
 template <int DT, int MI, int NI, int WM, int WN, int PER_CU>
@@ -24,10 +30,24 @@ void launch_tile(const Mx4TileArgs &a, hipStream_t st) {
 }  // namespace
 
 template <>
-void launch_mx4_stream<FL_INST_DTYPE>(int variant, const Mx4LinearArgs &a, hipStream_t st) {
+void launch_mx4_stream<FL_INST_DTYPE>(const Mx4StreamShape &shape, const Mx4LinearArgs &a, hipStream_t st) {
     constexpr int DT = FL_INST_DTYPE;
-    (void)variant;
-    launch_stream<DT, 1, 1, 4, 2>(a, st);
+    if (a.a_raw) {
+        if (shape.waves == 16) return launch_stream_of<DT, 1, 1, 16, true>(a, st);
+        return shape.nt == 1 ? launch_stream_of<DT, 1, 1, 8, true>(a, st) : launch_stream_of<DT, 1, 2, 8, true>(a, st);
+    }
+    if (shape.waves == 16) return launch_stream_of<DT, 1, 1, 16, false>(a, st);
+#define FL_STREAM(m, n) \
+    if (shape.mt == m && shape.nt == n) return launch_stream_of<DT, m, n, 8, false>(a, st)
+    FL_STREAM(1, 1);
+    FL_STREAM(1, 2);
+    FL_STREAM(1, 4);
+    FL_STREAM(2, 1);
+    FL_STREAM(2, 2);
+    FL_STREAM(2, 4);
+    FL_STREAM(4, 2);
+    FL_STREAM(4, 4);
+#undef FL_STREAM
 }
 
 template <>

@@ -28,15 +28,13 @@ struct Mx4LinearArgs {
     int K, blocks, act;
 };
 
+// n, m: operands of B and of A; the scales' byte `half`, 0 or 1, which has to be a constant.
 __device__ __forceinline__ f32x4_t mfma_mx4(u32x4_t n, u32x4_t m, f32x4_t c, uint32_t n_scales, uint32_t m_scales,
-                                            int step) {
+                                            int half) {
     const i32x8_mx_t x{(int)n[0], (int)n[1], (int)n[2], (int)n[3], 0, 0, 0, 0};
     const i32x8_mx_t y{(int)m[0], (int)m[1], (int)m[2], (int)m[3], 0, 0, 0, 0};
-    // 4: E2M1 operands; the selected byte of a scale register has to be a constant
-    return step == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)n_scales, 0, (int)m_scales)
-           : step == 1 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 1, (int)n_scales, 1, (int)m_scales)
-           : step == 2 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 2, (int)n_scales, 2, (int)m_scales)
-                       : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 3, (int)n_scales, 3, (int)m_scales);
+    return half ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 1, (int)n_scales, 1, (int)m_scales)
+                : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)n_scales, 0, (int)m_scales);
 }
 
 typedef uint32_t any2_u32_t __attribute__((aligned(2)));
@@ -113,115 +111,148 @@ __device__ __forceinline__ void finish_columns(const Mx4LinearArgs &a, int64_t m
 
 // ------------------------------------------------------------------ few rows
 
-// A lane's two chunks of 256 values of one row and their scales, from the rows
-// that the descriptors start at; zeros where a row or a block is none.
-struct Mx4Pair {
-    u32x4_t c[2];
-    uint32_t s;
-
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales, int row, int block,
-                                         int blocks) {
-        const bool two = block + 1 < blocks, one = block < blocks;
-        const uint32_t at = (uint32_t)row * (uint32_t)blocks + (uint32_t)block;
-        c[0] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(codes, one ? at * 16 : kOob, 0, 0));
-        c[1] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(codes, two ? at * 16 + 16 : kOob, 0, 0));
-        if (blocks & 1) {  // the last block of a row may be the first of a pair
-            s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(scales, one ? at : kOob, 0, 0) & 0xffu;
-            s |= ((uint32_t)__builtin_amdgcn_raw_buffer_load_b8(scales, two ? at + 1 : kOob, 0, 0) & 0xffu) << 8;
-        } else {
-            s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(scales, one ? at : kOob, 0, 0) & 0xffffu;
-        }
-    }
-};
-
-// The same from a row of values, quantised: a block of 32 is one lane's, so its
-// largest magnitude takes no exchange.
-template <int DT>
-__device__ __forceinline__ void quantize_pair(Mx4Pair &p, const void *x, int64_t row, bool on, int block, int K) {
-    using V = RowValues<DT, 32>;
-    V v[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t k = (int64_t)(block + h) * 32;
-        v[h].load(x, row * K + k, on ? K - k : 0);
-    }
-    p.s = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t m = magnitude_bits<DT>(v[h].w[0]);
-#pragma unroll
-        for (int e = 1; e < V::WORDS; ++e) m = larger_bits<DT>(m, magnitude_bits<DT>(v[h].w[e]));
-        const uint32_t s = scale_byte<DT>(m);
-        p.s |= s << (8 * h);
-#pragma unroll
-        for (int g = 0; g < 4; ++g) p.c[h][g] = s == 255 ? 0 : codes8<DT>(v[h].w + g * (V::WORDS / 4), scale_value(s));
-    }
-}
-
 // 16 MT rows by 16 NT columns to a block, whose WAVES waves share out K 256 values
 // at a time: each streams its part of B's rows straight into registers, as they
-// are operands, U steps in flight; the waves' sums meet in the LDS in a fixed
+// are operands; the waves' sums meet in the LDS in a fixed
 // order.  No row of B is read twice as long as M <= 16 MT; A comes from the caches.
-template <int DT, int MT, int NT, int WAVES, int U, bool RAW>
-__global__ void __launch_bounds__(64 * WAVES) mx4_stream_kernel(Mx4LinearArgs a) {
-    __shared__ f32x4_t sums[WAVES][MT * NT][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, d = lane & 15, q = lane >> 4;
+//
+// A load costs by the lines it touches, so the scales, of which a step needs 8
+// bytes of each row, are brought into the LDS in whole rows first, `panel` blocks of K
+// at a time.  VALUES: A (MT = 1) is given as values; every block quantises them into
+// the LDS, which takes less than another launch while the rows are few.
+constexpr int kMx4ScalePad = 16;  // rows of scales 16 bytes past a multiple of 256: 16 rows in different banks
+
+struct Mx4StreamArgs {
+    Mx4LinearArgs l;
+    int panel;  // blocks, a multiple of 256 (scales of 256 blocks: 256 bytes)
+};
+
+template <int DT, int MT, int NT, int WAVES, bool VALUES>
+__global__ void __launch_bounds__(64 * WAVES) mx4_stream_kernel(Mx4StreamArgs s) {
+    static_assert(!VALUES || MT == 1, "few rows");
+    extern __shared__ __align__(16) char lds[];
+    const Mx4LinearArgs &a = s.l;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), d = lane & 15, q = lane >> 4;
     const uint32_t across = (uint32_t)((a.N + 16 * NT - 1) / (16 * NT));
     const int64_t n0 = (int64_t)(blockIdx.x % across) * (16 * NT), m0 = (int64_t)(blockIdx.x / across) * (16 * MT);
-    const size_t pitch = (size_t)a.blocks * 16;
-    const int64_t n_left = a.N - n0 < 16 * NT ? a.N - n0 : 16 * NT, m_left = a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT;
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.b_codes + n0 * pitch, n_left * pitch);
-    const __amdgpu_buffer_rsrc_t rbs = make_rsrc(a.b_scales + n0 * a.blocks, n_left * a.blocks);
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(RAW ? nullptr : a.a_codes + m0 * pitch, RAW ? 0 : m_left * pitch);
-    const __amdgpu_buffer_rsrc_t ras = make_rsrc(RAW ? nullptr : a.a_scales + m0 * a.blocks, RAW ? 0 : m_left * a.blocks);
+    const uint32_t pitch = (uint32_t)a.blocks * 16;
+    const int n_left = (int)(a.N - n0 < 16 * NT ? a.N - n0 : 16 * NT), m_left = (int)(a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT);
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(a.b_codes + n0 * pitch, (size_t)n_left * pitch);
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(VALUES ? nullptr : a.a_codes + m0 * pitch, VALUES ? 0 : (size_t)m_left * pitch);
+    // in the LDS: rows of scales, B's then A's; the codes of A's values
+    const int row_bytes = s.panel + kMx4ScalePad;
+    char *b_scales = lds, *a_scales = lds + 16 * NT * row_bytes, *a_codes = a_scales + (VALUES ? m_left : 16 * MT) * row_bytes;
     f32x4_t acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int b0 = wave * 8; b0 < a.blocks; b0 += WAVES * U * 8) {
-        Mx4Pair b[U][NT], p[U][MT];
+
+    for (int p0 = 0; p0 < a.blocks; p0 += s.panel) {
+        const int blocks = a.blocks - p0 < s.panel ? a.blocks - p0 : s.panel;  // of this panel
+        u32x4_t b[NT][2], m[MT][2];
+        const auto load = [&](int c0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int h = 0; h < 2; ++h) {
+                const int block = c0 + 2 * q + h;  // in the panel
+                const bool on = block < blocks;
+                const uint32_t at = (uint32_t)(p0 + block) * 16;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) b[u][j].load(rb, rbs, j * 16 + d, b0 + u * WAVES * 8 + 2 * q, a.blocks);
-        if constexpr (!RAW) {
+                for (int j = 0; j < NT; ++j)
+                    b[j][h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                              rb, on ? (uint32_t)(j * 16 + d) * pitch + at : kOob, 0, 0));
+                if constexpr (!VALUES) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                    for (int i = 0; i < MT; ++i)
+                        m[i][h] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                                  ra, on ? (uint32_t)(i * 16 + d) * pitch + at : kOob, 0, 0));
+                }
+            }
+        };
+        load(wave * 8);
+        // scales, 16 blocks to a thread; zeros behind a row's last and in rows that are none
+        const int pieces = (blocks + 15) / 16, rows = VALUES ? 16 * NT : 16 * (NT + MT);
+        for (int i = threadIdx.x; i < pieces * rows; i += 64 * WAVES) {
+            const int row = i / pieces, k = (i - row * pieces) * 16;
+            const bool of_b = row < 16 * NT;
+            const int r = of_b ? row : row - 16 * NT;
+            const uint8_t *src = (of_b ? a.b_scales + (n0 + r) * a.blocks : a.a_scales + (m0 + r) * a.blocks) + p0 + k;
+            u32x4_t w{0, 0, 0, 0};
+            if (r < (of_b ? n_left : m_left)) {
+                if (k + 16 <= blocks) {
+                    typedef uint32_t any1_u32x4_t __attribute__((ext_vector_type(4), aligned(1)));
+                    w = *reinterpret_cast<const any1_u32x4_t *>(src);
+                } else {
 #pragma unroll
-                for (int i = 0; i < MT; ++i) p[u][i].load(ra, ras, i * 16 + d, b0 + u * WAVES * 8 + 2 * q, a.blocks);
+                    for (int t = 0; t < 16; ++t)
+                        if (k + t < blocks) w[t / 4] |= (uint32_t)src[t] << (8 * (t % 4));
+                }
+            }
+            *reinterpret_cast<u32x4_t *>(b_scales + row * row_bytes + k) = w;
         }
+        if constexpr (VALUES) {
+            // eight values to a thread, a block of 32 to four neighbours, up to whole pieces of 16 blocks
+            const int per_row = pieces * 64;
+            for (int i0 = 0; i0 < per_row * m_left; i0 += 64 * WAVES) {
+                const int i = i0 + threadIdx.x, row = i / per_row, unit = i - row * per_row;
+                const int64_t k = (int64_t)p0 * 32 + unit * 8;
+                RowValues<DT, 8> v;
+                v.load(a.a_raw, (m0 + row) * a.K + k, row < m_left ? a.K - k : 0);
+                uint32_t top = magnitude_bits<DT>(v.w[0]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if constexpr (RAW) {
+                for (int e = 1; e < RowValues<DT, 8>::WORDS; ++e) top = larger_bits<DT>(top, magnitude_bits<DT>(v.w[e]));
+                top = larger_bits<DT>(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xb1, 0xf, 0xf, true));
+                top = larger_bits<DT>(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4e, 0xf, 0xf, true));
+                const uint32_t sc = scale_byte<DT>(top);
+                if (row >= m_left) continue;
+                *reinterpret_cast<uint32_t *>(a_codes + row * (s.panel * 16) + unit * 4) =
+                    sc == 255 ? 0 : codes8<DT>(v.w, scale_value(sc));
+                if ((unit & 3) == 0) a_scales[row * row_bytes + unit / 4] = (char)sc;
+            }
+        }
+        __syncthreads();
+        for (int c0 = wave * 8; c0 < blocks;) {
+            const int at = c0 + 2 * q;
+            uint32_t sb[NT], sa[MT];
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    quantize_pair<DT>(p[u][i], a.a_raw, m0 + i * 16 + d, i * 16 + d < m_left,
-                                      b0 + u * WAVES * 8 + 2 * q, a.K);
+            for (int j = 0; j < NT; ++j) sb[j] = *reinterpret_cast<const uint16_t *>(b_scales + (j * 16 + d) * row_bytes + at);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                // a lane of no row takes the first's: its column of the results goes nowhere
+                const int row = VALUES ? (d < m_left ? d : 0) : i * 16 + d;
+                sa[i] = *reinterpret_cast<const uint16_t *>(a_scales + row * row_bytes + at);
+                if constexpr (VALUES) {
+                    m[i][0] = *reinterpret_cast<const u32x4_t *>(a_codes + row * (s.panel * 16) + at * 16);
+                    m[i][1] = *reinterpret_cast<const u32x4_t *>(a_codes + row * (s.panel * 16) + at * 16 + 16);
+                }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        acc[i][j] = mfma_mx4(b[u][j].c[h], p[u][i].c[h], acc[i][j], b[u][j].s, p[u][i].s, h);
+                    for (int j = 0; j < NT; ++j) acc[i][j] = mfma_mx4(b[j][h], m[i][h], acc[i][j], sb[j], sa[i], h);
+            c0 += WAVES * 8;
+            if (c0 < blocks) load(c0);
         }
+        __syncthreads();  // the scales are read; the next panel's, or the sums, take their place
     }
+    // the sums of the waves, whose place the scales had
+    f32x4_t *sums = reinterpret_cast<f32x4_t *>(lds);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) sums[wave][i * NT + j][lane] = acc[i][j];
+        for (int j = 0; j < NT; ++j) sums[(wave * (MT * NT) + i * NT + j) * 64 + lane] = acc[i][j];
     __syncthreads();
     for (int t = threadIdx.x; t < MT * NT * 64; t += 64 * WAVES) {
         const int l = t & 63, i = (t >> 6) / NT, j = (t >> 6) % NT;
-        f32x4_t s = sums[0][t >> 6][l];
+        f32x4_t v = sums[t];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) s += sums[w][t >> 6][l];
-        const int64_t m = m0 + i * 16 + (l & 15), n = n0 + j * 16 + (l >> 4) * 4;
-        if (m >= a.M || n >= a.N) continue;
-        float x[4] = {s[0], s[1], s[2], s[3]};
-        finish_columns<DT>(a, m, n, x);
+        for (int w = 1; w < WAVES; ++w) v += sums[w * (MT * NT * 64) + t];
+        const int64_t mm = m0 + i * 16 + (l & 15), n = n0 + j * 16 + (l >> 4) * 4;
+        if (mm >= a.M || n >= a.N) continue;
+        float x[4] = {v[0], v[1], v[2], v[3]};
+        finish_columns<DT>(a, mm, n, x);
     }
 }
 

@@ -417,8 +417,11 @@ struct Mx4TileShape {
     int bm, bn;
 };
 constexpr Mx4TileShape kMx4TileShapes[kMx4Tiles] = {{256, 256}, {128, 128}};
+struct Mx4StreamShape {
+    int mt, nt, waves;  // 16 mt rows by 16 nt columns to a block of this many waves
+};
 template <int DT>
-void launch_mx4_stream(int variant, const Mx4LinearArgs &a, hipStream_t st);
+void launch_mx4_stream(const Mx4StreamShape &shape, const Mx4LinearArgs &a, hipStream_t st);
 template <int DT>
 void launch_mx4_tile(int variant, const Mx4TileArgs &a, hipStream_t st);
 
