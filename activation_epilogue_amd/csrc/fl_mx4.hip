@@ -62,10 +62,10 @@ double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b);
 //   streaming   3.4 + 0.25 a round of the chip, 16 rows of A or B and 1024 values of K.  One token
 //               by 14336x4096: 7.7 us, tiles 33; 64 by 4096x14336: 17.5, tiles 19; 128 by
 //               14336x4096: 22, tiles 15.
-//   256x256     a round 6 + 1.75 a stage of 256 values of K.
+//   256x256     a round 8 + 1.75 a stage of 256 values of K.
 //   128x128     two to a CU: a round 4 + 1.24 a stage, 0.7 where they have a CU to
-//               themselves.  1024x21568x4096 80 us, 92 with 256x256; 8192x8192x8192 327
-//               and 260.
+//               themselves.  512x21568x1024 16 us, 18 with 256x256; 8192x14336x4096 318
+//               and 265.
 //   parts of K  a join of 4, and the sums written and read at 5 TB/s: 128 by 4096x14336
 //               43 us in one part, 18.7 in 6.
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
@@ -99,9 +99,9 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
             const double x = tiles * parts;
             double time = 3.4 + (parts > 1 ? 4 + parts * (double)M * N * 8 / 5e6 : 0);
             if (v == fl::kMx4Tile256)
-                time += ceil_div(x, 256) * (6 + 1.75 * run);
+                time += ceil_div(x, 256) * (8 + 1.75 * run);
             else
-                time += x <= 256 ? 4 + 0.7 * run : ceil_div(x, 512) * (4 + 1.24 * run);
+                time += x <= 256 ? 4 + 0.7 * run : (x <= 460 ? 1 : x / 512 + 0.1) * (4 + 1.24 * run);
             if (time < least) {
                 least = time;
                 p.stream = false;

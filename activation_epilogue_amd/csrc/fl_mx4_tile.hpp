@@ -254,70 +254,117 @@ struct Mx4Tile {
     }
 };
 
-// Eight neighbouring elements, all there, 16 bytes at a time.
+// Eight neighbouring elements of an operand or output through a descriptor, 16 bytes at
+// a time; kOob reads zeros and stores nothing.
 template <int DT>
-__device__ __forceinline__ void load_wide(const void *p, int64_t at, float (&f)[8]) {
-    RowValues<DT, 8> v;
-    v.load(p, at, 8);
+__device__ __forceinline__ void load_eight(__amdgpu_buffer_rsrc_t r, uint32_t off, float (&f)[8]) {
+    constexpr int PIECES = Io<DT>::size / 2;
+    u32x4_t w[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+        w[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, i * 16, 0));
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-        const uint32_t w = v.w[DT == FL_F32 ? t : t / 2];
-        f[t] = DT == FL_F32    ? __builtin_bit_cast(float, w)
-               : DT == FL_BF16 ? __builtin_bit_cast(float, t & 1 ? w & 0xffff0000u : w << 16)
-                               : Io<FL_F16>::to_f32((uint16_t)(t & 1 ? w >> 16 : w));
+        const uint32_t u = DT == FL_F32 ? w[t / 4][t % 4] : w[0][t / 2];
+        f[t] = DT == FL_F32    ? __builtin_bit_cast(float, u)
+               : DT == FL_BF16 ? __builtin_bit_cast(float, t & 1 ? u & 0xffff0000u : u << 16)
+                               : Io<FL_F16>::to_f32((uint16_t)(t & 1 ? u >> 16 : u));
     }
 }
 template <int DT>
-__device__ __forceinline__ void store_wide(void *p, int64_t at, const float (&f)[8]) {
-    using io = Io<DT>;
-    typename io::raw *q = static_cast<typename io::raw *>(p) + at;
-    uint32_t w[8 * io::size / 4];
+__device__ __forceinline__ void store_eight(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&f)[8]) {
+    constexpr int PIECES = Io<DT>::size / 2;
 #pragma unroll
-    for (int t = 0; t < 8 * io::size / 4; ++t) {
-        if constexpr (DT == FL_F32)
-            w[t] = __builtin_bit_cast(uint32_t, f[t]);
-        else
-            w[t] = io::pack2(f[2 * t], f[2 * t + 1]);
+    for (int i = 0; i < PIECES; ++i) {
+        u32x4_t w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (DT == FL_F32)
+                w[e] = __builtin_bit_cast(uint32_t, f[4 * i + e]);
+            else
+                w[e] = Io<DT>::pack2(f[2 * e], f[2 * e + 1]);
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u32_t, w), r, off, i * 16, 0);
     }
-#pragma unroll
-    for (int t = 0; t < io::size / 2; ++t)
-        reinterpret_cast<typename RowValues<DT, 8>::wide *>(q)[t] =
-            typename RowValues<DT, 8>::wide{w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]};
 }
 
-// A wave's tile that lies inside the output, straight from the accumulators, eight
-// columns at a time: ACT, or -1 for the sums of a part.
+// A wave's tile, straight from the accumulators, eight columns at a time: ACT, or -1
+// for the sums of a part.  Rows and eights across the output's edge are left out.
+// (m, n: the lane's first in the tile; m_left, n_left: of the output, from the tile's corner.)
 template <class T, int DT, int ACT, int MI, int NI>
-__device__ __forceinline__ void store_tile(const Mx4LinearArgs &l, float *part, const f32x4_t (&acc)[MI][NI], int64_t m1,
-                                           int64_t n1, int q) {
-    constexpr int RUNS = 4 / T::GROUP;
+__device__ __forceinline__ void store_tile(const Mx4LinearArgs &l, float *part, const f32x4_t (&acc)[MI][NI], int64_t m0,
+                                           int64_t n0, int m, int n, int64_t m_left, int64_t n_left) {
+    constexpr int RUNS = 4 / T::GROUP, ES = ACT < 0 ? 4 : Io<DT>::size;
+    const int64_t corner = m0 * l.N + n0;
+    const size_t rest = (size_t)(l.M * l.N - corner) * ES;
+    const __amdgpu_buffer_rsrc_t ro =
+        make_rsrc(ACT < 0 ? reinterpret_cast<char *>(part + corner) : static_cast<char *>(l.out) + corner * ES, rest);
+    const __amdgpu_buffer_rsrc_t rr = make_rsrc(static_cast<const char *>(l.R) + corner * ES, l.R ? rest : 0);
+    const __amdgpu_buffer_rsrc_t ry = make_rsrc(static_cast<const char *>(l.Y) + corner * ES, l.Y ? rest : 0);
+    const __amdgpu_buffer_rsrc_t rb =
+        make_rsrc(static_cast<const char *>(l.bias) + n0 * ES, l.bias ? (size_t)(l.N - n0) * ES : 0);
     float b[RUNS][8];
 #pragma unroll
-    for (int g = 0; g < RUNS; ++g) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) b[g][t] = 0.0f;
-        if (ACT >= 0 && l.bias) load_wide<DT>(l.bias, n1 + 32 * g + q * 8, b[g]);
-    }
+    for (int g = 0; g < RUNS; ++g)
+        if constexpr (ACT >= 0) load_eight<DT>(rb, n + 32 * g + 8 <= n_left ? (uint32_t)(n + 32 * g) * ES : kOob, b[g]);
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
-        const int64_t at = (m1 + mi * 16) * l.N + n1 + q * 8;
 #pragma unroll
         for (int g = 0; g < RUNS; ++g) {
+            const bool on = m + mi * 16 < m_left && n + 32 * g + 8 <= n_left;
+            const uint32_t at = on ? ((uint32_t)(m + mi * 16) * (uint32_t)l.N + (uint32_t)(n + 32 * g)) * ES : kOob;
             float x[8], y[8];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) x[t] = acc[mi][t % NI][g * T::GROUP + t / NI] + b[g][t];
+            for (int t = 0; t < 8; ++t) x[t] = acc[mi][t % NI][g * T::GROUP + t / NI];
             if constexpr (ACT < 0) {
-                store_wide<FL_F32>(part, at + 32 * g, x);
+                store_eight<FL_F32>(ro, at, x);
             } else {
+#pragma unroll
+                for (int t = 0; t < 8; ++t) x[t] += b[g][t];
                 if (l.R) {
-                    load_wide<DT>(l.R, at + 32 * g, y);
+                    load_eight<DT>(rr, at, y);
 #pragma unroll
                     for (int t = 0; t < 8; ++t) x[t] += y[t];
                 }
-                if constexpr (ACT == FL_ACT_GLU) load_wide<DT>(l.Y, at + 32 * g, y);
+                if constexpr (ACT == FL_ACT_GLU) load_eight<DT>(ry, at, y);
                 activate_all<ACT>(x, y);
-                store_wide<DT>(l.out, at + 32 * g, x);
+                store_eight<DT>(ro, at, x);
             }
+        }
+    }
+}
+
+// The columns behind the output's last whole eight, of which a lane of every row has
+// them: through the LDS, four to a thread.
+template <class T, int DT, int MI, int NI>
+__device__ __forceinline__ void store_edge(const Mx4LinearArgs &l, float *part, const f32x4_t (&acc)[MI][NI], char *lds,
+                                           int64_t m0, int64_t n0, int m, int n, int64_t m_left, int64_t n_left) {
+    constexpr int RUNS = 4 / T::GROUP;
+    f32x4_t *rows = reinterpret_cast<f32x4_t *>(lds);
+#pragma unroll
+    for (int g = 0; g < RUNS; ++g)
+        if (n + 32 * g < n_left && n + 32 * g + 8 > n_left)
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    f32x4_t v;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) v[t] = acc[mi][(4 * h + t) % NI][g * T::GROUP + (4 * h + t) / NI];
+                    rows[(m + mi * 16) * 2 + h] = v;
+                }
+    __syncthreads();
+    const int64_t n1 = n0 + n_left / 8 * 8;
+    for (int i = threadIdx.x; i < T::BM * 2; i += 64 * T::WAVES) {
+        const int64_t row = m0 + i / 2, col = n1 + i % 2 * 4;
+        if (i / 2 >= m_left || col >= l.N) continue;
+        float x[4] = {rows[i][0], rows[i][1], rows[i][2], rows[i][3]};
+        if (part) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < l.N) part[row * l.N + col + e] = x[e];
+        } else {
+            finish_columns<DT>(l, row, col, x);
         }
     }
 }
@@ -346,53 +393,20 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) mx4_tile_kernel(Mx4TileA
     // what follows is per lane and not to be computed before the loop and kept
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
-    const int d = lane & 15, q = lane >> 4, wm = t.wave / WN, wn = t.wave % WN;
+    const int m = t.wave / WN * (16 * MI) + (lane & 15), n = t.wave % WN * (16 * NI) + (lane >> 4) * 8;
+    const int64_t m_left = a.l.M - m0, n_left = a.l.N - n0;
     float *sums = a.parts > 1 ? a.part + (int64_t)part * a.l.M * a.l.N : nullptr;
-    if (m0 + T::BM <= a.l.M && n0 + T::BN <= a.l.N) {
-        const int64_t m1 = m0 + wm * (16 * MI) + d, n1 = n0 + wn * (16 * NI);
-        if (sums)
-            store_tile<T, DT, -1>(a.l, sums, acc, m1, n1, q);
-        else if (a.l.act == FL_ACT_NONE)
-            store_tile<T, DT, FL_ACT_NONE>(a.l, sums, acc, m1, n1, q);
-        else if (a.l.act == FL_ACT_RELU)
-            store_tile<T, DT, FL_ACT_RELU>(a.l, sums, acc, m1, n1, q);
-        else if (a.l.act == FL_ACT_GELU_TANH)
-            store_tile<T, DT, FL_ACT_GELU_TANH>(a.l, sums, acc, m1, n1, q);
-        else
-            store_tile<T, DT, FL_ACT_GLU>(a.l, sums, acc, m1, n1, q);
-        return;
-    }
-    // A tile across the output's edge: row by row through the stages' place, 16 MI / 2
-    // rows of every wave at a time, each wave its own.
-    constexpr int HALF = MI / 2, COLS = 16 * NI;
-    static_assert(T::WAVES * HALF * 16 * COLS * 4 <= T::LDS, "half a wave's tile fits its part of the LDS");
-    float *mine = reinterpret_cast<float *>(lds) + t.wave * (HALF * 16 * COLS);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int mi = 0; mi < HALF; ++mi)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int ni = 0; ni < NI; ++ni)
-                    mine[(mi * 16 + d) * COLS + T::wave_column(q, r, ni)] = acc[h * HALF + mi][ni][r];
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        for (int i = lane; i < HALF * 16 * COLS / 4; i += 64) {
-            const int row = i / (COLS / 4), col = i % (COLS / 4) * 4;
-            const int64_t m = m0 + wm * (16 * MI) + h * HALF * 16 + row, n = n0 + wn * COLS + col;
-            const f32x4_t v = *reinterpret_cast<const f32x4_t *>(mine + row * COLS + col);
-            float x[4] = {v[0], v[1], v[2], v[3]};
-            if (m >= a.l.M || n >= a.l.N) continue;
-            if (sums) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (n + e < a.l.N) sums[m * a.l.N + n + e] = x[e];
-            } else {
-                finish_columns<DT>(a.l, m, n, x);
-            }
-        }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
+    if (sums)
+        store_tile<T, DT, -1>(a.l, sums, acc, m0, n0, m, n, m_left, n_left);
+    else if (a.l.act == FL_ACT_NONE)
+        store_tile<T, DT, FL_ACT_NONE>(a.l, sums, acc, m0, n0, m, n, m_left, n_left);
+    else if (a.l.act == FL_ACT_RELU)
+        store_tile<T, DT, FL_ACT_RELU>(a.l, sums, acc, m0, n0, m, n, m_left, n_left);
+    else if (a.l.act == FL_ACT_GELU_TANH)
+        store_tile<T, DT, FL_ACT_GELU_TANH>(a.l, sums, acc, m0, n0, m, n, m_left, n_left);
+    else
+        store_tile<T, DT, FL_ACT_GLU>(a.l, sums, acc, m0, n0, m, n, m_left, n_left);
+    if (n_left < T::BN && n_left % 8) store_edge<T, DT>(a.l, sums, acc, lds, m0, n0, m, n, m_left, n_left);
 }
 
 // The sums of the parts in their order, then the epilogue: four columns to a thread.
