@@ -57,13 +57,14 @@ struct LinearPlan {
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b); }
 
-// The least estimated time, in us, of (measured at M 1 to 8192, N and K 1024 to
-// 21568; the estimates meet them to 10 to 25%):
-//   streaming   3.4 + 0.25 a round of the chip, 16 rows of A or B and 1024 values of K.  One token
-//               by 14336x4096: 7.7 us, tiles 33; 64 by 4096x14336: 17.5, tiles 19; 128 by
-//               14336x4096: 22, tiles 15.
+// The least estimated time, in us, of (the constants fitted to every shape's and
+// tile's times at 156 random sizes, M 1 to 8192, N and K 64 to 24576: what is
+// chosen takes 1.02 times the fastest's time in the mean, 1.20 at most):
+//   streaming   3, and a round of the chip 0.3 for each 16x16 of outputs and 0.25 for each
+//               16 rows of A or B and 1024 values of K.  One token by 14336x4096: 7.8 us,
+//               tiles 33; 64 by 4096x14336: 20, tiles 19; 128 by 14336x4096: 22, tiles 15.
 //   256x256     a round 8 + 1.75 a stage of 256 values of K.
-//   128x128     two to a CU: a round 4 + 1.24 a stage, 0.7 where they have a CU to
+//   128x128     two to a CU: a round 4 + 1.24 a stage, 2 + 0.65 where they have a CU to
 //               themselves.  512x21568x1024 16 us, 18 with 256x256; 8192x14336x4096 318
 //               and 265.
 //   parts of K  a join of 4, and the sums written and read at 5 TB/s: 128 by 4096x14336
@@ -81,9 +82,9 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
         for (int nt = 1; nt <= 4; nt *= 2) {
             if (mt == 4 && nt == 1) continue;                    // 2 by 2 has its products with fewer rows
             if ((mt > 1 && M <= 8 * mt) || (M <= 2 && nt > 1) || (M <= 4 && nt > 2)) continue;  // measured slower
-            const double x = ceil_div(N, 16 * nt) * ceil_div(M, 16 * mt) / 256;
+            const double rounds = ceil_div(ceil_div(N, 16 * nt) * ceil_div(M, 16 * mt), 256);
             const double rows = M < 16 * mt ? M / 16.0 : mt;  // of A, in units of 16
-            const double time = 3.4 + 0.25 * (x < 1 ? 1 : x) * (rows + nt) * K / 1024;
+            const double time = 3 + rounds * (0.3 * mt * nt + 0.25 * (rows + nt) * K / 1024);
             if (time < least) {
                 least = time;
                 p.shape = {mt, nt, 8};
@@ -101,7 +102,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
             if (v == fl::kMx4Tile256)
                 time += ceil_div(x, 256) * (8 + 1.75 * run);
             else
-                time += x <= 256 ? 4 + 0.7 * run : (x <= 460 ? 1 : x / 512 + 0.1) * (4 + 1.24 * run);
+                time += x <= 256 ? 2 + 0.65 * run : (x <= 460 ? 1 : x / 512 + 0.1) * (4 + 1.24 * run);
             if (time < least) {
                 least = time;
                 p.stream = false;
