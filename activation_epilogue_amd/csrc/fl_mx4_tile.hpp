@@ -8,10 +8,11 @@
 //     A copy costs by the lines it touches, 2 clocks each (a wave's copy of 64-byte
 //     pieces takes twice the time of 128-byte ones).
 //   * Scales are copied for four stages at a time, 32 bytes of each row (8 bytes of a
-//     row for every stage would touch as many lines as the codes do).  A last stage
-//     of fewer than 8 blocks goes by itself, after the others, with its scales
-//     gathered byte by byte and zeros behind them: what follows a row's scales in
-//     memory is the next row's, and may stand for NaN.
+//     row for every stage would touch as many lines as the codes do).  What follows
+//     a row's scales in memory is the next row's and may stand for NaN: bytes past
+//     the last block are cleared where a stage's scales are read.  The last one to four
+//     stages come first: what a copy cannot bring of the last rows' scales is put
+//     into its place before the loop (an outer loop around it for that: 8% slower).
 //   * A wave owns 16 MI x 16 NI outputs.  Operands of the next half stage are read
 //     while the matrix instructions of this one run, those of A into the registers
 //     whose row of products is done; the one barrier of a stage comes when its second
@@ -44,6 +45,17 @@ __device__ __forceinline__ void lds_copy16_if(uint32_t on, i32x4_t rsrc, uint32_
 __device__ __forceinline__ uint32_t add_now(uint32_t v, uint32_t step) {
     uint32_t r;
     asm volatile("v_add_u32 %0, %2, %1" : "=v"(r) : "v"(v), "s"(__builtin_amdgcn_readfirstlane(step)));
+    return r;
+}
+
+// a < b ? x : y of uniform values, without a branch.
+__device__ __forceinline__ int pick_less(int a, int b, int x, int y) {
+    int r;
+    asm("s_cmp_lt_i32 %1, %2\n\ts_cselect_b32 %0, %3, %4"
+        : "=s"(r)
+        : "s"(__builtin_amdgcn_readfirstlane(a)), "s"(__builtin_amdgcn_readfirstlane(b)),
+          "s"(__builtin_amdgcn_readfirstlane(x)), "s"(__builtin_amdgcn_readfirstlane(y))
+        : "scc");
     return r;
 }
 
@@ -88,6 +100,8 @@ struct Mx4Tile {
     struct Operands {
         u32x4_t a[MI], b[2][NI];     // b: of this half and the next
         uint32_t sa[MI], sb[2][NI];  // two bytes, the halves'; sb: of this stage and the next
+        uint32_t keep;               // their bits that are of blocks before the last
+        int next, ahead;             // the stages of K after this and after that
     };
 
     const Mx4LinearArgs &l;
@@ -115,8 +129,8 @@ struct Mx4Tile {
         vb = (uint32_t)column(wave * NB * 8 + (lane >> 3)) * pitch + chunk * 16;
         const int p = wave * NS * 32 + (lane >> 1);  // A's rows, then B's places
         const bool of_a = wave * NS * 32 < BM;
-        rs = of_a ? sgpr_rsrc(l.a_scales + m0 * l.blocks, (size_t)m_left * l.blocks)
-                  : sgpr_rsrc(l.b_scales + n0 * l.blocks, (size_t)n_left * l.blocks);
+        rs = of_a ? sgpr_rsrc(l.a_scales + m0 * l.blocks, (size_t)(l.M - m0) * l.blocks)
+                  : sgpr_rsrc(l.b_scales + n0 * l.blocks, (size_t)(l.N - n0) * l.blocks);
         vs = (uint32_t)(of_a ? p : column(p - BM)) * (uint32_t)l.blocks + piece() * 16;
         step_s = (uint32_t)(of_a ? 32 : 2) * (uint32_t)l.blocks;
         const int d = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
@@ -153,24 +167,8 @@ struct Mx4Tile {
     // rows or places, two accumulators, on).  The stage is in the lane's offset: 16 bytes
     // may pass the array's end, which only that is checked against.
     __device__ __forceinline__ void copy_scales(uint32_t on, int s, int t, int i) const {
-        const bool some = s * 8 + piece() * 16 < l.blocks;
-        const uint32_t v = add_now(vs, i * step_s + s * 8);
-        lds_copy16_if(on, rs, some ? v : kOob,
+        lds_copy16_if(on, rs, add_now(vs, i * step_s + s * 8),
                       lds_at(2 * STAGE + (t & 1) * SCALES + (wave * NS + i) * 1024));
-    }
-    // The scales of a last stage of fewer than 8 blocks, as a run's first.
-    __device__ __forceinline__ void gather_scales(int64_t m0, int64_t n0) const {
-        const int block = l.blocks / 8 * 8, n = l.blocks - block;
-        for (int p = threadIdx.x; p < BM + BN; p += 64 * WAVES) {
-            const int64_t row = p < BM ? m0 + p : n0 + column(p - BM);
-            const uint8_t *s = (p < BM ? l.a_scales : l.b_scales) + row * l.blocks + block;
-            const bool on = row < (p < BM ? l.M : l.N);
-            uint32_t w[2] = {0, 0};
-#pragma unroll
-            for (int b = 0; b < 8; ++b)
-                if (on && b < n) w[b / 4] |= (uint32_t)s[b] << (8 * (b % 4));
-            *reinterpret_cast<u32x2_t *>(lds + 2 * STAGE + p * 32 + fs(p) * 16) = u32x2_t{w[0], w[1]};
-        }
     }
     __device__ __forceinline__ u32x4_t read16(uint32_t off) const { return *reinterpret_cast<const u32x4_t *>(lds + off); }
     __device__ __forceinline__ u32x4_t read_a(int j, int h, int mi) const {
@@ -179,8 +177,27 @@ struct Mx4Tile {
     __device__ __forceinline__ u32x4_t read_b(int j, int h, int ni) const {
         return read16((j & 1) * STAGE + (fb_at ^ h * 16) + ni * 2048);
     }
-    __device__ __forceinline__ uint32_t read_scale(uint32_t at, int j, int i) const {
-        return *reinterpret_cast<const uint16_t *>(lds + (j >> 2 & 1) * SCALES + (j & 1) * 8 + (at ^ (j & 2) * 8) + i * 512);
+    // Four bytes of a copy of which one is past the array's end are zeros.  A row's last
+    // one to three scales where that is so (the last row's; one block: the last three's)
+    // are put in their places once stages s to s + 3, the first four of a run, have landed.
+    __device__ __forceinline__ void last_scales(int s, int64_t m0, int64_t n0) const {
+        for (int p = threadIdx.x; p < BM + BN; p += 64 * WAVES) {
+            const bool of_a = p < BM;
+            const int64_t row = of_a ? m0 + p : n0 + column(p - BM), left = (of_a ? l.M : l.N) - row;
+            if (left <= 0 || left * l.blocks >= (l.blocks & ~3) + 4) continue;
+            for (int b = l.blocks & ~3; b < l.blocks; ++b)
+                lds[2 * STAGE + p * 32 + ((b - s * 8) ^ fs(p) * 16)] =
+                    (char)(of_a ? l.a_scales : l.b_scales)[row * l.blocks + b];
+        }
+    }
+    // The bits of a lane's two scales in stage s of K that are of blocks.
+    __device__ __forceinline__ uint32_t kept(int s) const {
+        const int left = l.blocks - s * 8 - (lane >> 4) * 2;
+        return left >= 2 ? 0xffffu : left == 1 ? 0xffu : 0u;
+    }
+    __device__ __forceinline__ uint32_t read_scale(uint32_t at, int j, int i, uint32_t keep) const {
+        return keep &
+               *reinterpret_cast<const uint16_t *>(lds + (j >> 2 & 1) * SCALES + (j & 1) * 8 + (at ^ (j & 2) * 8) + i * 512);
     }
 
     // What this wave has asked for has landed and been read; then everybody's.
@@ -188,37 +205,52 @@ struct Mx4Tile {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
 
-    // A run of stages of whole blocks, or the last stage by itself.
-    __device__ __forceinline__ void run(f32x4_t (&acc)[MI][NI], int first, int stages, bool last, int64_t m0,
-                                        int64_t n0) const {
-        if (last) {
-            gather_scales(m0, n0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NS; ++i) copy_scales(1, first, 0, i);
+    // The stages of a run as they are computed: of more than four the last one to four as
+    // begin to 3, then the others from `first` on as 4 to end; behind them none of K.
+    struct Order {
+        int first, last, end, none;
+        __device__ __forceinline__ int stage(int j) const {
+            return pick_less(j, end, j + pick_less(j, 4, last, first - 4), none);
         }
+    };
+
+    // A run of stages.
+    __device__ __forceinline__ void run(f32x4_t (&acc)[MI][NI], int first, int stages, int64_t m0, int64_t n0) const {
+        const int four = (stages - 1) / 4, begin = four ? 3 - (stages - 1) % 4 : 0;
+        const Order r{first, first + four * 4 - begin, begin + stages, l.blocks};
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) copy(first, 0, i);
+        for (int i = 0; i < NS; ++i) copy_scales(1, r.last, 0, i);
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) copy(first + 1, 1, i);
+        for (int i = 0; i < NS; ++i) copy_scales(1, first, 1, i);
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) copy(r.stage(begin), begin, i);
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) copy(r.stage(begin + 1), begin + 1, i);
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(COPIES) : "memory");
+        if ((l.blocks & 3) && (first + stages) * 8 >= l.blocks && (m0 + BM + 2 >= l.M || n0 + BN + 2 >= l.N)) {
+            last_scales(r.last, m0, n0);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
         Operands o;
+        o.keep = kept(r.stage(begin));
+        o.next = r.stage(begin + 1);
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) {
-            o.b[0][ni] = read_b(0, 0, ni);
-            o.sb[0][ni] = read_scale(sb_at, 0, ni);
+            o.b[0][ni] = read_b(begin, 0, ni);
+            o.sb[0][ni] = read_scale(sb_at, begin, ni, o.keep);
         }
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi) {
-            o.a[mi] = read_a(0, 0, mi);
-            o.sa[mi] = read_scale(sa_at, 0, mi);
+            o.a[mi] = read_a(begin, 0, mi);
+            o.sa[mi] = read_scale(sa_at, begin, mi, o.keep);
         }
 #pragma unroll 1
-        for (int j = 0; j < stages; ++j) {
-            half<0, 0>(acc, o, j, first, stages);
-            half<1, 0>(acc, o, j, first, stages);
+        for (int j = begin; j < r.end; ++j) {
+            half<0, 0>(acc, o, j, r);
+            half<1, 0>(acc, o, j, r);
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni) o.sb[0][ni] = o.sb[1][ni];
+            o.next = o.ahead;
         }
         meet();  // the copies past the end
     }
@@ -231,25 +263,29 @@ struct Mx4Tile {
     // third, 2% faster than one after another.
     static constexpr int SLOTS = MI * NI, PACE = 2 * COPIES + NS <= SLOTS ? 2 : 1;  // products to a copy
     template <int H, int I>
-    __device__ __forceinline__ void half(f32x4_t (&acc)[MI][NI], Operands &o, int j, int first, int stages) const {
+    __device__ __forceinline__ void half(f32x4_t (&acc)[MI][NI], Operands &o, int j, const Order &r) const {
         if constexpr (I < SLOTS) {
             constexpr int mi = I / NI, ni = mi & 1 ? NI - 1 - I % NI : I % NI;
-            if constexpr (H == 1 && I == 0) meet();
+            if constexpr (H == 1 && I == 0) {
+                o.ahead = r.stage(j + 2);
+                meet();
+            }
             acc[mi][ni] = mfma_mx4(o.b[H][ni], o.a[mi], acc[mi][ni], o.sb[0][ni], o.sa[mi], H);
-            if constexpr (H == 1 && I % PACE == 0 && I / PACE < COPIES) copy(first + j + 2, j, I / PACE);
+            if constexpr (H == 1 && I % PACE == 0 && I / PACE < COPIES) copy(o.ahead, j, I / PACE);
             if constexpr (H == 1 && I >= SLOTS - NS)
-                copy_scales((j & 3) == 0 && j + 4 < stages, first + j + 4, (j >> 2) + 1, I - SLOTS + NS);
+                copy_scales((j & 3) == 0 && j && j + 4 < r.end, r.first + j, (j >> 2) + 1, I - SLOTS + NS);
+            if constexpr (H == 1 && I == 0) o.keep = kept(o.next);
             // B's operands first, all of them are needed at once; A's where their row is done
             if constexpr (I < NI) {
                 o.b[1 - H][I] = read_b(j + H, 1 - H, I);
-                if constexpr (H == 1) o.sb[1][I] = read_scale(sb_at, j + 1, I);
+                if constexpr (H == 1) o.sb[1][I] = read_scale(sb_at, j + 1, I, o.keep);
             }
             if constexpr (I % NI == NI - 1) {
                 o.a[mi] = read_a(j + H, 1 - H, mi);
-                if constexpr (H == 1) o.sa[mi] = read_scale(sa_at, j + 1, mi);
+                if constexpr (H == 1) o.sa[mi] = read_scale(sa_at, j + 1, mi, o.keep);
             }
             __builtin_amdgcn_sched_barrier(0);
-            half<H, I + 1>(acc, o, j, first, stages);
+            half<H, I + 1>(acc, o, j, r);
         }
     }
 };
@@ -386,10 +422,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) mx4_tile_kernel(Mx4TileA
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const T t(a.l, lds, m0, n0);
-    const int whole = (first + stages) * 8 > a.l.blocks ? stages - 1 : stages;
-#pragma unroll 1
-    for (int pass = whole > 0 ? 0 : 1; pass < (stages > whole ? 2 : 1); ++pass)
-        t.run(acc, pass ? first + whole : first, pass ? 1 : whole, pass, m0, n0);
+    t.run(acc, first, stages, m0, n0);
     // what follows is per lane and not to be computed before the loop and kept
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
