@@ -80,8 +80,8 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
     double least = 1e30;
     for (int mt = 1; mt <= 4 && M <= 512; mt *= 2)
         for (int nt = 1; nt <= 4; nt *= 2) {
-            if (mt == 4 && nt == 1) continue;                    // 2 by 2 has its products with fewer rows
-            if ((mt > 1 && M <= 8 * mt) || (M <= 2 && nt > 1) || (M <= 4 && nt > 2)) continue;  // measured slower
+            if (mt * nt == 4 && mt != nt) continue;  // 2 by 2 has their products with fewer rows
+            if ((mt > 1 && M <= 8 * mt) || (M <= 2 && nt > 1)) continue;  // measured slower
             const double rounds = ceil_div(ceil_div(N, 16 * nt) * ceil_div(M, 16 * mt), 256);
             const double rows = M < 16 * mt ? M / 16.0 : mt;  // of A, in units of 16
             const double time = 3 + rounds * (0.3 * mt * nt + 0.25 * (rows + nt) * K / 1024);

@@ -41,7 +41,6 @@ void launch_mx4_stream<FL_INST_DTYPE>(const Mx4StreamShape &shape, const Mx4Line
     if (shape.mt == m && shape.nt == n) return launch_stream_of<DT, m, n, 8, false>(a, st)
     FL_STREAM(1, 1);
     FL_STREAM(1, 2);
-    FL_STREAM(1, 4);
     FL_STREAM(2, 1);
     FL_STREAM(2, 2);
     FL_STREAM(2, 4);
