@@ -192,6 +192,49 @@ def test_larger(M, N, K):
     exact_case(M, N, K, 6, values=True, dtype=torch.float32)
 
 
+# Sizes at which each of the streaming kernel's shapes is the one that runs, both
+# tiles, and K in parts.
+@pytest.mark.parametrize("M,N,K", [(3, 1000, 2000), (9, 5001, 700), (257, 259, 100), (20, 2051, 130), (200, 1030, 65),
+                                   (200, 2051, 300), (33, 4099, 8200), (300, 2051, 4100), (600, 259, 4100),
+                                   (257, 4099, 8200), (3000, 5000, 65), (130, 16391, 8200), (513, 515, 16400)])
+def test_every_kernel(M, N, K):
+    exact_case(M, N, K, 7)
+    exact_case(M, N, K, 8, values=True)
+
+
+# A stage is 8 blocks of 32, scales come for four stages: every count of blocks in the
+# last of them, with the arrays' last bytes at every place in four.
+@pytest.mark.parametrize("blocks", list(range(1, 42)))
+def test_tiles_at_every_depth(blocks):
+    for M, N in ((1030, 514), (1025, 511), (1027, 385)):
+        exact_case(M, N, 32 * blocks - blocks % 3, blocks)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(700, 1, 64), (700, 7, 64), (700, 9, 64), (1030, 64, 64), (1030, 65, 64), (520, 127, 96),
+                                   (520, 777, 96), (700, 1030, 96), (3001, 5001, 65)])
+def test_rows_of_16_bits_at_any_address(M, N, K, dtype):
+    """Odd and even widths, from odd and even elements on; with a residual at another place, and over it."""
+    dt = DT[dtype]
+    a, b = bytes_of(M, K, 3, 1), bytes_of(N, K, 4, 1)
+    sums = values64(*a, K) @ values64(*b, K).t()
+    A, B = mx4(*a, K), mx4(*b, K)
+    R = torch.randint(-64, 65, (M, N), generator=torch.Generator().manual_seed(1)).to(dt)
+    want = sums.to(dt), (sums + R.double()).to(dt)  # exact in fp32 before they are rounded
+    for first in (8, 9, 10):
+        say("16-bit rows", M, N, K, dtype, first)
+        for residual in (False, True):
+            buf = torch.full((M * N + 64,), float("nan"), dtype=dt, device="cuda")
+            out = buf[first:first + M * N].view(M, N)
+            r = torch.empty(M * N + 1, dtype=dt, device="cuda")[1:].view(M, N).copy_(R) if residual else None
+            fl.fused_linear_mx4(A, B, act="none", out=out, R=r, dtype=dt)
+            assert torch.equal(out.cpu(), want[residual])
+            assert torch.isnan(buf[:first]).all() and torch.isnan(buf[first + M * N:]).all()
+        out.copy_(R)
+        fl.fused_linear_mx4(A, B, act="none", out=out, R=out, dtype=dt)
+        assert torch.equal(out.cpu(), want[1])
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu_tanh", "glu"])
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(1, 100, 300), (17, 257, 1000), (64, 64, 4096), (150, 333, 257), (520, 700, 640)])
@@ -305,6 +348,25 @@ def test_the_same_bits_again_on_another_stream_and_in_a_graph(M, N, K):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_two_streams_at_once():
+    """Two layers with a workspace each, at the same time and over and over."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    jobs = []
+    for M, N, K in ((64, 1030, 8000), (700, 1030, 777)):
+        x = torch.randn(M, K, generator=g, device="cuda").half()
+        W = fl.quantize_mx4(torch.randn(N, K, generator=g, device="cuda").half())
+        jobs.append((x, W, fl.fused_linear_mx4(x, W, act="relu"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = []
+        for x, W, _, s in jobs:
+            with torch.cuda.stream(s):
+                outs.append([fl.fused_linear_mx4(x, W, act="relu") for _ in range(3)])
+        torch.cuda.synchronize()
+        for (_, _, want, _), got in zip(jobs, outs):
+            assert all(torch.equal(t, want) for t in got)
 
 
 def test_offsets_past_32_bits():
