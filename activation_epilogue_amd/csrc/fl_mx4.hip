@@ -51,24 +51,35 @@ struct LinearPlan {
     bool stream, quantize;  // quantize: A's values first, into the workspace
     fl::Mx4StreamShape shape;
     int variant, parts, part_stages;
+    int64_t first_columns;  // of 256x256 tiles, the rest of 128x128 by another launch; 0: all of one size
     size_t codes, scales, sums;  // bytes of the workspace, in this order
 };
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b); }
 
-// The least estimated time, in us, of (the constants fitted to every shape's and
-// tile's times at 156 random sizes, M 1 to 8192, N and K 64 to 24576: what is
-// chosen takes 1.02 times the fastest's time in the mean, 1.20 at most):
+// Of the ways below the one of the least estimated time, in us (the constants fitted to
+// every shape's and tile's times at 156 random sizes, M 1 to 8192, N and K 64 to 24576:
+// what is chosen takes 1.02 times the fastest's time in the mean, 1.20 at most):
 //   streaming   3, and a round of the chip 0.3 for each 16x16 of outputs and 0.25 for each
-//               16 rows of A or B and 1024 values of K.  One token by 14336x4096: 7.8 us,
-//               tiles 33; 64 by 4096x14336: 20, tiles 19; 128 by 14336x4096: 22, tiles 15.
-//   256x256     a round 8 + 1.75 a stage of 256 values of K.
-//   128x128     two to a CU: a round 4 + 1.24 a stage, 2 + 0.65 where they have a CU to
-//               themselves.  512x21568x1024 16 us, 18 with 256x256; 8192x14336x4096 318
-//               and 265.
+//               16 rows of A or B and 1024 values of K.  One token by 14336x4096: 7.7 us,
+//               tiles 33; 64 by 4096x14336: 17.1, tiles 16.1; 128 by 14336x4096: 26, tiles
+//               16.
+//   256x256     3.4, and a round 8 + 1.75 a stage of 256 values of K.
+//   128x128     3.4, and two to a CU: a round 4 + 1.24 a stage, 2 + 0.65 where they have a
+//               CU to themselves.  4608x4096x4096 55 us, 63 with 256x256;
+//               8192x14336x4096 315 and 258.
+//   both        256x256 for whole rounds of the chip, 2 for a second launch of 128x128 for
+//               the columns behind them: 4096x4352x14336 152 us, 186 and 164 with one of
+//               them.
 //   parts of K  a join of 4, and the sums written and read at 5 TB/s: 128 by 4096x14336
-//               43 us in one part, 18.7 in 6.
+//               43 us in one part, 20 in 8.
+double tiles_time(int variant, double tiles, double stages) {
+    if (variant == fl::kMx4Tile256) return ceil_div(tiles, 256) * (8 + 1.75 * stages);
+    if (tiles <= 256) return 2 + 0.65 * stages;
+    return (tiles <= 460 ? 1 : tiles / 512 + 0.1) * (4 + 1.24 * stages);
+}
+
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
     LinearPlan p{};
     const int64_t blocks = blocks_of(K), stages = (blocks + 7) / 8;
@@ -98,11 +109,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
             const int64_t run = (stages + parts - 1) / parts;
             if (parts > 1 && (run < 2 || tiles * parts > 512 || (stages + run - 1) / run != parts)) continue;
             const double x = tiles * parts;
-            double time = 3.4 + (parts > 1 ? 4 + parts * (double)M * N * 8 / 5e6 : 0);
-            if (v == fl::kMx4Tile256)
-                time += ceil_div(x, 256) * (8 + 1.75 * run);
-            else
-                time += x <= 256 ? 2 + 0.65 * run : (x <= 460 ? 1 : x / 512 + 0.1) * (4 + 1.24 * run);
+            const double time = 3.4 + (parts > 1 ? 4 + parts * (double)M * N * 8 / 5e6 : 0) + tiles_time(v, x, run);
             if (time < least) {
                 least = time;
                 p.stream = false;
@@ -110,6 +117,20 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
                 p.parts = parts;
                 p.part_stages = (int)run;
             }
+        }
+    }
+    const int64_t down = (M + 255) / 256, across = (N + 255) / 256, rounds = down * across / 256;
+    const int64_t whole = rounds * 256 / down;  // columns of tiles that fill them
+    if (whole > 0 && whole < across) {
+        const double rest = ceil_div(M, 128) * ceil_div(N - whole * 256, 128);
+        const double time = 3.4 + tiles_time(fl::kMx4Tile256, whole * down, stages) + 2 +
+                            tiles_time(fl::kMx4Tile128, rest, stages);
+        if (time < least) {
+            p.stream = false;
+            p.variant = fl::kMx4Tile256;
+            p.parts = 1;
+            p.part_stages = (int)stages;
+            p.first_columns = whole * 256;
         }
     }
     // up to four rows every block quantises them faster than another launch does (4
@@ -145,14 +166,23 @@ void launch_linear(const LinearPlan &p, fl::Mx4LinearArgs l, uint8_t *ws, hipStr
         return;
     }
     fl::Mx4TileArgs a{};
-    const fl::Mx4TileShape &t = fl::kMx4TileShapes[p.variant];
     a.l = l;
     a.part = reinterpret_cast<float *>(ws + p.codes + p.scales);
     a.parts = p.parts;
     a.part_stages = p.part_stages;
-    a.tiles_m = (int)((l.M + t.bm - 1) / t.bm);
-    a.tiles_n = (int)((l.N + t.bn - 1) / t.bn);
-    fl::launch_mx4_tile<DT>(p.variant, a, st);
+    const auto launch = [&](int variant, int64_t from, int64_t to) {
+        const fl::Mx4TileShape &t = fl::kMx4TileShapes[variant];
+        a.n_from = from;
+        a.tiles_m = (int)((l.M + t.bm - 1) / t.bm);
+        a.tiles_n = (int)((to - from + t.bn - 1) / t.bn);
+        fl::launch_mx4_tile<DT>(variant, a, st);
+    };
+    if (p.first_columns) {
+        launch(p.variant, 0, p.first_columns);
+        launch(fl::kMx4Tile128, p.first_columns, l.N);
+    } else {
+        launch(p.variant, 0, l.N);
+    }
 }
 
 fl_status check_linear(int64_t M, int64_t N, int64_t K, int dtype) {

@@ -64,6 +64,7 @@ struct Mx4TileArgs {
     float *part;      // parts > 1: sums (parts, M, N)
     int parts;        // K is cut into this many runs of stages
     int part_stages;  // stages of a run
+    int64_t n_from;   // the first tile's column, of tiles_m x tiles_n
     int tiles_m, tiles_n;
 };
 
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) mx4_tile_kernel(Mx4TileA
     const int part = (int)(blockIdx.x / (unsigned)tiles), pid = (int)(blockIdx.x % (unsigned)tiles);
     int tm, tn;
     grouped_tile(xcd_logical(pid, tiles), a.tiles_m, a.tiles_n, 4, tm, tn);
-    const int64_t m0 = (int64_t)tm * T::BM, n0 = (int64_t)tn * T::BN;
+    const int64_t m0 = (int64_t)tm * T::BM, n0 = a.n_from + (int64_t)tn * T::BN;
     const int all = (a.l.blocks + 7) / 8, first = part * a.part_stages;
     const int stages = all - first < a.part_stages ? all - first : a.part_stages;
     f32x4_t acc[MI][NI];

@@ -193,10 +193,11 @@ def test_larger(M, N, K):
 
 
 # Sizes at which each of the streaming kernel's shapes is the one that runs, both
-# tiles, and K in parts.
+# tiles, K in parts, and tiles of both sizes.
 @pytest.mark.parametrize("M,N,K", [(3, 1000, 2000), (9, 5001, 700), (257, 259, 100), (20, 2051, 130), (200, 1030, 65),
                                    (200, 2051, 300), (33, 4099, 8200), (300, 2051, 4100), (600, 259, 4100),
-                                   (257, 4099, 8200), (3000, 5000, 65), (130, 16391, 8200), (513, 515, 16400)])
+                                   (257, 4099, 8200), (3000, 5000, 65), (130, 16391, 8200), (513, 515, 16400),
+                                   (4495, 11606, 65), (3331, 10282, 300)])
 def test_every_kernel(M, N, K):
     exact_case(M, N, K, 7)
     exact_case(M, N, K, 8, values=True)
@@ -212,7 +213,7 @@ def test_tiles_at_every_depth(blocks):
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(700, 1, 64), (700, 7, 64), (700, 9, 64), (1030, 64, 64), (1030, 65, 64), (520, 127, 96),
-                                   (520, 777, 96), (700, 1030, 96), (3001, 5001, 65)])
+                                   (520, 777, 96), (700, 1030, 96), (3001, 5001, 65), (4495, 11607, 65)])
 def test_rows_of_16_bits_at_any_address(M, N, K, dtype):
     """Odd and even widths, from odd and even elements on; with a residual at another place, and over it."""
     dt = DT[dtype]
