@@ -9,16 +9,17 @@ namespace {
 template <int DT, int MT, int NT, int WAVES, bool VALUES>
 void launch_stream_of(const Mx4LinearArgs &l, hipStream_t st) {
     // the largest panel whose scales (and codes of A's values) take 48 KB
-    const int64_t rows = VALUES ? l.M : 16 * MT;
+    const int64_t rows = VALUES ? l.M : 16 * MT, all = (l.blocks + 15) / 16 * 16;
     int64_t panel = 256;
+    auto code_pitch = [&](int64_t n) { return VALUES ? (n < all ? n : all) * 16 + 16 : 0; };
     auto bytes = [&](int64_t n) {
-        return 16 * NT * (n + kMx4ScalePad) + rows * (n + kMx4ScalePad) + (VALUES ? rows * n * 16 : 0);
+        return 16 * NT * (n + kMx4ScalePad) + rows * (n + kMx4ScalePad) + rows * code_pitch(n);
     };
     while (panel < l.blocks && bytes(panel + 256) <= 49152) panel += 256;
     const int64_t sums = (int64_t)WAVES * MT * NT * 1024, lds = bytes(panel) > sums ? bytes(panel) : sums;
     const dim3 grid((unsigned)(((l.N + 16 * NT - 1) / (16 * NT)) * ((l.M + 16 * MT - 1) / (16 * MT))));
     hipLaunchKernelGGL((mx4_stream_kernel<DT, MT, NT, WAVES, VALUES>), grid, dim3(64 * WAVES), (size_t)lds, st,
-                       Mx4StreamArgs{l, (int)panel});
+                       Mx4StreamArgs{l, (int)panel, (int)code_pitch(panel)});
 }
 
 template <int DT, int MI, int NI, int WM, int WN, int PER_CU>

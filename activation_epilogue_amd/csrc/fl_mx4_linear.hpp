@@ -119,7 +119,7 @@ __device__ __forceinline__ void finish_columns(const Mx4LinearArgs &a, int64_t m
 // A load costs by the lines it touches, so the scales, of which a step needs 8
 // bytes of each row, are brought into the LDS in whole rows first, `panel` blocks of K
 // at a time.  VALUES: A (MT = 1) is given as values; every block quantises them into
-// the LDS, which takes less than another launch while the rows are few.
+// the LDS, which takes less than another launch while they are few.
 //
 // Measured: one token by 14336x4096 fp16 with GELU 7.7 us, of which the launch takes 3
 // (31.3 MB, 6.7 TB/s of the rest: L2s and matrix cores wait for memory).  More rows are
@@ -130,7 +130,8 @@ constexpr int kMx4ScalePad = 16;  // rows of scales 16 bytes past a multiple of 
 
 struct Mx4StreamArgs {
     Mx4LinearArgs l;
-    int panel;  // blocks, a multiple of 256 (scales of 256 blocks: 256 bytes)
+    int panel;       // blocks, a multiple of 256 (scales of 256 blocks: 256 bytes)
+    int code_pitch;  // VALUES: bytes of a row of codes, 16 past whole pieces of 16 blocks: rows in different banks
 };
 
 template <int DT, int MT, int NT, int WAVES, bool VALUES>
@@ -198,22 +199,34 @@ __global__ void __launch_bounds__(64 * WAVES) mx4_stream_kernel(Mx4StreamArgs s)
         }
         if constexpr (VALUES) {
             // eight values to a thread, a block of 32 to four neighbours, up to whole pieces of 16 blocks
-            const int per_row = pieces * 64;
-            for (int i0 = 0; i0 < per_row * m_left; i0 += 64 * WAVES) {
-                const int i = i0 + threadIdx.x, row = i / per_row, unit = i - row * per_row;
-                const int64_t k = (int64_t)p0 * 32 + unit * 8;
-                RowValues<DT, 8> v;
-                v.load(a.a_raw, (m0 + row) * a.K + k, row < m_left ? a.K - k : 0);
-                uint32_t top = magnitude_bits<DT>(v.w[0]);
+            // (the loads of four at once)
+            constexpr int AHEAD = 4;
+            const int per_row = pieces * 64, all = per_row * m_left;
+            for (int i0 = 0; i0 < all; i0 += AHEAD * 64 * WAVES) {
+                RowValues<DT, 8> v[AHEAD];
 #pragma unroll
-                for (int e = 1; e < RowValues<DT, 8>::WORDS; ++e) top = larger_bits<DT>(top, magnitude_bits<DT>(v.w[e]));
-                top = larger_bits<DT>(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xb1, 0xf, 0xf, true));
-                top = larger_bits<DT>(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4e, 0xf, 0xf, true));
-                const uint32_t sc = scale_byte<DT>(top);
-                if (row >= m_left) continue;
-                *reinterpret_cast<uint32_t *>(a_codes + row * (s.panel * 16) + unit * 4) =
-                    sc == 255 ? 0 : codes8<DT>(v.w, scale_value(sc));
-                if ((unit & 3) == 0) a_scales[row * row_bytes + unit / 4] = (char)sc;
+                for (int u = 0; u < AHEAD; ++u) {
+                    if (i0 + u * 64 * WAVES >= all) break;
+                    const int i = i0 + u * 64 * WAVES + threadIdx.x, row = i / per_row, unit = i - row * per_row;
+                    const int64_t k = (int64_t)p0 * 32 + unit * 8;
+                    v[u].load(a.a_raw, (m0 + row) * a.K + k, row < m_left ? a.K - k : 0);
+                }
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    if (i0 + u * 64 * WAVES >= all) break;
+                    const int i = i0 + u * 64 * WAVES + threadIdx.x, row = i / per_row, unit = i - row * per_row;
+                    uint32_t top = magnitude_bits<DT>(v[u].w[0]);
+#pragma unroll
+                    for (int e = 1; e < RowValues<DT, 8>::WORDS; ++e)
+                        top = larger_bits<DT>(top, magnitude_bits<DT>(v[u].w[e]));
+                    top = larger_bits<DT>(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xb1, 0xf, 0xf, true));
+                    top = larger_bits<DT>(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4e, 0xf, 0xf, true));
+                    const uint32_t sc = scale_byte<DT>(top);
+                    if (row >= m_left) continue;
+                    *reinterpret_cast<uint32_t *>(a_codes + row * s.code_pitch + unit * 4) =
+                        sc == 255 ? 0 : codes8<DT>(v[u].w, scale_value(sc));
+                    if ((unit & 3) == 0) a_scales[row * row_bytes + unit / 4] = (char)sc;
+                }
             }
         }
         __syncthreads();
@@ -228,8 +241,8 @@ __global__ void __launch_bounds__(64 * WAVES) mx4_stream_kernel(Mx4StreamArgs s)
                 const int row = VALUES ? (d < m_left ? d : 0) : i * 16 + d;
                 sa[i] = *reinterpret_cast<const uint16_t *>(a_scales + row * row_bytes + at);
                 if constexpr (VALUES) {
-                    m[i][0] = *reinterpret_cast<const u32x4_t *>(a_codes + row * (s.panel * 16) + at * 16);
-                    m[i][1] = *reinterpret_cast<const u32x4_t *>(a_codes + row * (s.panel * 16) + at * 16 + 16);
+                    m[i][0] = *reinterpret_cast<const u32x4_t *>(a_codes + row * s.code_pitch + at * 16);
+                    m[i][1] = *reinterpret_cast<const u32x4_t *>(a_codes + row * s.code_pitch + at * 16 + 16);
                 }
             }
 #pragma unroll

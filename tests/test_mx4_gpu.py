@@ -211,6 +211,37 @@ def test_tiles_at_every_depth(blocks):
         exact_case(M, N, 32 * blocks - blocks % 3, blocks)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 50, 45000), (2, 3000, 8200), (5, 1000, 1000), (9, 257, 4000), (11, 5000, 3000),
+                                   (13, 130, 33), (16, 1000, 2800), (16, 1000, 2900), (16, 20000, 300)])
+def test_few_rows_of_values(M, N, K, dtype):
+    """In each block's own memory or by a launch of their own, over one run of K and over two."""
+    dt = DT[dtype]
+    x, b = some(M, K, dt, K), bytes_of(N, K, 2)
+    va, vb = values64(*quantize64(x), K), values64(*b, K)
+    out, buf = guarded(M, N, dt)
+    shifted = torch.empty(M * K + 1, dtype=dt, device="cuda")[1:].view(M, K).copy_(x)
+    say("few rows of values", M, N, K, dtype)
+    B = mx4(*b, K)
+    fl.fused_linear_mx4(shifted, B, act="none", out=out)
+    want, bound = linear64(va, vb, None, None, None, "none")
+    # fp16 ends at 65504: a value from half a step behind it on, 65520, rounds to an infinity, one whose
+    # bound reaches there may
+    far = torch.finfo(dt).max * (1 + torch.finfo(dt).eps / 4)
+    must, may = want.abs() - bound > far, want.abs() + bound >= far
+
+    def right(got):
+        got = got.cpu().double()
+        assert bool((got[must] == torch.copysign(torch.full_like(want, float("inf")), want)[must]).all())
+        return worst(torch.where(may, torch.zeros_like(want), got), torch.where(may, torch.zeros_like(want), want),
+                     bound, dt) <= 1.0
+    assert right(out)
+    assert torch.isnan(buf[:33]).all() and torch.isnan(buf[33 + M * N:]).all()
+    # codes given instead go another way to the same products
+    again = fl.fused_linear_mx4(fl.quantize_mx4(shifted), B, act="none", dtype=dt)
+    assert right(again)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(700, 1, 64), (700, 7, 64), (700, 9, 64), (1030, 64, 64), (1030, 65, 64), (520, 127, 96),
                                    (520, 777, 96), (700, 1030, 96), (3001, 5001, 65), (4495, 11607, 65)])
