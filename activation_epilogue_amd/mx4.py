@@ -56,16 +56,16 @@ def _ok(status):
         raise FusedLinearError(status, _lib().fl_mx4_last_error().decode())
 
 
-def _rows(q, name):
-    """(rows, K, blocks) of an Mx4 whose parts fit together."""
-    rows = _matrix(q.codes, f"{name}.codes")[0]
-    K = int(q.K)
+def _rows(q, name, like=None):
+    """(rows, K, pointers of codes and scales) of an Mx4 whose parts fit
+    together, on like's device."""
+    codes, K = q.codes, int(q.K)
+    rows = _matrix(codes, f"{name}.codes")[0]
     if K < 0:
         raise ValueError(f"{name}.K is negative")
     blocks = (K + 31) // 32
-    _ptr(q.codes, f"{name}.codes", torch.uint8, (rows, 16 * blocks))
-    _ptr(q.scales, f"{name}.scales", torch.uint8, (rows, blocks), q.codes)
-    return rows, K, blocks
+    return (rows, K, _ptr(codes, f"{name}.codes", torch.uint8, (rows, 16 * blocks), like),
+            _ptr(q.scales, f"{name}.scales", torch.uint8, (rows, blocks), codes))
 
 
 def quantize_mx4(X, transposed=False, out=None, *, stream=None):
@@ -89,12 +89,11 @@ def quantize_mx4(X, transposed=False, out=None, *, stream=None):
 
 def dequantize_mx4(q, dtype=torch.bfloat16, out=None, *, stream=None):
     """The values of q (rows,K) in dtype (fl_dequantize_mx4)."""
-    rows, K, _ = _rows(q, "q")
+    rows, K, codes, scales = _rows(q, "q")
     code = _code(dtype)
     with _On(q.codes, stream) as st:
         out = _out(out, "out", (rows, K), dtype, q.codes)
-        _ok(_lib().fl_dequantize_mx4(q.codes.data_ptr() or None, q.scales.data_ptr() or None, out.data_ptr() or None,
-                                     rows, K, code, st))
+        _ok(_lib().fl_dequantize_mx4(codes, scales, out.data_ptr() or None, rows, K, code, st))
     return out
 
 
@@ -116,18 +115,19 @@ def fused_linear_mx4(A, B, bias=None, Y=None, act="relu", out=None, *, R=None, d
     given).  out may be Y or R.  workspace: a device tensor of
     mx4_workspace_bytes(M, N, K, A is a matrix, dtype) bytes (allocated where it
     is needed and not given)."""
-    N, K, _ = _rows(B, "B")
     values = isinstance(A, torch.Tensor)
     if values:
         M, AK = _matrix(A, "A")
         dtype = dtype or A.dtype
         if dtype != A.dtype:
             raise TypeError(f"A has dtype {A.dtype}, expected {dtype}")
-        first = A
+        first, a_scales = A, None
+        a = _ptr(A, "A")
     else:
-        M, AK, _ = _rows(A, "A")
+        M, AK, a, a_scales = _rows(A, "A")
         dtype = dtype or torch.bfloat16
         first = A.codes
+    N, K, b, b_scales = _rows(B, "B", first)
     if AK != K:
         raise ValueError(f"A has rows of {AK} values and B of {K}")
     code = _code(dtype)
@@ -137,9 +137,7 @@ def fused_linear_mx4(A, B, bias=None, Y=None, act="relu", out=None, *, R=None, d
         if need and workspace is None:
             workspace = first.new_empty(need, dtype=torch.uint8)
         _ok(_lib().fl_fused_linear_mx4(
-            _ptr(first, "A"), None if values else A.scales.data_ptr() or None,
-            _ptr(B.codes, "B.codes", None, None, first), B.scales.data_ptr() or None,
-            _ptr(bias, "bias", dtype, (N,), first), _ptr(Y, "Y", dtype, (M, N), first),
+            a, a_scales, b, b_scales, _ptr(bias, "bias", dtype, (N,), first), _ptr(Y, "Y", dtype, (M, N), first),
             _ptr(R, "R", dtype, (M, N), first), out.data_ptr() or None, M, N, K, ACTS[act], code,
             _ptr(workspace, "workspace", None, None, first), _bytes(workspace), st))
     return out

@@ -51,7 +51,7 @@ def layer_norm(X, weight=None, bias=None, eps=1e-5, out=None, stats=False, mean=
     M, H = _matrix(X, "X")
     code = _code(X.dtype)
     with _On(X, stream) as st:
-        out = _out(out, "out", (M, H), X.dtype, X)
+        out = torch.empty_like(X) if out is None else _out(out, "out", (M, H), X.dtype, X)
         if stats:
             mean = _out(mean, "mean", (M,), torch.float32, X)
             rstd = _out(rstd, "rstd", (M,), torch.float32, X)
@@ -87,7 +87,7 @@ def layer_norm_bwd(dout, X, mean, rstd, weight=None, R=None, dX=None, dweight=Tr
     code = _code(dt)
     need = layer_norm_bwd_workspace_bytes(M, H, code)
     with _On(dout, stream) as st:
-        dX = _out(dX, "dX", (M, H), dt, dout)
+        dX = torch.empty_like(dout) if dX is None else _out(dX, "dX", (M, H), dt, dout)
         sums = []
         for name, t in (("dweight", dweight), ("dbias", dbias)):
             sums.append(None if t is None or t is False else
