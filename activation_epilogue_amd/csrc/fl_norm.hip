@@ -31,7 +31,9 @@ void launch_fwd(const fl::NormArgs &a, hipStream_t st) {
 // The smallest team whose lanes hold the row in 16 to 64 bytes each, 128 where it
 // takes many: rows of 1024 bf16 take 11.6 us with 64 lanes and 21.4 with 256
 // (16384 rows), of 2048 21.9 and 22.9, of 4096 40.6 and 38.6; 256 columns 11.6 with 16
-// lanes, 19.5 with 64 (65536 rows).
+// lanes, 19.5 with 64 (65536 rows).  Few rows do not fill the chip, and a lane's share
+// is what they wait for: 1725 bf16 take 3.0 us with 256 lanes and 3.6 with 64 (8 to 256
+// rows), 4.3 and 4.2 (1024).
 template <int DT>
 void launch_fwd_dt(const fl::NormArgs &a, hipStream_t st) {
     const int64_t p = pieces_of(a.H, DT);
@@ -43,6 +45,8 @@ void launch_fwd_dt(const fl::NormArgs &a, hipStream_t st) {
         launch_fwd<DT, 64, 1>(a, st);
     else if (p <= 128)
         launch_fwd<DT, 64, 2>(a, st);
+    else if (p <= 256 && a.M <= 512)
+        launch_fwd<DT, 256, 1>(a, st);
     else if (p <= 256)
         launch_fwd<DT, 64, 4>(a, st);
     else if (p <= 512)
@@ -60,12 +64,15 @@ void launch_fwd_dt(const fl::NormArgs &a, hipStream_t st) {
 
 // The team of the backward kernel, and its blocks where they keep sums: each
 // leaves a row of partial sums (8 H bytes), so no more of them than are resident
-// at once (16384x4096 bf16: 103 us with 512, 129 with 256, 111 with 1024; teams of
-// 1024 lanes 119 us with 256 at 8192x8192, 130 with 512).  Few rows go one to a
-// team all the same: 512x4096 14 us, 17 with four to a team.  The sums of a lane
-// take two registers an element, so teams are larger than the forward's: 2048
-// columns 55 us with 256 lanes, 66 with 64; 8192 columns 119 us with 1024 lanes, 129
-// with 256; but 512 columns 29 us with 64 lanes, 75 with 256.
+// at once (16384x4096 bf16: 512 or, of 1024 lanes, 256), half as many where a team has
+// fewer than four rows (1024x4096 bf16 13 us, 18 with 512 blocks; 4096x1000 9.6, 11.1),
+// and a block for a team's row each where they are fewer still (512x4096 11.4 us).  The
+// rows of two blocks are left to one, and those of three, which needs no join: 4x4096
+// bf16 7.3 us, 8.2 with it, 6x4096 8.7 and 8.2, and 3.4 of the host's time.
+// The sums of a lane take two registers an element, so teams are larger than the
+// forward's: 2048 columns 55 us with 256 lanes, 66 with 64; 512 columns 29 us with 64
+// lanes, 75 with 256.  Up to 2048 rows of 216 bf16 take 64 lanes with half of the sums each
+// (128 rows 5.5 us, 7.0 with 16 lanes; 2048: 6.5, 7.7; 8192: 9.2, 8.4).
 struct BwdShape {
     int team, nv, blocks;  // team 0: the long kernels
 };
@@ -73,7 +80,7 @@ struct BwdShape {
 BwdShape bwd_shape(int64_t M, int64_t H, int dtype) {
     const int64_t p = pieces_of(H, dtype);
     BwdShape b{};
-    if (p <= 32)
+    if (p <= 16 || (p <= 32 && M > 2048))
         b = {16, p <= 16 ? 1 : 2, 0};
     else if (p <= 128)
         b = {64, p <= 64 ? 1 : 2, 0};
@@ -85,7 +92,7 @@ BwdShape bwd_shape(int64_t M, int64_t H, int dtype) {
         b = {1024, 4, 0};
     const int64_t rows = b.team && b.team < 512 ? 512 / b.team : 1;  // of a block at once
     const int64_t blocks = (M + rows - 1) / rows, most = b.team == 1024 ? kBwdBlocks / 2 : kBwdBlocks;
-    b.blocks = (int)(blocks < most ? (blocks > 1 ? blocks : 1) : most);
+    b.blocks = blocks <= 3 ? 1 : (int)(blocks < most / 2 ? blocks : blocks < most * 4 ? most / 2 : most);
     return b;
 }
 

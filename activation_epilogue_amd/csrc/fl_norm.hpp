@@ -420,6 +420,9 @@ __global__ void __launch_bounds__(TEAM > 512 ? TEAM : 512) layer_norm_bwd_kernel
         }
     }
     if constexpr (SUMS) {
+        // 16 bytes to a lane: element by element, lanes lie 32 bytes apart and each of their
+        // stores meets a line of its own (1x16384 bf16 5.5 us, 17.3 so; 8192x8192 91, 97)
+        typedef float four_t __attribute__((ext_vector_type(4), aligned(4)));
         float *to[2] = {a.dweight, a.dbias};
         if (gridDim.x > 1)
             for (int k = 0; k < 2; ++k) to[k] = a.part + ((int64_t)blockIdx.x * 2 + k) * a.H;
@@ -428,32 +431,40 @@ __global__ void __launch_bounds__(TEAM > 512 ? TEAM : 512) layer_norm_bwd_kernel
 #pragma unroll
             for (int n = 0; n < NV; ++n)
 #pragma unroll
-                for (int t = 0; t < VEC; ++t) {
-                    const int i = (n * TEAM + x) * VEC + t;
-                    if (i < whole && to[0]) to[0][i] = sw[n][t];
-                    if (i < whole && to[1]) to[1][i] = sb[n][t];
-                }
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int h = 0; h < VEC / 4; ++h) {
+                        const float(&v)[VEC] = k ? sb[n] : sw[n];
+                        const int i = (n * TEAM + x) * VEC + h * 4;
+                        if (i < whole && to[k])
+                            *reinterpret_cast<four_t *>(to[k] + i) = four_t{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+                    }
             if (at.one != kOob && to[0]) to[0][whole + x] = sw1;
             if (at.one != kOob && to[1]) to[1][whole + x] = sb1;
         } else {
-            __shared__ float sums[TEAMS][TEAM * VEC];
+            constexpr int QUADS = VEC / 4;
+            __shared__ __align__(16) f32x4_t sums[2][QUADS][TEAMS][TEAM];
 #pragma unroll
-            for (int n = 0; n < NV; ++n)
+            for (int n = 0; n < NV; ++n) {
+                if (n) __syncthreads();
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    __syncthreads();
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int t = 0; t < VEC; ++t) sums[team][t * TEAM + x] = k ? sb[n][t] : sw[n][t];
-                    __syncthreads();
-                    for (int c = threadIdx.x; c < TEAM * VEC; c += THREADS) {
-                        const int i = n * TEAM * VEC + c;
-                        float v = sums[0][c % VEC * TEAM + c / VEC];
-                        for (int m = 1; m < TEAMS; ++m) v += sums[m][c % VEC * TEAM + c / VEC];
-                        if (i < whole && to[k]) to[k][i] = v;
+                    for (int h = 0; h < QUADS; ++h) {
+                        const float(&v)[VEC] = k ? sb[n] : sw[n];
+                        sums[k][h][team][x] = f32x4_t{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
                     }
+                __syncthreads();
+                for (int c = threadIdx.x; c < 2 * QUADS * TEAM; c += THREADS) {
+                    const int k = c / (QUADS * TEAM), h = c / TEAM % QUADS, l = c % TEAM;
+                    const int i = (n * TEAM + l) * VEC + h * 4;
+                    f32x4_t v = sums[k][h][0][l];
+                    for (int m = 1; m < TEAMS; ++m) v += sums[k][h][m][l];
+                    if (i < whole && to[k]) *reinterpret_cast<four_t *>(to[k] + i) = four_t{v[0], v[1], v[2], v[3]};
                 }
+            }
             if (at.tail) {
-                float *one = &sums[0][0];  // (2, teams, VEC)
+                float *one = reinterpret_cast<float *>(sums);  // (2, teams, VEC)
                 __syncthreads();
                 if (x < VEC) {
                     one[team * VEC + x] = sw1;
