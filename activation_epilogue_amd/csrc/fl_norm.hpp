@@ -16,10 +16,11 @@
 // sums, which column_join_kernel adds in a fixed order: no atomics.
 //
 // Measured, 16384x4096 bf16: forward 38.6 us (7.0 TB/s of the 268 MB, some of
-// which the last-level cache serves), backward with a residual 103 us (5.2 TB/s of
+// which the last-level cache serves), backward with a residual 102 us (5.3 TB/s of
 // 537 MB; 89 us, 6.0 TB/s, without the weight's and bias's sums: their 16 MB of
 // partial sums written and read and one more launch are the rest).  Outputs that
-// pass the L2 by: forward 40.6 -> 42.6 us without.
+// pass the L2 by: forward 40.6 -> 42.6 us without.  The next row's loads ahead of
+// this one's sums: no gain (8192x8192 114 us both) or worse (102 -> 128: the registers).
 //
 // Pieces are read and written 16 bytes wide whatever the rows' alignment (the
 // hardware takes any that suits the elements); what is left behind the last
