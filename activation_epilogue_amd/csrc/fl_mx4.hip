@@ -76,7 +76,7 @@ double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b);
 //               43 us in one part, 20 in 8.
 double tiles_time(int variant, double tiles, double stages) {
     if (variant == fl::kMx4Tile256) return ceil_div(tiles, 256) * (8 + 1.75 * stages);
-    if (tiles <= 256) return 2 + 0.65 * stages;
+    if (variant == fl::kMx4Tile128Alone) return tiles <= 256 ? 2 + 0.35 * stages : 1e9;
     return (tiles <= 460 ? 1 : tiles / 512 + 0.1) * (4 + 1.24 * stages);
 }
 

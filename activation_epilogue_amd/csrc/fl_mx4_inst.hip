@@ -22,10 +22,12 @@ void launch_stream_of(const Mx4LinearArgs &l, hipStream_t st) {
                        Mx4StreamArgs{l, (int)panel, (int)code_pitch(panel)});
 }
 
-template <int DT, int MI, int NI, int WM, int WN, int PER_CU>
+template <int DT, int MI, int NI, int WM, int WN, int PER_CU, int RING>
 void launch_tile(const Mx4TileArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL((mx4_tile_kernel<DT, MI, NI, WM, WN, PER_CU>),
-                       dim3((unsigned)(a.tiles_m * a.tiles_n) * (unsigned)a.parts), dim3(64 * WM * WN), 0, st, a);
+    constexpr size_t lds = Mx4Tile<DT, MI, NI, WM, WN, RING>::LDS;
+    hipLaunchKernelGGL((mx4_tile_kernel<DT, MI, NI, WM, WN, PER_CU, RING>),
+                       dim3((unsigned)(a.tiles_m * a.tiles_n) * (unsigned)a.parts), dim3(64 * WM * WN),
+                       lds, st, a);
 }
 
 }  // namespace
@@ -54,9 +56,11 @@ template <>
 void launch_mx4_tile<FL_INST_DTYPE>(int variant, const Mx4TileArgs &a, hipStream_t st) {
     constexpr int DT = FL_INST_DTYPE;
     if (variant == kMx4Tile256)
-        launch_tile<DT, 8, 4, 2, 4, 1>(a, st);
+        launch_tile<DT, 8, 4, 2, 4, 1, 2>(a, st);
+    else if (variant == kMx4Tile128)
+        launch_tile<DT, 4, 4, 2, 2, 2, 2>(a, st);
     else
-        launch_tile<DT, 4, 4, 2, 2, 2>(a, st);
+        launch_tile<DT, 4, 4, 2, 2, 2, 4>(a, st);
     if (a.parts > 1) {
         const int64_t quads = (a.l.N + 3) / 4 * a.l.M;
         hipLaunchKernelGGL((mx4_join_kernel<DT>), dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, a);

@@ -9,10 +9,10 @@
 //     pieces takes twice the time of 128-byte ones).
 //   * Scales are copied for four stages at a time, 32 bytes of each row (8 bytes of a
 //     row for every stage would touch as many lines as the codes do).  What follows
-//     a row's scales in memory is the next row's and may stand for NaN: bytes past
-//     the last block are cleared where a stage's scales are read.  The last one to four
-//     stages come first: what a copy cannot bring of the last rows' scales is put
-//     into its place before the loop (an outer loop around it for that: 8% slower).
+//     a row's scales in memory is the next row's and may stand for NaN.  The last one to
+//     four stages come first, so that the bytes behind the last block are cleared
+//     before the loop (where a stage's scales are read, the wait for them to be cleared
+//     takes 8% of the time; an outer loop around it as much).
 //   * A wave owns 16 MI x 16 NI outputs.  Operands of the next half stage are read
 //     while the matrix instructions of this one run, those of A into the registers
 //     whose row of products is done; the one barrier of a stage comes when its second
@@ -82,15 +82,18 @@ struct Mx4TileArgs {
     int tiles_m, tiles_n;
 };
 
-template <int DT, int MI, int NI, int WM, int WN, int PER_CU>
+template <int DT, int MI, int NI, int WM, int WN, int RING>
 struct Mx4Tile {
     static constexpr int WAVES = WM * WN, BM = 16 * MI * WM, BN = 16 * NI * WN;
     static constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128, SCALES = (BM + BN) * 32;
-    static constexpr int LDS = 2 * (STAGE + SCALES);                // two stages, the scales of twice four
+    static constexpr int LDS = RING * STAGE + 2 * SCALES;           // RING stages, the scales of twice four
     static constexpr int NA = BM / 8 / WAVES, NB = BN / 8 / WAVES;  // copies of a wave and stage
     static constexpr int NS = (BM + BN) / 32 / WAVES;               // and of four stages' scales
     static constexpr int COPIES = NA + NB;
+    // of a stage's copies those that go out in a second half, the rest in the half behind it
+    static constexpr int FIRST = RING > 2 ? COPIES / 2 : COPIES;
     static_assert(NA * 8 * WAVES == BM && NB * 8 * WAVES == BN, "whole copies");
+    static_assert((RING & (RING - 1)) == 0, "a stage's place is its number's low bits");
 
     // A 16-byte read is served 16 lanes at a time, lanes 0-3, 12-15 and 20-27 first
     // (measured): eight rows of a chunk c and the eight others of chunk c + 2.  Rows
@@ -115,8 +118,7 @@ struct Mx4Tile {
     struct Operands {
         u32x4_t a[MI], b[2][NI];     // b: of this half and the next
         uint32_t sa[MI], sb[2][NI];  // two bytes, the halves'; sb: of this stage and the next
-        uint32_t keep;               // their bits that are of blocks before the last
-        int next, ahead;             // the stages of K after this and after that
+        int ahead;                   // the stage of K behind the ring
     };
 
     const Mx4LinearArgs &l;
@@ -151,8 +153,8 @@ struct Mx4Tile {
         const int d = lane & 15, q = lane >> 4, wm = wave / WN, wn = wave % WN;
         fa_at = (wm * MI * 16 + d) * 128 + (2 * q ^ fa(d)) * 16;
         fb_at = A_BYTES + (wn * NI * 16 + d) * 128 + (2 * q ^ fa(d)) * 16;
-        sa_at = 2 * STAGE + (wm * MI * 16 + d) * 32 + fs(d) * 16 + 2 * q;
-        sb_at = 2 * STAGE + (BM + wn * NI * 16 + d) * 32 + fs(d) * 16 + 2 * q;
+        sa_at = RING * STAGE + (wm * MI * 16 + d) * 32 + fs(d) * 16 + 2 * q;
+        sb_at = RING * STAGE + (BM + wn * NI * 16 + d) * 32 + fs(d) * 16 + 2 * q;
     }
 
     // Which 16 bytes of a row's scales the lane copies.
@@ -171,11 +173,11 @@ struct Mx4Tile {
         const uint32_t v = i < NA ? add_now(va, i * 8 * pitch) : add_now(vb, ((i - NA & 1) * 16 + (i - NA) / 2) * pitch);
         if (i < NA) {
             lds_copy16(ra, on ? v : kOob, (uint32_t)s * 128,
-                       lds_at((j & 1) * STAGE + (wave * NA + i) * 1024));
+                       lds_at((j & RING - 1) * STAGE + (wave * NA + i) * 1024));
         } else {
             const int k = i - NA;
             lds_copy16(rb, on ? v : kOob, (uint32_t)s * 128,
-                       lds_at((j & 1) * STAGE + A_BYTES + (wave * NB + k) * 1024));
+                       lds_at((j & RING - 1) * STAGE + A_BYTES + (wave * NB + k) * 1024));
         }
     }
     // Copy i of a wave of the scales of stages s to s + 3, the t-th four of a run (32
@@ -183,41 +185,41 @@ struct Mx4Tile {
     // may pass the array's end, which only that is checked against.
     __device__ __forceinline__ void copy_scales(uint32_t on, int s, int t, int i) const {
         lds_copy16_if(on, rs, add_now(vs, i * step_s + s * 8),
-                      lds_at(2 * STAGE + (t & 1) * SCALES + (wave * NS + i) * 1024));
+                      lds_at(RING * STAGE + (t & 1) * SCALES + (wave * NS + i) * 1024));
     }
     __device__ __forceinline__ u32x4_t read16(uint32_t off) const { return *reinterpret_cast<const u32x4_t *>(lds + off); }
     __device__ __forceinline__ u32x4_t read_a(int j, int h, int mi) const {
-        return read16((j & 1) * STAGE + (fa_at ^ h * 16) + mi * 2048);
+        return read16((j & RING - 1) * STAGE + (fa_at ^ h * 16) + mi * 2048);
     }
     __device__ __forceinline__ u32x4_t read_b(int j, int h, int ni) const {
-        return read16((j & 1) * STAGE + (fb_at ^ h * 16) + ni * 2048);
+        return read16((j & RING - 1) * STAGE + (fb_at ^ h * 16) + ni * 2048);
     }
-    // Four bytes of a copy of which one is past the array's end are zeros.  A row's last
-    // one to three scales where that is so (the last row's; one block: the last three's)
-    // are put in their places once stages s to s + 3, the first four of a run, have landed.
+    // The scales of the last stage, of n < 8 blocks, once stages s to s + 3, the first four of
+    // a run, have landed.  What follows them is the next row's and becomes zeros.  Four bytes
+    // of a copy that pass the array's end did not come: a row's last one to three
+    // where that is so (the last row's; one block: the last three's) are read here.
     __device__ __forceinline__ void last_scales(int s, int64_t m0, int64_t n0) const {
+        const int n = l.blocks & 7, block = l.blocks - n;
         for (int p = threadIdx.x; p < BM + BN; p += 64 * WAVES) {
             const bool of_a = p < BM;
             const int64_t row = of_a ? m0 + p : n0 + column(p - BM), left = (of_a ? l.M : l.N) - row;
-            if (left <= 0 || left * l.blocks >= (l.blocks & ~3) + 4) continue;
-            for (int b = l.blocks & ~3; b < l.blocks; ++b)
-                lds[2 * STAGE + p * 32 + ((b - s * 8) ^ fs(p) * 16)] =
-                    (char)(of_a ? l.a_scales : l.b_scales)[row * l.blocks + b];
+            const bool cut = left > 0 && left * l.blocks < (l.blocks & ~3) + 4;
+            uint64_t *at = reinterpret_cast<uint64_t *>(lds + RING * STAGE + p * 32 + ((block - s * 8) ^ fs(p) * 16));
+            uint64_t w = *at & ((1ull << (cut ? n & ~3 : n) * 8) - 1);
+            for (int b = n & ~3; b < n && cut; ++b)
+                w |= (uint64_t)(of_a ? l.a_scales : l.b_scales)[row * l.blocks + block + b] << b * 8;
+            *at = w;
         }
     }
-    // The bits of a lane's two scales in stage s of K that are of blocks.
-    __device__ __forceinline__ uint32_t kept(int s) const {
-        const int left = l.blocks - s * 8 - (lane >> 4) * 2;
-        return left >= 2 ? 0xffffu : left == 1 ? 0xffu : 0u;
-    }
-    __device__ __forceinline__ uint32_t read_scale(uint32_t at, int j, int i, uint32_t keep) const {
-        return keep &
-               *reinterpret_cast<const uint16_t *>(lds + (j >> 2 & 1) * SCALES + (j & 1) * 8 + (at ^ (j & 2) * 8) + i * 512);
+    __device__ __forceinline__ uint32_t read_scale(uint32_t at, int j, int i) const {
+        return *reinterpret_cast<const uint16_t *>(lds + (j >> 2 & 1) * SCALES + (j & 1) * 8 + (at ^ (j & 2) * 8) + i * 512);
     }
 
-    // What this wave has asked for has landed and been read; then everybody's.
+    // What this wave has asked for, but for the last AHEAD copies, has landed and been read;
+    // then everybody's.
+    template <int AHEAD>
     __device__ __forceinline__ static void meet() {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(AHEAD) : "memory");
     }
 
     // The stages of a run as they are computed: of more than four the last one to four as
@@ -238,26 +240,25 @@ struct Mx4Tile {
 #pragma unroll
         for (int i = 0; i < NS; ++i) copy_scales(1, first, 1, i);
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) copy(r.stage(begin), begin, i);
+        for (int j = 0; j < RING; ++j)
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) copy(r.stage(begin + 1), begin + 1, i);
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(COPIES) : "memory");
-        if ((l.blocks & 3) && (first + stages) * 8 >= l.blocks && (m0 + BM + 2 >= l.M || n0 + BN + 2 >= l.N)) {
+            for (int i = 0; i < (j < RING - 1 ? COPIES : FIRST); ++i) copy(r.stage(begin + j), begin + j, i);
+        meet<(RING - 2) * COPIES + FIRST>();
+        if ((l.blocks & 7) && (first + stages) * 8 >= l.blocks) {
             last_scales(r.last, m0, n0);
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         }
         Operands o;
-        o.keep = kept(r.stage(begin));
-        o.next = r.stage(begin + 1);
+        o.ahead = r.stage(begin + RING - 1);
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) {
             o.b[0][ni] = read_b(begin, 0, ni);
-            o.sb[0][ni] = read_scale(sb_at, begin, ni, o.keep);
+            o.sb[0][ni] = read_scale(sb_at, begin, ni);
         }
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi) {
             o.a[mi] = read_a(begin, 0, mi);
-            o.sa[mi] = read_scale(sa_at, begin, mi, o.keep);
+            o.sa[mi] = read_scale(sa_at, begin, mi);
         }
 #pragma unroll 1
         for (int j = begin; j < r.end; ++j) {
@@ -265,39 +266,39 @@ struct Mx4Tile {
             half<1, 0>(acc, o, j, r);
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni) o.sb[0][ni] = o.sb[1][ni];
-            o.next = o.ahead;
         }
-        meet();  // the copies past the end
+        meet<0>();  // the copies past the end
     }
 
     // The matrix instructions of half H of stage j, row by row of the wave's blocks, and
     // between them the operand reads of the half after it; in the second half also the
-    // next stage's scales, the copies of stage j + 2 and, in the first NS of four
+    // next stage's scales, the copies of stage j + RING and, in the first NS of four
     // stages, a copy of the scales of the next four.  The rows go forth and back:
     // neighbours share an operand.  Copies every second product measured the same as every
     // third, 2% faster than one after another.
-    static constexpr int SLOTS = MI * NI, PACE = 2 * COPIES + NS <= SLOTS ? 2 : 1;  // products to a copy
+    static constexpr int SLOTS = MI * NI, PACE = (SLOTS - NS) / FIRST < 3 ? (SLOTS - NS) / FIRST : 3;  // products to a copy
     template <int H, int I>
     __device__ __forceinline__ void half(f32x4_t (&acc)[MI][NI], Operands &o, int j, const Order &r) const {
         if constexpr (I < SLOTS) {
             constexpr int mi = I / NI, ni = mi & 1 ? NI - 1 - I % NI : I % NI;
             if constexpr (H == 1 && I == 0) {
-                o.ahead = r.stage(j + 2);
-                meet();
+                o.ahead = r.stage(j + RING);
+                meet<(RING - 2) * COPIES>();
             }
             acc[mi][ni] = mfma_mx4(o.b[H][ni], o.a[mi], acc[mi][ni], o.sb[0][ni], o.sa[mi], H);
-            if constexpr (H == 1 && I % PACE == 0 && I / PACE < COPIES) copy(o.ahead, j, I / PACE);
+            if constexpr (H == 1 && I % PACE == 0 && I / PACE < FIRST) copy(o.ahead, j, I / PACE);
+            if constexpr (H == 0 && I % PACE == 0 && FIRST + I / PACE < COPIES)
+                copy(o.ahead, j + RING - 1, FIRST + I / PACE);
             if constexpr (H == 1 && I >= SLOTS - NS)
                 copy_scales((j & 3) == 0 && j && j + 4 < r.end, r.first + j, (j >> 2) + 1, I - SLOTS + NS);
-            if constexpr (H == 1 && I == 0) o.keep = kept(o.next);
             // B's operands first, all of them are needed at once; A's where their row is done
             if constexpr (I < NI) {
                 o.b[1 - H][I] = read_b(j + H, 1 - H, I);
-                if constexpr (H == 1) o.sb[1][I] = read_scale(sb_at, j + 1, I, o.keep);
+                if constexpr (H == 1) o.sb[1][I] = read_scale(sb_at, j + 1, I);
             }
             if constexpr (I % NI == NI - 1) {
                 o.a[mi] = read_a(j + H, 1 - H, mi);
-                if constexpr (H == 1) o.sa[mi] = read_scale(sa_at, j + 1, mi, o.keep);
+                if constexpr (H == 1) o.sa[mi] = read_scale(sa_at, j + 1, mi);
             }
             __builtin_amdgcn_sched_barrier(0);
             half<H, I + 1>(acc, o, j, r);
@@ -464,10 +465,10 @@ __device__ __forceinline__ void store_edge(const Mx4LinearArgs &l, float *part, 
     }
 }
 
-template <int DT, int MI, int NI, int WM, int WN, int PER_CU>
+template <int DT, int MI, int NI, int WM, int WN, int PER_CU, int RING>
 __global__ void __launch_bounds__(64 * WM * WN, PER_CU) mx4_tile_kernel(Mx4TileArgs a) {
-    using T = Mx4Tile<DT, MI, NI, WM, WN, PER_CU>;
-    __shared__ __align__(1024) char lds[T::LDS];
+    using T = Mx4Tile<DT, MI, NI, WM, WN, RING>;
+    extern __shared__ __align__(1024) char lds[];  // T::LDS
     const int tiles = a.tiles_m * a.tiles_n;
     const int part = (int)(blockIdx.x / (unsigned)tiles), pid = (int)(blockIdx.x % (unsigned)tiles);
     int tm, tn;
@@ -524,11 +525,11 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4TileArgs a) {
 }
 
 // The kernels of one type (fl_mx4_inst.hip).
-enum { kMx4Tile256, kMx4Tile128, kMx4Tiles };
+enum { kMx4Tile256, kMx4Tile128, kMx4Tile128Alone, kMx4Tiles };
 struct Mx4TileShape {
     int bm, bn;
 };
-constexpr Mx4TileShape kMx4TileShapes[kMx4Tiles] = {{256, 256}, {128, 128}};
+constexpr Mx4TileShape kMx4TileShapes[kMx4Tiles] = {{256, 256}, {128, 128}, {128, 128}};
 struct Mx4StreamShape {
     int mt, nt, waves;  // 16 mt rows by 16 nt columns to a block of this many waves
 };
