@@ -66,9 +66,10 @@ double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b);
 //               tiles 33; 64 by 4096x14336: 17.1, tiles 16.1; 128 by 14336x4096: 26, tiles
 //               16.
 //   256x256     3.4, and a round 8 + 1.75 a stage of 256 values of K.
-//   128x128     3.4, and two to a CU: a round 4 + 1.24 a stage, 2 + 0.65 where they have a
-//               CU to themselves.  4608x4096x4096 55 us, 63 with 256x256;
-//               8192x14336x4096 315 and 258.
+//   128x128     3.4, and two to a CU: a round 4 + 1.24 a stage.  4608x4096x4096 55 us, 63
+//               with 256x256; 8192x14336x4096 312 and 256.  Up to 256 of them, which have a
+//               CU to themselves, of eight waves with four stages under way: 2 + 0.52 a
+//               stage (128 by 14336x4096 13.7 us, 14.9 as the others are).
 //   both        256x256 for whole rounds of the chip, 2 for a second launch of 128x128 for
 //               the columns behind them: 4096x4352x14336 152 us, 186 and 164 with one of
 //               them.
@@ -76,9 +77,12 @@ double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b);
 //               43 us in one part, 20 in 8.
 double tiles_time(int variant, double tiles, double stages) {
     if (variant == fl::kMx4Tile256) return ceil_div(tiles, 256) * (8 + 1.75 * stages);
-    if (variant == fl::kMx4Tile128Alone) return tiles <= 256 ? 2 + 0.35 * stages : 1e9;
+    if (variant == fl::kMx4Tile128Alone) return 2 + 0.52 * stages;
     return (tiles <= 460 ? 1 : tiles / 512 + 0.1) * (4 + 1.24 * stages);
 }
+
+// The 128x128 tile of so many.
+int small_tile(double tiles) { return tiles <= 256 ? fl::kMx4Tile128Alone : fl::kMx4Tile128; }
 
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
     LinearPlan p{};
@@ -102,13 +106,14 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
             }
         }
     if (p.shape.mt == 1 && p.shape.nt == 1 && N <= 256 * 16) p.shape.waves = 16;  // a block to a CU
-    for (int v = 0; v < fl::kMx4Tiles; ++v) {
-        const fl::Mx4TileShape &t = fl::kMx4TileShapes[v];
+    for (int size : {fl::kMx4Tile256, fl::kMx4Tile128}) {
+        const fl::Mx4TileShape &t = fl::kMx4TileShapes[size];
         const double tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
         for (int parts = 1; parts <= 16; ++parts) {
             const int64_t run = (stages + parts - 1) / parts;
             if (parts > 1 && (run < 2 || tiles * parts > 512 || (stages + run - 1) / run != parts)) continue;
             const double x = tiles * parts;
+            const int v = size == fl::kMx4Tile256 ? size : small_tile(x);
             const double time = 3.4 + (parts > 1 ? 4 + parts * (double)M * N * 8 / 5e6 : 0) + tiles_time(v, x, run);
             if (time < least) {
                 least = time;
@@ -122,9 +127,9 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
     const int64_t down = (M + 255) / 256, across = (N + 255) / 256, rounds = down * across / 256;
     const int64_t whole = rounds * 256 / down;  // columns of tiles that fill them
     if (whole > 0 && whole < across) {
-        const double rest = ceil_div(M, 128) * ceil_div(N - whole * 256, 128);
+        const double rest = ceil_div(M, 128) * ceil_div(N - whole * 256, 128);  // of the small ones
         const double time = 3.4 + tiles_time(fl::kMx4Tile256, whole * down, stages) + 2 +
-                            tiles_time(fl::kMx4Tile128, rest, stages);
+                            tiles_time(small_tile(rest), rest, stages);
         if (time < least) {
             p.stream = false;
             p.variant = fl::kMx4Tile256;
@@ -183,7 +188,9 @@ void launch_linear(const LinearPlan &p, fl::Mx4LinearArgs l, uint8_t *ws, hipStr
     };
     if (p.first_columns) {
         launch(p.variant, 0, p.first_columns);
-        launch(fl::kMx4Tile128, p.first_columns, l.N);
+        const fl::Mx4TileShape &t = fl::kMx4TileShapes[fl::kMx4Tile128];
+        const double rest = ceil_div(l.M, t.bm) * ceil_div(l.N - p.first_columns, t.bn);
+        launch(small_tile(rest), p.first_columns, l.N);
     } else {
         launch(p.variant, 0, l.N);
     }

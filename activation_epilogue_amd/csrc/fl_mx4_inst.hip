@@ -60,7 +60,7 @@ void launch_mx4_tile<FL_INST_DTYPE>(int variant, const Mx4TileArgs &a, hipStream
     else if (variant == kMx4Tile128)
         launch_tile<DT, 4, 4, 2, 2, 2, 2>(a, st);
     else
-        launch_tile<DT, 4, 4, 2, 2, 2, 4>(a, st);
+        launch_tile<DT, 2, 4, 4, 2, 1, 4>(a, st);
     if (a.parts > 1) {
         const int64_t quads = (a.l.N + 3) / 4 * a.l.M;
         hipLaunchKernelGGL((mx4_join_kernel<DT>), dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, a);

@@ -4,7 +4,8 @@
 //   * A stage is 256 values of K: 128 bytes of codes of each of the tile's rows of
 //     A and of B, copied straight into the LDS (16 bytes a lane), 8 chunks to a row
 //     with chunk c of row r at c ^ fa(r), so that an operand read asks no bank
-//     twice.  Two stages are held: while one is computed the copies of the next land.
+//     twice.  Two stages are held, or four (RING): while one is computed the copies of
+//     the others land.
 //     A copy costs by the lines it touches, 2 clocks each (a wave's copy of 64-byte
 //     pieces takes twice the time of 128-byte ones).
 //   * Scales are copied for four stages at a time, 32 bytes of each row (8 bytes of a
@@ -260,6 +261,14 @@ struct Mx4Tile {
             o.a[mi] = read_a(begin, 0, mi);
             o.sa[mi] = read_scale(sa_at, begin, mi);
         }
+        // Words here, not 16 bits and zeros: the compiler would keep the 16 bits over the loop, and
+        // put zeros to all of them, and wait for all of them, at its start.  lgkmcnt(0): what it
+        // knows to be under way here it waits for in every stage.
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) asm volatile("" : "+v"(o.sa[mi]));
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) asm volatile("" : "+v"(o.sb[0][ni]));
+        __builtin_amdgcn_s_waitcnt(0xc07f);
 #pragma unroll 1
         for (int j = begin; j < r.end; ++j) {
             half<0, 0>(acc, o, j, r);
@@ -524,7 +533,7 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4TileArgs a) {
     finish_columns<DT>(a.l, m, n, x);
 }
 
-// The kernels of one type (fl_mx4_inst.hip).
+// The kernels of one type (fl_mx4_inst.hip); Alone: on a CU each.
 enum { kMx4Tile256, kMx4Tile128, kMx4Tile128Alone, kMx4Tiles };
 struct Mx4TileShape {
     int bm, bn;
