@@ -63,8 +63,8 @@ double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b);
 // what is chosen takes 1.02 times the fastest's time in the mean, 1.20 at most):
 //   streaming   3, and a round of the chip 0.3 for each 16x16 of outputs and 0.25 for each
 //               16 rows of A or B and 1024 values of K.  One token by 14336x4096: 7.7 us,
-//               tiles 33; 64 by 4096x14336: 17.1, tiles 16.1; 128 by 14336x4096: 26, tiles
-//               16.
+//               tiles 33; 64 by 4096x14336: 17.1, tiles 14.9; 128 by 14336x4096: 26, tiles
+//               13.7.
 //   256x256     3.4, and a round 8 + 1.75 a stage of 256 values of K.
 //   128x128     3.4, and two to a CU: a round 4 + 1.24 a stage.  4608x4096x4096 55 us, 63
 //               with 256x256; 8192x14336x4096 312 and 256.  Up to 256 of them, which have a

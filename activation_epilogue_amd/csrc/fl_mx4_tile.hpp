@@ -24,13 +24,13 @@
 //     and with them the four lanes of a row: 16-byte stores of 64 bytes in a row,
 //     straight from the accumulators.
 //
-// Measured, bf16 from codes: 8192x8192x8192 255 us, 4.3 PFLOP/s; 8192x14336x4096 262
-// us, with GELU 272.  The matrix cores alone, products of random codes out of registers,
-// reach 6.4 at the 1.7 GHz that their power leaves.  A stage of 256x256 takes 1.75 us
+// Measured, bf16 from codes: 8192x8192x8192 246 us, 4.5 PFLOP/s; 8192x14336x4096 256
+// us, with GELU 262.  The matrix cores alone, products of random codes out of registers,
+// reach 6.4 at the 1.7 GHz that their power leaves.  A stage of 256x256 takes 1.7 us
 // of which its 2048 clocks of products would take 1.25; its operand reads have the LDS
 // busy for 1200 clocks (a sixth of them conflicts) and its copies for another 512, and a
-// copy's lines take 1024 on their way.  Without the copies the first case took 209 us,
-// without the reads as well 193.  A tile's own time, 8 us, is mostly its output, which
+// copy's lines take 1024 on their way.  Without the copies the first case took 209 us (of
+// 255 then), without the reads as well 193.  A tile's own time, 8 us, is mostly its output, which
 // all CUs write at once (33.5 MB, 6 us): workgroups that go from tile to tile and
 // fetch the next one's first stages before that were slower (306 us against 287), as were
 // touching lines ahead for the L2 (337 against 275), a ring of four halves of a stage,
