@@ -139,7 +139,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
         }
     }
     // Few values every block quantises for itself, which is less than another launch's 2.9 us
-    // while 0.06 us for 1024 values past 3072, more where a CU has several blocks, are (16 by
+    // while 0.06 us for 1024 values past three times that, more where a CU has several blocks, are (16 by
     // 1024x1024 bf16 4.4 us, 6.6 with the launch; 8 by 4096x4096 6.0, 7.0; 12: 7.3, 7.3; 4 by
     // 14336x4096 9.4, 10.8; 8: 11.5, 11.1).
     const double on_a_cu = N > 4096 ? N / 4096.0 : 1;
