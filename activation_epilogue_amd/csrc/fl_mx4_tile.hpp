@@ -17,8 +17,8 @@
 //   * A wave owns 16 MI x 16 NI outputs.  Operands of the next half stage are read
 //     while the matrix instructions of this one run, those of A into the registers
 //     whose row of products is done; the one barrier of a stage comes when its second
-//     half is in registers: behind it the stage's place is free for the copies of
-//     the stage after next.
+//     half is in registers: behind it the stage's place is free for the copies of a
+//     later one.
 //   * The rows of B are placed so that the eight results that a lane has of an output
 //     row in NI accumulators (two elements of four, one of eight) are neighbours,
 //     and with them the four lanes of a row: 16-byte stores of 64 bytes in a row,
