@@ -69,7 +69,8 @@ fl_status fl_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, void *X
  *            is given as values.
  *   workspace  fl_mx4_workspace_bytes(M, N, K, A as values, dtype) bytes, 16-byte
  *            aligned (may be NULL when that is 0); written and read by this
- *            call's launches only.
+ *            call's launches only, so calls (and captured graphs) that may run at the
+ *            same time need one each.
  * K == 0 gives act(bias + R); M == 0 or N == 0 writes nothing.  256 rows of
  * codes, of A as values and of out must each span less than 2 GiB.
  */

@@ -18,7 +18,8 @@
  *              zero costs no digits beyond those of x - mean itself.
  *   Values     a row that holds an infinity or a NaN gives NaN throughout
  *              that row and touches no other; so does a row of equal values
- *              with eps 0 (0 * infinity).
+ *              with eps 0 (0 * infinity).  Sums and squares past fp32's range are
+ *              infinities: rows of fp32 values above 2^63 or so.
  *   Alignment  pointers aligned to their elements (workspace: 16 bytes); any H.
  *   Errors     fl_status as in fused_linear.h; the message of the last failed
  *              call of this header is read with fl_norm_last_error().
@@ -54,7 +55,8 @@ fl_status fl_layer_norm(const void *X, const void *weight, const void *bias, voi
  *   dweight, dbias  (H,) fp32, each or NULL; overwritten, zeros where M == 0.
  *   workspace  fl_layer_norm_bwd_workspace_bytes(M, H, dtype) bytes, 16-byte
  *           aligned (may be NULL when that is 0); written and read by this
- *           call's launches only.
+ *           call's launches only, so calls (and captured graphs) that may run at the
+ *           same time need one each.
  */
 fl_status fl_layer_norm_bwd(const void *dY, const void *X, const void *weight, const float *mean, const float *rstd,
                             const void *R, void *dX, float *dweight, float *dbias, int64_t M, int64_t H,

@@ -149,6 +149,31 @@ def test_in_place(H):
         assert got[0] is args[name] and all(torch.equal(p, q) for p, q in zip(got, want))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [1, 5, 100, 3000])
+@pytest.mark.parametrize("H", [5, 64, 216, 217, 1000, 1725, 4099, 9001, 16385, 33001])
+def test_sums_where_they_belong(H, M, dtype):
+    """The weight's and bias's gradients at any address of a float, nothing around them, and each alone."""
+    if M * H > 2 ** 24:
+        M = 300
+    dt = DT[dtype]
+    x, w, _, dy, _ = rows(M, H, dt, H)
+    x, w, dy = x.cuda(), w.cuda(), dy.cuda()
+    say("gradients' places", M, H, dtype)
+    _, mean, rstd = fl.layer_norm(x, w, stats=True)
+    (dw, wbuf), (db, bbuf) = guarded(H, dtype=torch.float32), guarded(H, dtype=torch.float32)
+    fl.layer_norm_bwd(dy, x, mean, rstd, w, dweight=dw, dbias=db)
+    untouched(wbuf, H)
+    untouched(bbuf, H)
+    _, dw64, db64, (_, e_w, e_b) = backward64(dy.cpu(), x.cpu(), mean.cpu(), rstd.cpu(), w.cpu(), None)
+    inside(dw, dw64, e_w)
+    inside(db, db64, e_b)
+    _, one, none = fl.layer_norm_bwd(dy, x, mean, rstd, w, dbias=False)
+    assert none is None and torch.equal(one, dw)
+    _, none, one = fl.layer_norm_bwd(dy, x, mean, rstd, w, dweight=False)
+    assert none is None and torch.equal(one, db)
+
+
 def test_gradients_against_differences():
     """The loss sum(dy * y): its slope along each direction, by differences in
     64 bits of the formula, is what the gradients say."""
