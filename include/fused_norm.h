@@ -19,7 +19,7 @@
  *   Values     a row that holds an infinity or a NaN gives NaN throughout
  *              that row and touches no other; so does a row of equal values
  *              with eps 0 (0 * infinity).  Sums and squares past fp32's range are
- *              infinities: rows of fp32 values above 2^63 or so.
+ *              infinities (rows of fp32 or bf16 values above 2^63 or so).
  *   Alignment  pointers aligned to their elements (workspace: 16 bytes); any H.
  *   Errors     fl_status as in fused_linear.h; the message of the last failed
  *              call of this header is read with fl_norm_last_error().
