@@ -290,6 +290,19 @@ def test_against_64_bits(M, N, K, dtype, act):
         assert torch.isnan(buf[:33]).all() and torch.isnan(buf[33 + M * N:]).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 70, 100001), (130, 150, 100033), (1, 40, 600011)])
+def test_long_rows(M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(K)
+    a, b = (torch.randn(n, K, generator=g, device="cuda") for n in (M, N))
+    say("long rows", M, N, K)
+    A, B = fl.quantize_mx4(a), fl.quantize_mx4(b)
+    va, vb = (values64(q.codes.cpu(), q.scales.cpu(), K) for q in (A, B))
+    want, bound = linear64(va, vb, None, None, None, "none")
+    for src in (A, a):
+        out = fl.fused_linear_mx4(src, B, act="none", dtype=torch.float32)
+        assert worst(out.cpu(), want, bound, torch.float32) <= 1.0
+
+
 @pytest.mark.parametrize("M,N,K", [(4, 40, 96), (64, 200, 520), (300, 280, 257), (1100, 1300, 257)])
 @pytest.mark.parametrize("values", [False, True])
 def test_nan_stays_in_its_row_and_column(M, N, K, values):
