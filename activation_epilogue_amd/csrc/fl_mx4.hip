@@ -10,13 +10,23 @@ namespace {
 
 int64_t blocks_of(int64_t K) { return (K + 31) / 32; }
 
+// Whether four lanes share a block's 32 rows: where that many lanes do not fill the chip a
+// lane's share is what is waited for (bf16 7 rows of 373: 5.6 us, 15.7 with one lane to a
+// block; 2247 of 2091: 9.8, 22.0; 4096 of 2048: 5.5, 7.7; 4096 of 4096: 9.4, 9.0; 14336 of
+// 4096: 27.5, 26.1).  A launch has 65535 blocks in its second dimension.
+bool split_columns(const fl::Mx4Args &a) { return a.rows * a.blocks <= 3 << 17 && a.blocks <= 2 * 65535; }
+
 template <int DT>
 void launch_quantize(const fl::Mx4Args &a, bool transposed, hipStream_t st) {
     if (transposed) {
         const int64_t per_block = 32 * (DT == FL_F32 ? 4 : 8);
-        hipLaunchKernelGGL((fl::quantize_mx4_transposed_kernel<DT>),
-                           dim3((unsigned)((a.rows + per_block - 1) / per_block), (unsigned)((a.blocks + 7) / 8)),
-                           dim3(256), 0, st, a);
+        const unsigned across = (unsigned)((a.rows + per_block - 1) / per_block);
+        if (split_columns(a))
+            hipLaunchKernelGGL((fl::quantize_mx4_transposed_kernel<DT, 4>), dim3(across, (unsigned)((a.blocks + 1) / 2)),
+                               dim3(256), 0, st, a);
+        else
+            hipLaunchKernelGGL((fl::quantize_mx4_transposed_kernel<DT, 1>), dim3(across, (unsigned)((a.blocks + 7) / 8)),
+                               dim3(256), 0, st, a);
     } else {
         const int64_t units = a.rows * a.blocks * 4, per_block = 256 * fl::kMx4Units;
         hipLaunchKernelGGL((fl::quantize_mx4_kernel<DT>), dim3((unsigned)((units + per_block - 1) / per_block)),

@@ -154,19 +154,20 @@ __global__ void __launch_bounds__(256) quantize_mx4_kernel(Mx4Args a) {
 // from neighbouring rows.  The eight lanes of a group take neighbouring blocks, so
 // a wave reads whole lines of 128 bytes and writes each column's codes as whole
 // lines too: nothing passes through the LDS.  8192x4096 bf16 15.9 us (5.3 TB/s), fp32
-// 36 (4.2); rows of 1537 fp16, whose pieces start at any multiple of 2 bytes, 1.2 TB/s.
-template <int DT>
+// 36 (4.2).  SPLIT 4: four neighbouring lanes share a block's rows, for matrices that
+// would fill few waves (4097 rows of 1537 fp16 7.4 us, 2.2 TB/s; 15.0 with one lane).
+template <int DT, int SPLIT>
 __global__ void __launch_bounds__(256) quantize_mx4_transposed_kernel(Mx4Args a) {
     using P = RowValues<DT, 16 / Io<DT>::size>;
-    constexpr int VEC = P::VEC;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int VEC = P::VEC, ROWS = 32 / SPLIT;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, part = lane % SPLIT;
     const int64_t col0 = ((int64_t)blockIdx.x * 32 + wave * 8 + (lane >> 3)) * VEC;
-    const int block = (int)blockIdx.y * 8 + (lane & 7);
+    const int block = (int)blockIdx.y * (8 / SPLIT) + (lane & 7) / SPLIT;
     if (col0 >= a.rows || block >= a.blocks) return;
-    P v[32];
+    P v[ROWS];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-        const int64_t at = (int64_t)block * 32 + k;
+    for (int k = 0; k < ROWS; ++k) {
+        const int64_t at = (int64_t)block * 32 + part * ROWS + k;
         v[k].load(a.x, at * a.rows + col0, at < a.K ? a.rows - col0 : 0);
     }
     uint32_t m[4];
@@ -174,7 +175,11 @@ __global__ void __launch_bounds__(256) quantize_mx4_transposed_kernel(Mx4Args a)
     for (int e = 0; e < 4; ++e) {
         m[e] = magnitude_bits<DT>(v[0].w[e]);
 #pragma unroll
-        for (int k = 1; k < 32; ++k) m[e] = larger_bits<DT>(m[e], magnitude_bits<DT>(v[k].w[e]));
+        for (int k = 1; k < ROWS; ++k) m[e] = larger_bits<DT>(m[e], magnitude_bits<DT>(v[k].w[e]));
+        if constexpr (SPLIT == 4) {  // lanes 1 and 2 apart
+            m[e] = larger_bits<DT>(m[e], (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m[e], 0xb1, 0xf, 0xf, true));
+            m[e] = larger_bits<DT>(m[e], (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m[e], 0x4e, 0xf, 0xf, true));
+        }
     }
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
@@ -182,10 +187,10 @@ __global__ void __launch_bounds__(256) quantize_mx4_transposed_kernel(Mx4Args a)
         const int e = DT == FL_F32 ? j : j / 2;
         const uint32_t s = scale_byte<DT>(DT == FL_F32 ? m[e] : high ? m[e] >> 16 : m[e] & 0xffffu);
         if (col0 + j >= a.rows) break;
-        u32x4_t c{0, 0, 0, 0};
+        uint32_t c[ROWS / 8] = {};
         if (s != 255) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {  // eight values along K at a time
+            for (int g = 0; g < ROWS / 8; ++g) {  // eight values along K at a time
                 uint32_t w[8];
 #pragma unroll
                 for (int t = 0; t < (DT == FL_F32 ? 8 : 4); ++t) {
@@ -198,8 +203,12 @@ __global__ void __launch_bounds__(256) quantize_mx4_transposed_kernel(Mx4Args a)
                 c[g] = codes8<DT>(w, scale_value(s));
             }
         }
-        *reinterpret_cast<u32x4_t *>(a.codes + ((col0 + j) * a.blocks + block) * 16) = c;
-        a.scales[(col0 + j) * a.blocks + block] = (uint8_t)s;
+        uint8_t *to = a.codes + ((col0 + j) * a.blocks + block) * 16;
+        if constexpr (SPLIT == 4)
+            *reinterpret_cast<uint32_t *>(to + part * 4) = c[0];
+        else
+            *reinterpret_cast<u32x4_t *>(to) = u32x4_t{c[0], c[1], c[2], c[3]};
+        if (part == 0) a.scales[(col0 + j) * a.blocks + block] = (uint8_t)s;
     }
 }
 

@@ -77,6 +77,25 @@ def test_quantize(rows, K, dtype):
         assert torch.isnan(buf[:33]).all() and torch.isnan(buf[33 + rows * K:]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,K", [(1030, 1500), (12288, 1024), (12289, 1024), (4100, 3100), (200001, 33), (393217, 5),
+                                    (1, 4200001), (3, 4194241)])
+def test_columns_as_rows(rows, K, dtype):
+    """Many columns, by one lane to a block and by four, to the bits of the rows they become."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, K, generator=g, device="cuda") * torch.exp2(torch.randint(-9, 9, (rows, 1), generator=g, device="cuda"))
+    x = x.to(DT[dtype])
+    say("columns as rows", rows, K, dtype)
+    want = fl.quantize_mx4(x)
+    blocks = (K + 31) // 32
+    codes, cbuf = among(torch.zeros(rows, 16 * blocks, dtype=torch.uint8), 1024)
+    scales, sbuf = among(torch.zeros(rows, blocks, dtype=torch.uint8), 1025)
+    fl.quantize_mx4(x.t().contiguous(), transposed=True, out=fl.Mx4(codes, scales, K))
+    assert torch.equal(codes, want.codes) and torch.equal(scales, want.scales)
+    assert (cbuf[:1024] == FF).all() and (cbuf[1024 + codes.numel():] == FF).all()
+    assert (sbuf[:1025] == FF).all() and (sbuf[1025 + scales.numel():] == FF).all()
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_every_value(dtype):
     """All finite 16-bit values in blocks of their neighbours, and each below a
