@@ -69,15 +69,16 @@ size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b); }
 
 // Of the ways below the one of the least estimated time, in us (the constants fitted to
-// every shape's and tile's times at 156 random sizes, M 1 to 8192, N and K 64 to 24576:
-// what is chosen takes 1.02 times the fastest's time in the mean, 1.20 at most):
+// every shape's and tile's times at 270 random sizes, M 1 to 8192, N and K 64 to 24576;
+// at 100 others what is chosen takes the fastest's time in the mean, 1.14 times it at most):
 //   streaming   3, and a round of the chip 0.3 for each 16x16 of outputs and 0.25 for each
 //               16 rows of A or B and 1024 values of K.  One token by 14336x4096: 7.7 us,
 //               tiles 33; 64 by 4096x14336: 17.1, tiles 14.9; 128 by 14336x4096: 26, tiles
 //               13.7.
-//   256x256     3.4, and a round 8 + 1.75 a stage of 256 values of K.
-//   128x128     3.4, and two to a CU: a round 4 + 1.24 a stage.  4608x4096x4096 55 us, 63
-//               with 256x256; 8192x14336x4096 312 and 256.  Up to 256 of them, which have a
+//   256x256     3.4, and a round 7.5 + 1.62 a stage of 256 values of K.
+//   128x128     3.4, and two to a CU: a round 4.3 + 1.24 a stage, a part of one a third
+//               more than its share and not under 0.54.  4608x4096x4096 55 us, 63 with
+//               256x256; 8192x14336x4096 312 and 256.  Up to 256 of them, which have a
 //               CU to themselves, of eight waves with four stages under way: 2 + 0.52 a
 //               stage (128 by 14336x4096 13.7 us, 14.9 as the others are).
 //   both        256x256 for whole rounds of the chip, 2 for a second launch of 128x128 for
@@ -86,9 +87,10 @@ double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b);
 //   parts of K  a join of 4, and the sums written and read at 5 TB/s: 128 by 4096x14336
 //               43 us in one part, 20 in 8.
 double tiles_time(int variant, double tiles, double stages) {
-    if (variant == fl::kMx4Tile256) return ceil_div(tiles, 256) * (8 + 1.75 * stages);
+    if (variant == fl::kMx4Tile256) return ceil_div(tiles, 256) * (7.5 + 1.62 * stages);
     if (variant == fl::kMx4Tile128Alone) return 2 + 0.52 * stages;
-    return (tiles <= 460 ? 1 : tiles / 512 + 0.1) * (4 + 1.24 * stages);
+    const double rounds = (double)(int64_t)(tiles / 512), rest = tiles / 512 - rounds;
+    return (rounds == 0 ? 1 : rest == 0 ? rounds : rounds + (rest < 0.21 ? 0.54 : rest + 0.33)) * (4.3 + 1.24 * stages);
 }
 
 // The 128x128 tile of so many.
@@ -115,7 +117,9 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
                 p.shape = {mt, nt, 8};
             }
         }
-    if (p.shape.mt == 1 && p.shape.nt == 1 && N <= 256 * 16) p.shape.waves = 16;  // a block to a CU
+    // a block to a CU: 1 by 4096x4096 4.2 us, 4.4 with eight waves; 69x235x15993 9.1, 9.5; but
+    // two or three of them, 211x608x239, 6.6 and 4.4
+    if (p.shape.mt == 1 && p.shape.nt == 1 && ceil_div(M, 16) * ceil_div(N, 16) <= 256) p.shape.waves = 16;
     for (int size : {fl::kMx4Tile256, fl::kMx4Tile128}) {
         const fl::Mx4TileShape &t = fl::kMx4TileShapes[size];
         const double tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
