@@ -14,8 +14,9 @@
  * synchronisation, no allocation, arguments validated before any HIP call),
  * with these additions:
  *   Precision  statistics and sums in fp32, one rounding to dtype at the
- *              store; the squares are those of x - mean, so a mean far from
- *              zero costs no digits beyond those of x - mean itself.
+ *              store; the squares are those of x - mean, and a mean far from
+ *              zero (above 16 deviations) is taken to its last place, so it costs no
+ *              digits beyond those of x - mean itself.
  *   Values     a row that holds an infinity or a NaN gives NaN throughout
  *              that row and touches no other; so does a row of equal values
  *              with eps 0 (0 * infinity).  Sums and squares past fp32's range are

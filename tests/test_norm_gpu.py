@@ -5,7 +5,7 @@ import torch
 import activation_epilogue_amd as fl
 from activation_epilogue_amd import norm
 from gpu_util import say
-from norm_util import DT, backward64, forward64, inside
+from norm_util import DT, U, backward64, chain, forward64, inside
 
 pytestmark = pytest.mark.gpu
 
@@ -122,6 +122,39 @@ def test_rows_of_equal_values():
     assert torch.equal(fl.layer_norm(x, None, b), b.expand(3, 777))
     y, mean, rstd = fl.layer_norm(x, eps=0.0, stats=True)
     assert torch.isnan(y).all() and torch.isinf(rstd).all() and (mean == 2.5).all()
+
+
+@pytest.mark.parametrize("value", [0.1, 33.3, 1000.1, 12345.67, -98765.4])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("H", [31, 100, 777, 2048, 4096, 4099, 8192, 16383, 16384, 16385, 32767, 40001])
+def test_rows_of_any_equal_value(H, dtype, value):
+    """The mean of equal values is that value, to the bit, and nothing is left of them: the bias."""
+    dt = DT[dtype]
+    if dtype == "f16" and abs(value) > 65504:
+        value = -65504.0
+    x, b = torch.full((3, H), value, device="cuda", dtype=dt), torch.randn(H, device="cuda").to(dt)
+    say("equal values", H, dtype, value)
+    y, mean, rstd = fl.layer_norm(x, None, b, stats=True)
+    assert torch.equal(mean, x[:, 0].float()) and torch.equal(y, b.expand(3, H))
+    # sqrt and the quotient: a rounding each, and one of eps
+    assert bool(((rstd.double() * 1e-5 ** 0.5 - 1).abs() <= 3 * U).all())
+    y, _, rstd = fl.layer_norm(x, eps=0.0, stats=True)
+    assert torch.isnan(y).all() and torch.isinf(rstd).all()
+
+
+@pytest.mark.parametrize("H", [64, 1000, 4096, 12000, 40001])
+@pytest.mark.parametrize("offset", [300.0, -4000.0, 1e6])
+def test_the_mean_is_good_to_its_last_bits(H, offset):
+    """Of rows far from zero: one rounding, and what the sum of the deviations from a
+    first mean (off by far less than they are) is off by: chain(H) roundings, one of each
+    deviation, two of its quotient."""
+    x, _, _, _, _ = rows(40, H, torch.float32, H, offset)
+    say("mean", H, offset)
+    _, mean, _ = fl.layer_norm(x.cuda(), stats=True)
+    want = x.double().mean(1)
+    spread = (x.double() - want[:, None]).abs().mean(1)
+    off = (mean.cpu().double() - want).abs()
+    assert bool((off <= U * want.abs() + (chain(H) + 4) * U * spread).all())
 
 
 @pytest.mark.parametrize("M,H", [(0, 100), (3, 0), (0, 0)])
