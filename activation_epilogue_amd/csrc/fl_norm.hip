@@ -240,8 +240,11 @@ fl_status fl_layer_norm_bwd(const void *dY, const void *X, const void *weight, c
         launch_bwd_dt<FL_F16>(a, b, sums, c, st);
     else
         launch_bwd_dt<FL_BF16>(a, b, sums, c, st);
-    if (join)
-        hipLaunchKernelGGL(fl::column_join_kernel, dim3((unsigned)((H + 31) / 32), 2), dim3(1024), 0, st, a, b.blocks);
+    if (join) {
+        const int64_t cols = (H + 31) / 32, across = cols < kGridMax ? cols : kGridMax;
+        hipLaunchKernelGGL(fl::column_join_kernel, dim3((unsigned)across, 2, (unsigned)((cols + across - 1) / across)),
+                           dim3(1024), 0, st, a, b.blocks);
+    }
     return check_launch("fl_layer_norm_bwd");
 }
 

@@ -601,13 +601,14 @@ __global__ void __launch_bounds__(256) layer_norm_bwd_columns_kernel(NormArgs a,
 
 // The sum of `rows` rows of partial sums (rows, 2, H): 32 columns to a block, 32
 // runs of rows side by side, whose loads go out eight at a time.  blockIdx.y: 0
-// the weight's, 1 the bias's.
+// the weight's, 1 the bias's.  The columns' blocks lie in the first and the last dimension of
+// the launch (one has less than 2^32 threads: 2^27 columns).
 __global__ void __launch_bounds__(1024) column_join_kernel(NormArgs a, int rows) {
     __shared__ float sums[32][32];
     float *out = blockIdx.y ? a.dbias : a.dweight;
     if (!out) return;
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 32 + x;
+    const int64_t i = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * 32 + x;
     float s = 0.0f;
     if (i < a.H) {
 #pragma unroll 8

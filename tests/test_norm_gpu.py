@@ -306,6 +306,24 @@ def test_offsets_past_32_bits():
     assert torch.isfinite(db).all()
 
 
+@pytest.mark.parametrize("H", [2 ** 25 + 40, 2 ** 27 + 40])
+def test_sums_of_very_long_rows(H):
+    """More columns than one dimension of the join's launch takes; sums of small whole numbers, exact."""
+    M = 4
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, dy = (torch.randint(-4, 5, (M, H), generator=g, device="cuda", dtype=torch.int8).bfloat16() for _ in range(2))
+    zero, one = torch.zeros(M, device="cuda"), torch.ones(M, device="cuda")
+    say("sums of rows of", H)
+    (dw, wbuf), (db, bbuf) = guarded(H, dtype=torch.float32), guarded(H, dtype=torch.float32)
+    fl.layer_norm_bwd(dy, x, zero, one, dweight=dw, dbias=db)
+    want = torch.zeros(H, device="cuda")
+    for r in range(M):
+        want += dy[r].float() * x[r].float()
+    assert torch.equal(dw, want) and torch.equal(db, dy.float().sum(0))
+    untouched(wbuf, H)
+    untouched(bbuf, H)
+
+
 def test_refusals():
     x = torch.zeros(4, 8, device="cuda")
     one = torch.zeros(4, device="cuda")
