@@ -96,10 +96,11 @@ BwdShape bwd_shape(int64_t M, int64_t H, int dtype) {
     return b;
 }
 
-size_t bwd_bytes(int64_t M, int64_t H, int dtype) {
+// sums: whether the weight's or the bias's gradient is asked for.
+size_t bwd_bytes(int64_t M, int64_t H, int dtype, bool sums) {
     if (M == 0 || H == 0) return 0;
     const BwdShape b = bwd_shape(M, H, dtype);
-    const size_t part = b.blocks > 1 ? (size_t)b.blocks * 2 * H * 4 : 0;
+    const size_t part = sums && b.blocks > 1 ? (size_t)b.blocks * 2 * H * 4 : 0;
     return b.team ? part : part + (size_t)M * 8;
 }
 
@@ -183,7 +184,7 @@ fl_status fl_layer_norm_bwd_workspace_bytes(int64_t M, int64_t H, fl_dtype dtype
     fl_status s = check_norm(M, H, dtype);
     if (s != FL_OK) return s;
     if (!bytes) return fail(FL_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = bwd_bytes(M, H, dtype);
+    *bytes = bwd_bytes(M, H, dtype, true);
     return FL_OK;
 }
 
@@ -193,7 +194,8 @@ fl_status fl_layer_norm_bwd(const void *dY, const void *X, const void *weight, c
     clear_error();
     fl_status s = check_norm(M, H, dtype);
     if (s != FL_OK) return s;
-    const size_t need = bwd_bytes(M, H, dtype);
+    const bool sums = dweight || dbias;
+    const size_t need = bwd_bytes(M, H, dtype, sums);
     if (need && (!workspace || workspace_bytes < need))
         return fail(FL_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
     const size_t es = elem_size(dtype), rows = (size_t)M * H * es, stats = H ? (size_t)M * 4 : 0;
@@ -229,11 +231,10 @@ fl_status fl_layer_norm_bwd(const void *dY, const void *X, const void *weight, c
     a.dy = dY;
     a.residual = R;
     a.M = M;
-    const bool sums = dweight || dbias;
     const BwdShape b = bwd_shape(M, H, dtype);
     const bool join = sums && b.blocks > 1;
     a.part = join ? static_cast<float *>(workspace) : nullptr;
-    float *c = b.team ? nullptr : static_cast<float *>(workspace) + (b.blocks > 1 ? (size_t)b.blocks * 2 * H : 0);
+    float *c = b.team ? nullptr : static_cast<float *>(workspace) + (join ? (size_t)b.blocks * 2 * H : 0);
     if (dtype == FL_F32)
         launch_bwd_dt<FL_F32>(a, b, sums, c, st);
     else if (dtype == FL_F16)

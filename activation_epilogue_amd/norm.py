@@ -66,7 +66,8 @@ def layer_norm(X, weight=None, bias=None, eps=1e-5, out=None, stats=False, mean=
 
 @functools.lru_cache(maxsize=1024)
 def layer_norm_bwd_workspace_bytes(M, H, dtype):
-    """Bytes of workspace fl_layer_norm_bwd needs."""
+    """Bytes of workspace fl_layer_norm_bwd needs for the weight's or the bias's gradient (for neither: 8 M of
+    rows above 16384, else none)."""
     n = ctypes.c_size_t()
     _ok(_lib().fl_layer_norm_bwd_workspace_bytes(M, H, _code(dtype) if not isinstance(dtype, int) else dtype,
                                                  ctypes.byref(n)))
@@ -81,17 +82,20 @@ def layer_norm_bwd(dout, X, mean, rstd, weight=None, R=None, dX=None, dweight=Tr
     norm.  dweight/dbias: True allocates the result, a tensor is overwritten,
     None/False skips it.  dX may be dout, X or R.  workspace: a device tensor of
     layer_norm_bwd_workspace_bytes(M, H, dtype) bytes (allocated where it is
-    needed and not given)."""
+    needed and not given; with neither gradient 8 M bytes for H above 16384, else none)."""
     M, H = _matrix(dout, "dout")
     dt = dout.dtype
     code = _code(dt)
-    need = layer_norm_bwd_workspace_bytes(M, H, code)
     with _On(dout, stream) as st:
         dX = torch.empty_like(dout) if dX is None else _out(dX, "dX", (M, H), dt, dout)
         sums = []
         for name, t in (("dweight", dweight), ("dbias", dbias)):
             sums.append(None if t is None or t is False else
                         _out(None if t is True else t, name, (H,), torch.float32, dout))
+        if sums[0] is None and sums[1] is None:
+            need = 8 * M if H > 16384 else 0
+        else:
+            need = layer_norm_bwd_workspace_bytes(M, H, code)
         if need and workspace is None:
             workspace = dout.new_empty(need, dtype=torch.uint8)
         _ok(_lib().fl_layer_norm_bwd(

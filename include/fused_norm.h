@@ -54,7 +54,8 @@ fl_status fl_layer_norm(const void *X, const void *weight, const void *bias, voi
  *           gradient that passes the norm by, where x also goes on as it is).
  *   dX      (M,H) in dtype; may equal dY, X or R.
  *   dweight, dbias  (H,) fp32, each or NULL; overwritten, zeros where M == 0.
- *   workspace  fl_layer_norm_bwd_workspace_bytes(M, H, dtype) bytes, 16-byte
+ *   workspace  fl_layer_norm_bwd_workspace_bytes(M, H, dtype) bytes (with neither
+ *           dweight nor dbias 8 M where H is above 16384, else none), 16-byte
  *           aligned (may be NULL when that is 0); written and read by this
  *           call's launches only, so calls (and captured graphs) that may run at the
  *           same time need one each.

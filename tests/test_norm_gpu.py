@@ -257,6 +257,31 @@ def test_workspace():
         fl.layer_norm_bwd(dy, x, mean, rstd, w, workspace=buf[:need - 1])
 
 
+@pytest.mark.parametrize("H", [200, 4096, 16384, 16385, 40001])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_workspace_without_sums(H, dtype):
+    """dX alone: what its rows need and no more, at the end of a page of the caller's."""
+    M, dt = 700 if H < 20000 else 33, DT[dtype]
+    x, w, _, dy, _ = (t.cuda() for t in rows(M, H, dt, 9))
+    _, mean, rstd = fl.layer_norm(x, w, stats=True)
+    want = fl.layer_norm_bwd(dy, x, mean, rstd, w)[0]
+    need = 8 * M if H > 16384 else 0
+    say("dX alone", M, H, dtype)
+    buf = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    dx = torch.empty_like(x)
+    call = lambda nbytes: norm._lib().fl_layer_norm_bwd(  # noqa: E731
+        dy.data_ptr(), x.data_ptr(), w.data_ptr(), mean.data_ptr(), rstd.data_ptr(), None, dx.data_ptr(), None, None, M, H,
+        {"f32": 0, "bf16": 2}[dtype], buf.data_ptr() if nbytes else None, nbytes, torch.cuda.current_stream().cuda_stream)
+    assert call(need) == 0
+    assert torch.equal(dx, want) and (buf[need:] == 255).all()
+    if need:
+        assert call(need - 1) == 1
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    fl.layer_norm_bwd(dy, x, mean, rstd, w, dX=dx, dweight=False, dbias=False)
+    assert torch.cuda.max_memory_allocated() - before <= need + 512  # the allocator's step
+
+
 def test_captured_and_replayed():
     """A block's norm forward and backward in a graph, with new inputs and eager
     work between the replays."""
