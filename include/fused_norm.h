@@ -19,8 +19,11 @@
  *              digits beyond those of x - mean itself.
  *   Values     a row that holds an infinity or a NaN gives NaN throughout
  *              that row and touches no other; so does a row of equal values
- *              with eps 0 (0 * infinity).  Sums and squares past fp32's range are
- *              infinities (rows of fp32 or bf16 values above 2^63 or so).
+ *              with eps 0 (0 * infinity).  The squares are summed in fp32: from
+ *              deviations of 2^64 / sqrt(H) on (rows of fp32 or bf16; 2^58 for H =
+ *              4096) their sum is infinite and rstd 0, so that y is the bias and dx R or
+ *              0; deviations below 2^-75 have no squares, and with eps 0 rstd is infinite.
+ *              A row whose sum passes 2^128 is NaN throughout.
  *   Alignment  pointers aligned to their elements (workspace: 16 bytes); any H.
  *   Errors     fl_status as in fused_linear.h; the message of the last failed
  *              call of this header is read with fl_norm_last_error().

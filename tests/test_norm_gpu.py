@@ -157,6 +157,35 @@ def test_the_mean_is_good_to_its_last_bits(H, offset):
     assert bool((off <= U * want.abs() + (chain(H) + 4) * U * spread).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [64, 1024, 4096, 16384, 65536])
+def test_ends_of_the_squares(H, dtype):
+    """Deviations of 2^64 / sqrt(H): their squares' sum is infinite, the row its bias, its gradient the path around
+    it.  Half of them, and the smallest that have squares: as any."""
+    dt = DT[dtype]
+    signs = torch.ones(H)
+    signs[1::2] = -1.0
+    most = 2.0 ** 64 / H ** 0.5
+    x = torch.stack([signs * most, signs * most / 2, signs * 2.0 ** -60, signs * 2.0 ** -76, signs * 2.0 ** 127]).to(dt).cuda()
+    g = torch.Generator().manual_seed(H)
+    b, dy, R = (torch.randn(*s, generator=g).to(dt).cuda() for s in ((H,), x.shape, x.shape))
+    say("ends of the squares", H, dtype)
+    y, mean, rstd = fl.layer_norm(x, None, b, eps=0.0, stats=True)
+    assert (mean == 0).all() and rstd.tolist() == [0.0, 2 / most, 2.0 ** 60, float("inf"), 0.0]
+    hat = signs.cuda()
+    assert torch.equal(y[0], b) and torch.equal(y[4], b)
+    assert torch.equal(y[1], (hat + b.float()).to(dt)) and torch.equal(y[2], y[1])
+    assert torch.isinf(y[3]).all()
+    dx, _, _ = fl.layer_norm_bwd(dy, x, mean, rstd, R=R)
+    assert torch.equal(dx[0], R[0]) and torch.equal(dx[4], R[4])
+    only = fl.layer_norm_bwd(dy, x, mean, rstd, dweight=False, dbias=False)[0]
+    assert (only[0] == 0).all() and torch.isfinite(only[1:3]).all()
+    far = torch.full((2, H), torch.finfo(dt).max, dtype=dt, device="cuda")
+    far[1] = 1.0
+    y = fl.layer_norm(far, None, b)
+    assert torch.isnan(y[0]).all() and torch.equal(y[1], b)
+
+
 @pytest.mark.parametrize("M,H", [(0, 100), (3, 0), (0, 0)])
 def test_nothing(M, H):
     x = torch.zeros(M, H, device="cuda", dtype=torch.bfloat16)
