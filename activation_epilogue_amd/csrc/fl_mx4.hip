@@ -56,11 +56,11 @@ fl_status check_matrix(int64_t rows, int64_t K, int dtype) {
 }
 
 // How a linear layer runs: the streaming kernel for few rows, else tiles of a
-// size, K in parts where there are few of them.
+// size, K in parts where there are few of them; the epilogue alone for no K.
 struct LinearPlan {
     bool stream, quantize;  // quantize: A's values first, into the workspace
     fl::Mx4StreamShape shape;
-    int variant, parts, part_stages;
+    int variant, parts, part_stages;  // parts 0: the epilogue alone
     int64_t first_columns;  // of 256x256 tiles, the rest of 128x128 by another launch; 0: all of one size
     size_t codes, scales, sums;  // bytes of the workspace, in this order
 };
@@ -103,7 +103,12 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
     p.part_stages = (int)stages;
     p.stream = true;
     p.shape = {1, 1, 8};
-    if (!M || !N || !K) return p;
+    if (!M || !N) return p;
+    if (!K) {
+        p.stream = false;
+        p.parts = 0;
+        return p;
+    }
     double least = 1e30;
     for (int mt = 1; mt <= 4 && M <= 512; mt *= 2)
         for (int nt = 1; nt <= 4; nt *= 2) {
@@ -193,6 +198,7 @@ void launch_linear(const LinearPlan &p, fl::Mx4LinearArgs l, uint8_t *ws, hipStr
     a.part = reinterpret_cast<float *>(ws + p.codes + p.scales);
     a.parts = p.parts;
     a.part_stages = p.part_stages;
+    if (p.parts == 0) return fl::launch_mx4_join<DT>(a, st);
     const auto launch = [&](int variant, int64_t from, int64_t to) {
         const fl::Mx4TileShape &t = fl::kMx4TileShapes[variant];
         a.n_from = from;

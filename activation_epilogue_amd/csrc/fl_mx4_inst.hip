@@ -53,6 +53,13 @@ void launch_mx4_stream<FL_INST_DTYPE>(const Mx4StreamShape &shape, const Mx4Line
 }
 
 template <>
+void launch_mx4_join<FL_INST_DTYPE>(const Mx4TileArgs &a, hipStream_t st) {
+    const int64_t blocks = ((a.l.N + 3) / 4 * a.l.M + 255) / 256, across = blocks < 1 << 20 ? blocks : 1 << 20;
+    hipLaunchKernelGGL((mx4_join_kernel<FL_INST_DTYPE>), dim3((unsigned)across, (unsigned)((blocks + across - 1) / across)),
+                       dim3(256), 0, st, a);
+}
+
+template <>
 void launch_mx4_tile<FL_INST_DTYPE>(int variant, const Mx4TileArgs &a, hipStream_t st) {
     constexpr int DT = FL_INST_DTYPE;
     if (variant == kMx4Tile256)
@@ -61,10 +68,7 @@ void launch_mx4_tile<FL_INST_DTYPE>(int variant, const Mx4TileArgs &a, hipStream
         launch_tile<DT, 4, 4, 2, 2, 2, 2>(a, st);
     else
         launch_tile<DT, 2, 4, 4, 2, 1, 4>(a, st);
-    if (a.parts > 1) {
-        const int64_t quads = (a.l.N + 3) / 4 * a.l.M;
-        hipLaunchKernelGGL((mx4_join_kernel<DT>), dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, st, a);
-    }
+    if (a.parts > 1) launch_mx4_join<DT>(a, st);
 }
 
 }  // namespace fl

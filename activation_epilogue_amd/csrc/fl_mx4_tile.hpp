@@ -77,7 +77,7 @@ __device__ __forceinline__ int pick_less(int a, int b, int x, int y) {
 struct Mx4TileArgs {
     Mx4LinearArgs l;
     float *part;      // parts > 1: sums (parts, M, N)
-    int parts;        // K is cut into this many runs of stages
+    int parts;        // K is cut into this many runs of stages (K = 0: none)
     int part_stages;  // stages of a run
     int64_t n_from;   // the first tile's column, of tiles_m x tiles_n
     int tiles_m, tiles_n;
@@ -513,9 +513,11 @@ __global__ void __launch_bounds__(64 * WM * WN, PER_CU) mx4_tile_kernel(Mx4TileA
 
 // The sums of the parts in their order, then the epilogue: four columns to a thread, the
 // loads of eight parts under way at once (64 by 4096x14336 bf16 16.0 -> 15.2 us with its tiles).
+// No parts: the layer of no K.  The blocks lie in two dimensions (one has less than 2^32 threads).
 template <int DT>
 __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4TileArgs a) {
-    const int64_t across = (a.l.N + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t across = (a.l.N + 3) / 4;
+    const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
     if (i >= across * a.l.M) return;
     const int64_t m = i / across, n = (i - m * across) * 4;
     const int64_t left = a.l.N - n, step = a.l.M * a.l.N;
@@ -546,5 +548,7 @@ template <int DT>
 void launch_mx4_stream(const Mx4StreamShape &shape, const Mx4LinearArgs &a, hipStream_t st);
 template <int DT>
 void launch_mx4_tile(int variant, const Mx4TileArgs &a, hipStream_t st);
+template <int DT>
+void launch_mx4_join(const Mx4TileArgs &a, hipStream_t st);
 
 }  // namespace fl

@@ -362,6 +362,41 @@ def test_nothing(M, N, K):
     assert fl.quantize_mx4(torch.zeros(K, M, device="cuda"), transposed=True).scales.shape == (M, blocks)
 
 
+@pytest.mark.parametrize("act", ["none", "relu", "gelu_tanh", "glu"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N", [(1, 1), (3, 5), (37, 70), (300, 515)])
+def test_no_depth(M, N, dtype, act):
+    """K = 0: the epilogue of nothing but zeros."""
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(M)
+    bias, Y, R = (torch.randn(*s, generator=g).to(dt) for s in ((N,), (M, N), (M, N)))
+    e = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    B = fl.Mx4(e(N, 0), e(N, 0), 0)
+    y = Y if act == "glu" else None
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    say("no depth", M, N, dtype, act)
+    for A in (torch.zeros(M, 0, dtype=dt, device="cuda"), fl.Mx4(e(M, 0), e(M, 0), 0)):
+        for b, r in ((bias, R), (None, R), (bias, None), (None, None)):
+            out, buf = guarded(M, N, dt)
+            fl.fused_linear_mx4(A, B, dev(b), dev(y), act=act, out=out, R=dev(r), dtype=dt)
+            want, bound = linear64(torch.zeros(M, 0).double(), torch.zeros(N, 0).double(), b, y, r, act)
+            assert worst(out.cpu(), want, bound, dt) <= 1.0
+            assert torch.isnan(buf[:33]).all() and torch.isnan(buf[33 + M * N:]).all()
+
+
+def test_a_long_output_of_no_depth():
+    """More outputs than one dimension of a launch has threads for, 16x16 of them to 512."""
+    M, N = 70_001, 33_000
+    e = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    bias = torch.randn(N, device="cuda").bfloat16()
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    R = torch.ones(M, N, dtype=torch.bfloat16, device="cuda")
+    say("a long output of no depth")
+    fl.fused_linear_mx4(fl.Mx4(e(M, 0), e(M, 0), 0), fl.Mx4(e(N, 0), e(N, 0), 0), bias, act="relu", R=R, out=out)
+    want = (bias.float() + 1).clamp(min=0).bfloat16()
+    assert bool((out == want).all())
+
+
 def test_weights_from_a_layer_and_back():
     """The weight of a fused_linear layer, held in 4 bits: what fused_linear
     gives with the values read back, to the sums' rounding."""
