@@ -16,6 +16,13 @@ int64_t blocks_of(int64_t K) { return (K + 31) / 32; }
 // 4096: 27.5, 26.1).  A launch has 65535 blocks in its second dimension.
 bool split_columns(const fl::Mx4Args &a) { return a.rows * a.blocks <= 3 << 17 && a.blocks <= 2 * 65535; }
 
+// Blocks of 1024 units of eight values, in two dimensions (mx4_first_unit).
+dim3 grid_of_units(const fl::Mx4Args &a) {
+    const int64_t per_block = 256 * fl::kMx4Units, all = (a.rows * a.blocks * 4 + per_block - 1) / per_block;
+    const int64_t across = all < 1 << 20 ? all : 1 << 20;
+    return dim3((unsigned)across, (unsigned)((all + across - 1) / across));
+}
+
 template <int DT>
 void launch_quantize(const fl::Mx4Args &a, bool transposed, hipStream_t st) {
     if (transposed) {
@@ -28,9 +35,7 @@ void launch_quantize(const fl::Mx4Args &a, bool transposed, hipStream_t st) {
             hipLaunchKernelGGL((fl::quantize_mx4_transposed_kernel<DT, 1>), dim3(across, (unsigned)((a.blocks + 7) / 8)),
                                dim3(256), 0, st, a);
     } else {
-        const int64_t units = a.rows * a.blocks * 4, per_block = 256 * fl::kMx4Units;
-        hipLaunchKernelGGL((fl::quantize_mx4_kernel<DT>), dim3((unsigned)((units + per_block - 1) / per_block)),
-                           dim3(256), 0, st, a);
+        hipLaunchKernelGGL((fl::quantize_mx4_kernel<DT>), grid_of_units(a), dim3(256), 0, st, a);
     }
 }
 
@@ -274,8 +279,7 @@ fl_status fl_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, void *X
     a.rows = rows;
     a.K = (int)K;
     a.blocks = (int)blocks;
-    const int64_t units = rows * (int64_t)blocks * 4, per_block = 256 * fl::kMx4Units;
-    const dim3 grid((unsigned)((units + per_block - 1) / per_block));
+    const dim3 grid = grid_of_units(a);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (dtype == FL_F32)
         hipLaunchKernelGGL((fl::dequantize_mx4_kernel<FL_F32>), grid, dim3(256), 0, st, a);

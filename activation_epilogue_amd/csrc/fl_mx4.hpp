@@ -116,12 +116,18 @@ struct Mx4Args {
 
 constexpr int kMx4Units = 4;  // units of eight values to a thread
 
+// The first unit of a block of 256 threads.  The blocks lie in two dimensions of the launch, as
+// one has less than 2^32 threads; those behind the last unit find no row.
+__device__ __forceinline__ int64_t mx4_first_unit() {
+    return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (256 * kMx4Units);
+}
+
 // Rows along K: eight values to a lane, a block to four neighbouring lanes.  Bound
 // by memory (2 + 17/32 bytes a 16-bit value): 8192x4096 bf16 14.4 us, 5.9 TB/s.
 template <int DT>
 __global__ void __launch_bounds__(256) quantize_mx4_kernel(Mx4Args a) {
     const uint32_t per_row = (uint32_t)a.blocks * 4;
-    const int64_t first = (int64_t)blockIdx.x * (256 * kMx4Units), row0 = first / per_row;
+    const int64_t first = mx4_first_unit(), row0 = first / per_row;
     const uint32_t col0 = (uint32_t)(first - row0 * per_row);
     RowValues<DT, 8> v[kMx4Units];
     int64_t row[kMx4Units];
@@ -221,7 +227,7 @@ __global__ void __launch_bounds__(256) dequantize_mx4_kernel(Mx4Args a) {
     using raw = typename io::raw;
     using wide = typename RowValues<DT, 8>::wide;
     const uint32_t per_row = (uint32_t)a.blocks * 4;
-    const int64_t first = (int64_t)blockIdx.x * (256 * kMx4Units), row0 = first / per_row;
+    const int64_t first = mx4_first_unit(), row0 = first / per_row;
     const uint32_t col0 = (uint32_t)(first - row0 * per_row);
     uint32_t c[kMx4Units], s[kMx4Units], col[kMx4Units];
     int64_t row[kMx4Units];

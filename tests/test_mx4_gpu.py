@@ -493,6 +493,23 @@ def test_offsets_past_32_bits():
     assert torch.equal(q.codes[-1000:], one.codes) and torch.equal(q.scales[-1000:], one.scales)
 
 
+def test_many_blocks_of_units():
+    """More of them than a launch's first dimension takes: rows around its end and the last
+    as they are alone."""
+    rows, K = 2 ** 27 + 5003, 40
+    say("units past the first dimension")
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda").normal_()
+    q = fl.quantize_mx4(x)
+    y = fl.dequantize_mx4(q, torch.bfloat16)
+    for part in (slice(0, 1000), slice(2 ** 27 - 1000, 2 ** 27 + 1000), slice(rows - 1001, rows)):
+        codes, scales = quantize64(x[part].cpu())
+        assert torch.equal(q.codes[part].cpu(), codes) and torch.equal(q.scales[part].cpu(), scales)
+        assert torch.equal(y[part].cpu(), values64(codes, scales, K).bfloat16())
+    # every row was written: a value is off by at most half of the largest step, 1, of the scale,
+    # and by 2 where it saturates: less than half of the block's largest
+    assert bool(((y - x).abs().amax(1) <= x.abs().amax(1) / 2).all())
+
+
 def test_a_long_output():
     M, N, K = 70_001, 33_000, 64
     a, b = bytes_of(M, K, 1), bytes_of(N, K, 2)
