@@ -60,6 +60,8 @@ fl_status check_matrix(int64_t rows, int64_t K, int dtype) {
     return FL_OK;
 }
 
+constexpr int64_t kLinearK = 1 << 22;
+
 // How a linear layer runs: the streaming kernel for few rows, else tiles of a
 // size, K in parts where there are few of them; the epilogue alone for no K.
 struct LinearPlan {
@@ -224,9 +226,9 @@ void launch_linear(const LinearPlan &p, fl::Mx4LinearArgs l, uint8_t *ws, hipStr
 fl_status check_linear(int64_t M, int64_t N, int64_t K, int dtype) {
     fl_status s = check_matrix(M, K, dtype);
     if (s != FL_OK || (s = check_matrix(N, K, dtype)) != FL_OK) return s;
-    const size_t es = elem_size(dtype);
-    if ((size_t)blocks_of(K) * 16 * 256 >= kTwoGiB || (size_t)K * es * 256 >= kTwoGiB || (size_t)N * es * 256 >= kTwoGiB)
-        return fail(FL_ERR_UNSUPPORTED, "K or N too large (256 rows must span < 2 GiB)");
+    // 32-bit offsets: into 256 rows of codes (512 MiB at that K) and of the output; values are read by 64-bit ones
+    if (K >= kLinearK || (size_t)N * elem_size(dtype) * 256 >= kTwoGiB)
+        return fail(FL_ERR_UNSUPPORTED, "K or N too large (K must be below 2^22, 256 rows of out span < 2 GiB)");
     if (((N + 15) / 16) * ((M + 15) / 16) > kMaxDim)
         return fail(FL_ERR_UNSUPPORTED, "more than 2^31-1 tiles of 16x16 outputs");
     return FL_OK;

@@ -21,7 +21,8 @@
  * synchronisation, no allocation, arguments validated before any HIP call),
  * with these additions:
  *   Alignment  codes: 16 bytes; scales: any; other pointers: their elements
- *              (workspace: 16 bytes).  Any sizes.
+ *              (workspace: 16 bytes).
+ *   Sizes      any up to 2^31 - 1; K up to 2^24 - 256 (the linear layer: below 2^22).
  *   Errors     fl_status as in fused_linear.h; the message of the last failed
  *              call of this header is read with fl_mx4_last_error().
  *   Order      every result is the same to the bit from run to run.
@@ -71,8 +72,8 @@ fl_status fl_dequantize_mx4(const uint8_t *codes, const uint8_t *scales, void *X
  *            aligned (may be NULL when that is 0); written and read by this
  *            call's launches only, so calls (and captured graphs) that may run at the
  *            same time need one each.
- * K == 0 gives act(bias + R); M == 0 or N == 0 writes nothing.  256 rows of
- * codes, of A as values and of out must each span less than 2 GiB.
+ * K == 0 gives act(bias + R); M == 0 or N == 0 writes nothing.  K must be below
+ * 2^22, and 256 rows of out span less than 2 GiB.
  */
 fl_status fl_fused_linear_mx4(const void *A, const uint8_t *A_scales, const uint8_t *B, const uint8_t *B_scales,
                               const void *bias, const void *Y, const void *R, void *out, int64_t M, int64_t N,

@@ -109,6 +109,16 @@ def test_workspace(lib):
         assert linear(lib, **big, ws=P[7]) == INVALID and "overlaps" in said(lib)
 
 
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+@pytest.mark.parametrize("values", [0, 1])
+def test_the_longest_rows(lib, dt, values):
+    """The same of every type, codes or values."""
+    n = ctypes.c_size_t()
+    assert lib.fl_mx4_workspace_bytes(8, 32, 2 ** 22 - 1, values, dt, ctypes.byref(n)) == OK
+    assert lib.fl_mx4_workspace_bytes(8, 32, 2 ** 22, values, dt, ctypes.byref(n)) == UNSUPPORTED and "2^22" in said(lib)
+    assert linear(lib, K=2 ** 22, dt=dt, **({} if values == 0 else dict(As=None))) == UNSUPPORTED
+
+
 def test_the_definition():
     """Ties to the even code, saturation, the scale's exponent, the ends."""
     x = torch.zeros(4, 32)

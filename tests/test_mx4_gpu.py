@@ -322,6 +322,24 @@ def test_long_rows(M, N, K):
         assert worst(out.cpu(), want, bound, torch.float32) <= 1.0
 
 
+@pytest.mark.parametrize("M,N,K", [(2, 3, 2 ** 21 + 33), (70, 40, 2 ** 21 + 33), (1, 5, 2 ** 22 - 1)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_longest_rows(M, N, K, dtype):
+    """Up to the longest that are taken, whatever the type: from codes and from values of it."""
+    dt = DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(K)
+    a, b = (torch.randn(n, K, generator=g, device="cuda").to(dt) for n in (M, N))
+    say("longest rows", M, N, K, dtype)
+    A, B = fl.quantize_mx4(a), fl.quantize_mx4(b)
+    va, vb = (values64(q.codes.cpu(), q.scales.cpu(), K) for q in (A, B))
+    want, bound = linear64(va, vb, None, None, None, "none")
+    for src in (A, a):
+        out = fl.fused_linear_mx4(src, B, act="none", dtype=dt)
+        assert worst(out.cpu(), want, bound, dt) <= 1.0
+    with pytest.raises(fl.FusedLinearError, match="2\\^22"):
+        fl.mx4_workspace_bytes(M, N, 2 ** 22, True, dt)
+
+
 @pytest.mark.parametrize("M,N,K", [(4, 40, 96), (64, 200, 520), (300, 280, 257), (1100, 1300, 257)])
 @pytest.mark.parametrize("values", [False, True])
 def test_nan_stays_in_its_row_and_column(M, N, K, values):
