@@ -35,6 +35,7 @@ Layer norm (C ABI in ``include/fused_norm.h``, binding in ``norm.py``):
 Microscaled 4-bit floating point (C ABI in ``include/fused_mx4.h``, binding in ``mx4.py``):
   Mx4, quantize_mx4, dequantize_mx4       # blocks of 32 values with a scale of their own
   fused_linear_mx4                        # the fused linear layer over operands held so
+  mx4_plan                                # how it runs at given sizes
 """
 from __future__ import annotations
 
@@ -436,7 +437,7 @@ _MODULES = {
     "moe": ("Plan", "moe_route", "moe_route_bwd", "moe_plan", "moe_plan_workspace_bytes", "moe_gather", "moe_combine",
             "moe_combine_bwd", "grouped_linear", "grouped_linear_bwd", "grouped_weight_grad",
             "grouped_workspace_bytes", "grouped_grad_workspace_bytes"),
-    "mx4": ("Mx4", "quantize_mx4", "dequantize_mx4", "fused_linear_mx4", "mx4_workspace_bytes"),
+    "mx4": ("Mx4", "Mx4Plan", "quantize_mx4", "dequantize_mx4", "fused_linear_mx4", "mx4_plan", "mx4_workspace_bytes"),
     "norm": ("layer_norm", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes"),
 }
 

@@ -179,6 +179,12 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, bool values) {
     return p;
 }
 
+// The variant of the second launch, for the columns behind the first's.
+int second_tile(const LinearPlan &p, int64_t M, int64_t N) {
+    const fl::Mx4TileShape &t = fl::kMx4TileShapes[fl::kMx4Tile128];
+    return small_tile(ceil_div(M, t.bm) * ceil_div(N - p.first_columns, t.bn));
+}
+
 size_t linear_bytes(const LinearPlan &p) { return p.codes + p.scales + p.sums; }
 
 template <int DT>
@@ -215,9 +221,7 @@ void launch_linear(const LinearPlan &p, fl::Mx4LinearArgs l, uint8_t *ws, hipStr
     };
     if (p.first_columns) {
         launch(p.variant, 0, p.first_columns);
-        const fl::Mx4TileShape &t = fl::kMx4TileShapes[fl::kMx4Tile128];
-        const double rest = ceil_div(l.M, t.bm) * ceil_div(l.N - p.first_columns, t.bn);
-        launch(small_tile(rest), p.first_columns, l.N);
+        launch(second_tile(p, l.M, l.N), p.first_columns, l.N);
     } else {
         launch(p.variant, 0, l.N);
     }
@@ -299,6 +303,38 @@ fl_status fl_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t values
     if (values != 0 && values != 1) return fail(FL_ERR_INVALID_ARG, "values must be 0 or 1");
     if (!bytes) return fail(FL_ERR_INVALID_ARG, "bytes is NULL");
     *bytes = linear_bytes(plan_linear(M, N, K, values));
+    return FL_OK;
+}
+
+fl_status fl_mx4_linear_plan(int64_t M, int64_t N, int64_t K, int32_t values, fl_dtype dtype, fl_mx4_plan *plan) {
+    clear_error();
+    fl_status s = check_linear(M, N, K, dtype);
+    if (s != FL_OK) return s;
+    if (values != 0 && values != 1) return fail(FL_ERR_INVALID_ARG, "values must be 0 or 1");
+    if (!plan) return fail(FL_ERR_INVALID_ARG, "plan is NULL");
+    *plan = fl_mx4_plan{};
+    plan->parts = 1;
+    if (!M || !N || !K) return FL_OK;
+    const LinearPlan p = plan_linear(M, N, K, values);
+    plan->quantize = p.quantize ? 1 : values ? 2 : 0;
+    plan->kernel = p.stream ? 1 : 2;
+    if (p.stream) {
+        plan->rows = 16 * p.shape.mt;
+        plan->columns = 16 * p.shape.nt;
+        plan->waves = p.shape.waves;
+        return FL_OK;
+    }
+    const fl::Mx4TileShape &t = fl::kMx4TileShapes[p.variant];
+    plan->rows = t.bm;
+    plan->columns = t.bn;
+    plan->waves = t.waves;
+    plan->parts = p.parts;
+    if ((plan->first_columns = p.first_columns)) {
+        const fl::Mx4TileShape &u = fl::kMx4TileShapes[second_tile(p, M, N)];
+        plan->second_rows = u.bm;
+        plan->second_columns = u.bn;
+        plan->second_waves = u.waves;
+    }
     return FL_OK;
 }
 

@@ -538,9 +538,9 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(Mx4TileArgs a) {
 // The kernels of one type (fl_mx4_inst.hip); Alone: on a CU each.
 enum { kMx4Tile256, kMx4Tile128, kMx4Tile128Alone, kMx4Tiles };
 struct Mx4TileShape {
-    int bm, bn;
+    int bm, bn, waves;
 };
-constexpr Mx4TileShape kMx4TileShapes[kMx4Tiles] = {{256, 256}, {128, 128}, {128, 128}};
+constexpr Mx4TileShape kMx4TileShapes[kMx4Tiles] = {{256, 256, 8}, {128, 128, 4}, {128, 128, 8}};
 struct Mx4StreamShape {
     int mt, nt, waves;  // 16 mt rows by 16 nt columns to a block of this many waves
 };

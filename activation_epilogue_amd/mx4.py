@@ -8,6 +8,7 @@ library; outputs are allocated with torch where they are not given.
   quantize_mx4(X, transposed=False, out=None)   -> Mx4 of X's rows (of its columns)
   dequantize_mx4(q, dtype, out=None)            -> the values (rows,K)
   fused_linear_mx4(A, B, bias=None, Y=None, act="relu", ...) -> act(A @ B + bias [+ R]), A a matrix or an Mx4
+  mx4_plan(M, N, K, values, dtype)              -> Mx4Plan, the kernels that such a call takes
 """
 from __future__ import annotations
 
@@ -21,7 +22,7 @@ from . import ACTS, FusedLinearError, load_library
 from .moe import _bytes, _code, _matrix, _On, _out, _ptr
 
 MX4_EXPORTS = ("fl_quantize_mx4", "fl_dequantize_mx4", "fl_fused_linear_mx4", "fl_mx4_workspace_bytes",
-               "fl_mx4_last_error")
+               "fl_mx4_linear_plan", "fl_mx4_last_error")
 
 
 class Mx4(NamedTuple):
@@ -29,6 +30,14 @@ class Mx4(NamedTuple):
     codes: torch.Tensor   # (rows, 16 * ceil(K/32)) uint8, two codes to a byte
     scales: torch.Tensor  # (rows, ceil(K/32)) uint8, E8M0
     K: int                # values of a row
+
+
+class Mx4Plan(ctypes.Structure):
+    """Mirror of fl_mx4_plan."""
+    _fields_ = [("kernel", ctypes.c_int32), ("rows", ctypes.c_int32), ("columns", ctypes.c_int32),
+                ("waves", ctypes.c_int32), ("quantize", ctypes.c_int32), ("parts", ctypes.c_int32),
+                ("first_columns", ctypes.c_int64), ("second_rows", ctypes.c_int32),
+                ("second_columns", ctypes.c_int32), ("second_waves", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _mx4 = None
@@ -44,6 +53,7 @@ def _lib():
         lib.fl_dequantize_mx4.argtypes = [vp, vp, vp, i64, i64, c_int, vp]
         lib.fl_fused_linear_mx4.argtypes = [vp] * 8 + [i64] * 3 + [c_int, c_int, vp, sz, vp]
         lib.fl_mx4_workspace_bytes.argtypes = [i64, i64, i64, i32, c_int, ctypes.POINTER(sz)]
+        lib.fl_mx4_linear_plan.argtypes = [i64, i64, i64, i32, c_int, ctypes.POINTER(Mx4Plan)]
         for name in MX4_EXPORTS[:-1]:
             getattr(lib, name).restype = c_int
         lib.fl_mx4_last_error.restype = ctypes.c_char_p
@@ -104,6 +114,13 @@ def mx4_workspace_bytes(M, N, K, values, dtype):
     _ok(_lib().fl_mx4_workspace_bytes(M, N, K, 1 if values else 0,
                                       _code(dtype) if not isinstance(dtype, int) else dtype, ctypes.byref(n)))
     return n.value
+
+
+def mx4_plan(M, N, K, values, dtype):
+    """How fused_linear_mx4 runs at these sizes (fl_mx4_linear_plan), as an Mx4Plan; values: A is a matrix."""
+    plan = Mx4Plan()
+    _ok(_lib().fl_mx4_linear_plan(M, N, K, 1 if values else 0, _code(dtype), ctypes.byref(plan)))
+    return plan
 
 
 def fused_linear_mx4(A, B, bias=None, Y=None, act="relu", out=None, *, R=None, dtype=None, stream=None,

@@ -81,6 +81,19 @@ fl_status fl_fused_linear_mx4(const void *A, const uint8_t *A_scales, const uint
                               void *stream);
 fl_status fl_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t values, fl_dtype dtype, size_t *bytes);
 
+/* How such a call runs: what a workgroup of its launch has of the output. */
+typedef struct fl_mx4_plan {
+    int32_t kernel;        /* 0 the epilogue alone (no K, or nothing to write), 1 B streamed by few rows of A, 2 tiles */
+    int32_t rows, columns; /* of the output */
+    int32_t waves;
+    int32_t quantize;      /* A's values: 0 there are none, 1 by a launch before, 2 by every workgroup */
+    int32_t parts;         /* runs of K, whose sums another launch joins; 1: one */
+    int64_t first_columns; /* of the output, in tiles as above; behind them by a second launch; 0: all */
+    int32_t second_rows, second_columns, second_waves; /* of that launch, or 0 */
+    int32_t reserved;
+} fl_mx4_plan;
+fl_status fl_mx4_linear_plan(int64_t M, int64_t N, int64_t K, int32_t values, fl_dtype dtype, fl_mx4_plan *plan);
+
 const char *fl_mx4_last_error(void); /* thread-local; "" when none */
 
 #ifdef __cplusplus

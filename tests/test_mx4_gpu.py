@@ -211,8 +211,7 @@ def test_larger(M, N, K):
     exact_case(M, N, K, 6, values=True, dtype=torch.float32)
 
 
-# Sizes at which each of the streaming kernel's shapes is the one that runs, both
-# tiles, K in parts, and tiles of both sizes.
+# Sizes of several kernels (mx4_kernels.py has sizes of each, held to the choice).
 @pytest.mark.parametrize("M,N,K", [(3, 1000, 2000), (9, 5001, 700), (257, 259, 100), (20, 2051, 130), (200, 1030, 65),
                                    (200, 2051, 300), (33, 4099, 8200), (300, 2051, 4100), (600, 259, 4100),
                                    (257, 4099, 8200), (3000, 5000, 65), (130, 16391, 8200), (513, 515, 16400),
