@@ -81,7 +81,8 @@ double ceil_div(double a, double b) { return (double)(int64_t)((a + b - 1) / b);
 //   streaming   3, and a round of the chip 0.3 for each 16x16 of outputs and 0.25 for each
 //               16 rows of A or B and 1024 values of K.  One token by 14336x4096: 7.7 us,
 //               tiles 33; 64 by 4096x14336: 17.1, tiles 14.9; 128 by 14336x4096: 26, tiles
-//               13.7.
+//               13.7.  64 by 64 outputs to a block, seldom the least: 33 by 13961x3612 10.6,
+//               13.2 without (tiles), 39 by 13972x4985 15.6 and 16.1.
 //   256x256     3.4, and a round 7.5 + 1.62 a stage of 256 values of K.
 //   128x128     3.4, and two to a CU: a round 4.3 + 1.24 a stage, a part of one a third
 //               more than its share and not under 0.54.  4608x4096x4096 55 us, 63 with

@@ -35,7 +35,7 @@
 // fetch the next one's first stages before that were slower (306 us against 287), as were
 // touching lines ahead for the L2 (337 against 275), a ring of four halves of a stage,
 // whose 64-byte rows are two lines' work for one (297 against 275), four waves of 128x128
-// with half of the B reads (322 against 262: nothing runs while the one wave of a SIMD
+// with half of the A reads (322 against 262: nothing runs while the one wave of a SIMD
 // waits), and first workgroups that start staggered (no difference).
 #pragma once
 

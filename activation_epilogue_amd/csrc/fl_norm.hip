@@ -33,7 +33,8 @@ void launch_fwd(const fl::NormArgs &a, hipStream_t st) {
 // (16384 rows), of 2048 21.9 and 22.9, of 4096 40.6 and 38.6; 256 columns 11.6 with 16
 // lanes, 19.5 with 64 (65536 rows).  Few rows do not fill the chip, and a lane's share
 // is what they wait for: 1725 bf16 take 3.0 us with 256 lanes and 3.6 with 64 (8 to 256
-// rows), 4.3 and 4.2 (1024).
+// rows), 4.3 and 4.2 (1024).  1024 lanes for longer ones do not help: 8 rows of 8192 bf16 3.6
+// us both ways, 512 4.7 and 5.2; of 16384 4.5 with 256, 4.3 with 1024, 6.1 and 6.5.
 template <int DT>
 void launch_fwd_dt(const fl::NormArgs &a, hipStream_t st) {
     const int64_t p = pieces_of(a.H, DT);
@@ -66,7 +67,10 @@ void launch_fwd_dt(const fl::NormArgs &a, hipStream_t st) {
 // leaves a row of partial sums (8 H bytes), so no more of them than are resident
 // at once (16384x4096 bf16: 512 or, of 1024 lanes, 256), half as many where a team has
 // fewer than four rows (1024x4096 bf16 13 us, 18 with 512 blocks; 4096x1000 9.6, 11.1),
-// and a block for a team's row each where they are fewer still (512x4096 11.4 us).  The
+// and a block for a team's row each where they are fewer still (512x4096 11.4 us).  Teams of
+// 1024 lanes, of which a CU holds one: 256x8192 13.4 us, 15.4 with all 256 blocks, 256x16384
+// 19.2 and 23.3, 512 24.0 and 24.3; from there on all would be better, 768 27.3 and 25.9,
+// 1023 31.3 and 28.5.  The
 // rows of two blocks are left to one, and those of three, which needs no join: 4x4096
 // bf16 7.3 us, 8.2 with it, 6x4096 8.7 and 8.2, and 3.4 of the host's time.
 // The sums of a lane take two registers an element, so teams are larger than the
