@@ -157,6 +157,26 @@ def test_the_mean_is_good_to_its_last_bits(H, offset):
     assert bool((off <= U * want.abs() + (chain(H) + 4) * U * spread).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("H", [31, 64, 100, 128, 200, 1000, 4096, 12000, 16384, 40001])
+def test_rows_of_many_kinds_side_by_side(H, dtype):
+    """Rows with a mean far from zero beside others, in one wave where rows are short: each as it is alone."""
+    x, w, b, _, _ = rows(37, H, DT[dtype], H)
+    kind = torch.arange(37) * 7 % 5
+    x[kind == 1] += 4000.0
+    x[kind == 2] = x[kind == 2][:, :1]
+    x[3], x[11, 0] = 0.0, float("nan")
+    x, w, b = x.cuda(), w.cuda(), b.cuda()
+    say("kinds of rows", H, dtype)
+    got = fl.layer_norm(x, w, b, stats=True)
+    for r in range(37):
+        alone = fl.layer_norm(x[r:r + 1], w, b, stats=True)
+        assert all(torch.equal(torch.nan_to_num(p[r:r + 1]), torch.nan_to_num(q)) for p, q in zip(got, alone))
+    y64, _, _, (e_y, _, _) = forward64(x.cpu(), w.cpu(), b.cpu(), 1e-5)
+    keep = torch.arange(37) != 11
+    inside(got[0][keep.cuda()], y64[keep], e_y[keep])
+    assert torch.isnan(got[0][11]).all()
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("H", [64, 1024, 4096, 16384, 65536])
 def test_ends_of_the_squares(H, dtype):
