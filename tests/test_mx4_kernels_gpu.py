@@ -4,6 +4,8 @@ activations, scales that are NaN, outputs in place, streams and graphs.
 The products are exact in fp32 where codes and scales are those of exact_operands(); else
 bounds are mx4_util's.  The 64-bit products are torch's, on the GPU.
 """
+import threading
+
 import pytest
 import torch
 
@@ -204,6 +206,44 @@ def test_two_streams_at_once(one, two):
         for (_, _, want, _), got in zip(jobs, outs):
             assert all(torch.equal(t, want) for t in got)
 
+
+def test_two_threads_two_streams():
+    """Layers of two kernels, and quantising, from two host threads at the same time."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    jobs = []
+    for name in ("parts_of_128x128_alone", "tile_128x128"):
+        k = KERNELS[name]
+        x = torch.randn(k.M, depth(k.deep), generator=g, device="cuda").half()
+        W = operand(k.N, depth(k.deep), g)
+        q = fl.quantize_mx4(x.t().contiguous(), transposed=True)
+        jobs.append((x, W, (fl.fused_linear_mx4(x, W, act="relu"), q.codes, q.scales)))
+    torch.cuda.synchronize()
+    got, errors, start = [[], []], [], threading.Barrier(2)
+
+    def work(i):
+        try:
+            x, W, _ = jobs[i]
+            stream = torch.cuda.Stream()
+            start.wait()
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    q = fl.quantize_mx4(x.t().contiguous(), transposed=True)
+                    got[i].append((fl.fused_linear_mx4(x, W, act="relu"), q.codes, q.scales))
+                    with pytest.raises(fl.FusedLinearError, match="needs Y"):  # a message of the thread's own
+                        fl.fused_linear_mx4(x, W, act="glu")
+            stream.synchronize()
+        except Exception as e:  # reported by the main thread
+            errors.append(repr(e))
+    say("two threads, two streams")
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for (_, _, want), each in zip(jobs, got):
+        assert len(each) == 20 and all(torch.equal(p, q) for one in each for p, q in zip(one, want))
 
 def test_scales_of_the_whole_range():
     """Products whose scales lie outside of fp32's range each, and inside together."""

@@ -1,4 +1,6 @@
 """Layer norm and its gradients on the GPU against the 64-bit plain forms."""
+import threading
+
 import pytest
 import torch
 
@@ -292,6 +294,41 @@ def test_the_same_bits_again_and_on_another_stream():
     assert all(torch.equal(p, q) for p, q in zip((y, mean, rstd, *first), again))
 
 
+def test_two_threads_two_streams():
+    """Forward and backward passes of two shapes, from two host threads at the same time."""
+    jobs = []
+    for M, H, dt in ((3001, 1537, torch.bfloat16), (515, 12000, torch.float32)):
+        x, w, b, dy, res = (t.cuda() for t in rows(M, H, dt, M))
+        f = fl.layer_norm(x, w, b, stats=True)
+        jobs.append(((x, w, b, dy, res), (*f, *fl.layer_norm_bwd(dy, x, f[1], f[2], w, R=res))))
+    torch.cuda.synchronize()
+    got, errors, start = [[], []], [], threading.Barrier(2)
+
+    def work(i):
+        try:
+            x, w, b, dy, res = jobs[i][0]
+            stream = torch.cuda.Stream()
+            start.wait()
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    f = fl.layer_norm(x, w, b, stats=True)
+                    got[i].append((*f, *fl.layer_norm_bwd(dy, x, f[1], f[2], w, R=res)))
+                    with pytest.raises(fl.FusedLinearError, match="eps"):  # a message of the thread's own
+                        fl.layer_norm(x, eps=-1.0)
+            stream.synchronize()
+        except Exception as e:  # reported by the main thread
+            errors.append(repr(e))
+    say("two threads, two streams")
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for (_, want), each in zip(jobs, got):
+        assert len(each) == 20 and all(torch.equal(p, q) for g in each for p, q in zip(g, want))
+
 def test_workspace():
     M, H = 3001, 1537
     x, w, b, dy, _ = (t.cuda() for t in rows(M, H, torch.float16, 9))
@@ -379,6 +416,24 @@ def test_offsets_past_32_bits():
     assert torch.equal(dx[-1000:], fl.layer_norm_bwd(dy[-1000:], x[-1000:], mean[-1000:], rstd[-1000:])[0])
     assert torch.isfinite(db).all()
 
+
+@pytest.mark.parametrize("dtype,H", [("f32", 2052), ("bf16", 4104)])
+def test_more_rows_than_blocks(dtype, H):
+    """Blocks that go from row to row, a row to each at once: rows on both sides of the launch's 2^20 blocks."""
+    M, dt = 2 ** 20 + 3001, DT[dtype]
+    x = torch.empty(M, H, dtype=dt, device="cuda").normal_()
+    x[::3] += 100.0
+    say("more rows than blocks", M, H, dtype)
+    y, mean, rstd = fl.layer_norm(x, stats=True)
+    dx, _, _ = fl.layer_norm_bwd(y, x, mean, rstd, dweight=False, dbias=False)
+    for part in (slice(0, 300), slice(2 ** 20 - 300, 2 ** 20 + 300), slice(M - 300, M)):
+        xs, ys = x[part].cpu(), y[part].cpu()
+        y64, mean64, rstd64, (e_y, e_mean, e_rstd) = forward64(xs, None, None, 1e-5)
+        inside(ys, y64, e_y)
+        inside(mean[part], mean64, e_mean)
+        inside(rstd[part], rstd64, e_rstd)
+        dx64, _, _, (e_dx, _, _) = backward64(ys, xs, mean[part].cpu(), rstd[part].cpu(), None, None)
+        inside(dx[part], dx64, e_dx)
 
 @pytest.mark.parametrize("H", [2 ** 25 + 40, 2 ** 27 + 40])
 def test_sums_of_very_long_rows(H):
